@@ -88,6 +88,89 @@ size_t bwd_workspace(const ssa_params_t& p) {
 
 }  // namespace
 
+namespace {
+
+int validate_scale(float sm_scale) {
+    if (!(sm_scale > 0.f) || !std::isfinite(sm_scale))
+        return fail(SSA_ERR_INVALID_ARG, "sm_scale must be positive and finite");
+    return SSA_OK;
+}
+
+// The checks that window attention and the paged cache share.
+int validate_heads(int B, int Hq, int Hkv, int D, int window, int sinks, int dtype, float sm_scale) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0)
+        return fail(SSA_ERR_INVALID_ARG, "B, Hq, Hkv, D must be positive (got %d, %d, %d, %d)", B, Hq, Hkv, D);
+    if (Hq % Hkv != 0)
+        return fail(SSA_ERR_INVALID_ARG, "Hq (%d) must be a multiple of Hkv (%d)", Hq, Hkv);
+    if (dtype != SSA_F32 && dtype != SSA_BF16) return fail(SSA_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+    if (D != 64 && D != 128) return fail(SSA_ERR_UNSUPPORTED, "head dim D must be 64 or 128 (got %d)", D);
+    if (window < 0) return fail(SSA_ERR_INVALID_ARG, "window must not be negative (got %d)", window);
+    if (sinks < 0) return fail(SSA_ERR_INVALID_ARG, "sinks must not be negative (got %d)", sinks);
+    if (sinks > 128) return fail(SSA_ERR_UNSUPPORTED, "at most 128 sinks (got %d)", sinks);
+    if (B > 65535 || Hq > 65535)
+        return fail(SSA_ERR_UNSUPPORTED, "at most 65535 sequences and heads (got %d, %d)", B, Hq);
+    return validate_scale(sm_scale);
+}
+
+int validate(const ssa_window_params_t* p) {
+    if (!p) return fail(SSA_ERR_INVALID_ARG, "params is NULL");
+    const int st = validate_heads(p->B, p->Hq, p->Hkv, p->D, p->window, p->sinks, p->dtype, p->sm_scale);
+    if (st != SSA_OK) return st;
+    if (p->T <= 0) return fail(SSA_ERR_INVALID_ARG, "T must be positive (got %d)", p->T);
+    if (p->T > (1 << 30)) return fail(SSA_ERR_UNSUPPORTED, "T must be at most 2^30 (got %d)", p->T);
+    if (p->flags & ~(unsigned)SSA_FLAG_FORCE_SIMT)
+        return fail(SSA_ERR_INVALID_ARG, "unknown flag bits 0x%x", p->flags);
+    return SSA_OK;
+}
+
+int validate(const ssa_cache_params_t* p) {
+    if (!p) return fail(SSA_ERR_INVALID_ARG, "params is NULL");
+    const int st = validate_heads(p->B, p->Hq, p->Hkv, p->D, p->window, p->sinks, p->dtype, p->sm_scale);
+    if (st != SSA_OK) return st;
+    if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128)
+        return fail(SSA_ERR_UNSUPPORTED, "page must be 16, 32, 64 or 128 tokens (got %d)", p->page);
+    if (p->n_pages <= 0 || p->max_pages <= 0)
+        return fail(SSA_ERR_INVALID_ARG, "n_pages and max_pages must be positive (got %d, %d)", p->n_pages,
+                    p->max_pages);
+    if ((long long)p->max_pages * p->page > 0x7fffffffll - 256)
+        return fail(SSA_ERR_UNSUPPORTED, "max_pages * page must be below 2^31 - 256");
+    if (p->page_stride < (long long)p->Hkv * p->page * p->D)
+        return fail(SSA_ERR_INVALID_ARG, "page_stride (%lld) is smaller than a page (%lld)", p->page_stride,
+                    (long long)p->Hkv * p->page * p->D);
+    if (p->page_stride % (p->dtype == SSA_BF16 ? 8 : 4) != 0)
+        return fail(SSA_ERR_INVALID_ARG, "page_stride must be a multiple of 16 bytes");
+    if (p->flags) return fail(SSA_ERR_INVALID_ARG, "unknown flag bits 0x%x", p->flags);
+    return SSA_OK;
+}
+
+// Reads a view and checks its pointer and the strides of its axes (an axis of
+// length 0 is one that the call does not have).
+int need_view(const ssa_view_t* v, const char* name, int dtype, int D, int nb, int nh, int nt, View* out) {
+    if (!v) return fail(SSA_ERR_INVALID_ARG, "%s is NULL", name);
+    const int st = need_ptr(v->data, name);
+    if (st != SSA_OK) return st;
+    const long long unit = dtype == SSA_BF16 ? 8 : 4;
+    const struct { int n; long long s; const char* axis; } ax[3] = {
+        {nb, v->stride_b, "batch"}, {nh, v->stride_h, "head"}, {nt, v->stride_t, "token"}};
+    for (const auto& x : ax) {
+        if (x.n <= 1) continue;
+        if (x.s < D)
+            return fail(SSA_ERR_INVALID_ARG, "%s: the %s stride (%lld) is smaller than a row of %d elements", name,
+                        x.axis, x.s, D);
+        if (x.s % unit != 0)
+            return fail(SSA_ERR_INVALID_ARG, "%s: the %s stride (%lld) is not a multiple of 16 bytes", name, x.axis,
+                        x.s);
+    }
+    // axes of length 1 get a stride that every kernel may multiply and encode
+    out->data = v->data;
+    out->sb = nb > 1 ? v->stride_b : D;
+    out->sh = nh > 1 ? v->stride_h : D;
+    out->st = nt > 1 ? v->stride_t : D;
+    return SSA_OK;
+}
+
+}  // namespace
+
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
 unsigned long long ds_budget_bytes() { return g_ds_budget.load(std::memory_order_relaxed); }
 
@@ -337,6 +420,138 @@ int ssa_attn_bwd(const ssa_params_t* p, const void* q, const void* k, const void
                            dh_sparse, w_s, w_c, dq, dk, dv, ws, s);
 }
 
+size_t ssa_window_workspace_size(const ssa_window_params_t* p) {
+    if (validate(p) != SSA_OK) return (size_t)-1;
+    return window_bwd_simt_workspace(*p);
+}
+
+int ssa_window_fwd(const ssa_window_params_t* p, const ssa_view_t* q, const ssa_view_t* k,
+                   const ssa_view_t* v, const int32_t* lens, const ssa_view_t* h, float* lse, void* stream) {
+    g_last_error[0] = 0;
+    SSA_TRY(validate(p));
+    View vq, vk, vv, vh;
+    SSA_TRY(need_view(q, "q", p->dtype, p->D, p->B, p->Hq, p->T, &vq));
+    SSA_TRY(need_view(k, "k", p->dtype, p->D, p->B, p->Hkv, p->T, &vk));
+    SSA_TRY(need_view(v, "v", p->dtype, p->D, p->B, p->Hkv, p->T, &vv));
+    SSA_TRY(opt_ptr(lens, "lens"));
+    SSA_TRY(need_view(h, "h", p->dtype, p->D, p->B, p->Hq, p->T, &vh));
+    SSA_TRY(need_ptr(lse, "lse"));
+    return launch_window_fwd_simt(*p, vq, vk, vv, lens, vh, lse, static_cast<cudaStream_t>(stream));
+}
+
+int ssa_window_bwd(const ssa_window_params_t* p, const ssa_view_t* q, const ssa_view_t* k,
+                   const ssa_view_t* v, const int32_t* lens, const ssa_view_t* h, const float* lse,
+                   const ssa_view_t* dh, const ssa_view_t* dq, const ssa_view_t* dk,
+                   const ssa_view_t* dv, void* ws, size_t ws_bytes, void* stream) {
+    g_last_error[0] = 0;
+    SSA_TRY(validate(p));
+    View vq, vk, vv, vh, vdh, vdq, vdk, vdv;
+    SSA_TRY(need_view(q, "q", p->dtype, p->D, p->B, p->Hq, p->T, &vq));
+    SSA_TRY(need_view(k, "k", p->dtype, p->D, p->B, p->Hkv, p->T, &vk));
+    SSA_TRY(need_view(v, "v", p->dtype, p->D, p->B, p->Hkv, p->T, &vv));
+    SSA_TRY(opt_ptr(lens, "lens"));
+    SSA_TRY(need_view(h, "h", p->dtype, p->D, p->B, p->Hq, p->T, &vh));
+    SSA_TRY(need_ptr(lse, "lse"));
+    SSA_TRY(need_view(dh, "dh", p->dtype, p->D, p->B, p->Hq, p->T, &vdh));
+    SSA_TRY(need_view(dq, "dq", p->dtype, p->D, p->B, p->Hq, p->T, &vdq));
+    SSA_TRY(need_view(dk, "dk", p->dtype, p->D, p->B, p->Hkv, p->T, &vdk));
+    SSA_TRY(need_view(dv, "dv", p->dtype, p->D, p->B, p->Hkv, p->T, &vdv));
+    SSA_TRY(need_ws(ws, ws_bytes, window_bwd_simt_workspace(*p), "ssa_window_bwd"));
+    return launch_window_bwd_simt(*p, vq, vk, vv, lens, vh, lse, vdh, vdq, vdk, vdv, ws,
+                                  static_cast<cudaStream_t>(stream));
+}
+
+int ssa_cache_append(const ssa_cache_params_t* p, int n_tokens, const ssa_view_t* k, const ssa_view_t* v,
+                     const ssa_view_t* q, void* k_pages, void* v_pages, const int32_t* table,
+                     const int32_t* lens, int32_t* new_lens, const int32_t* q_start, const double* inv_freq,
+                     int rot_dim, int interleaved, int pos_offset, const ssa_view_t* q_out,
+                     const ssa_view_t* k_out, void* stream) {
+    g_last_error[0] = 0;
+    SSA_TRY(validate(p));
+    if (n_tokens < 0) return fail(SSA_ERR_INVALID_ARG, "n_tokens must not be negative (got %d)", n_tokens);
+    if (n_tokens == 0x7fffffff) return fail(SSA_ERR_UNSUPPORTED, "n_tokens must be below 2^31 - 1");
+    if (rot_dim < 0 || rot_dim > p->D || rot_dim % 2 != 0)
+        return fail(SSA_ERR_INVALID_ARG, "rot_dim must be even and in [0, D = %d] (got %d)", p->D, rot_dim);
+    if (pos_offset < 0) return fail(SSA_ERR_INVALID_ARG, "pos_offset must not be negative (got %d)", pos_offset);
+    if (!q_start && n_tokens % p->B != 0)
+        return fail(SSA_ERR_INVALID_ARG, "without q_start n_tokens (%d) must be a multiple of B (%d)", n_tokens, p->B);
+    if ((q == nullptr) != (q_out == nullptr))
+        return fail(SSA_ERR_INVALID_ARG, "q and q_out go together");
+    View vk{}, vv{}, vq{}, vqo{}, vko{};
+    if (n_tokens > 0) {  // an empty tensor has no address
+        SSA_TRY(need_view(k, "k", p->dtype, p->D, 0, p->Hkv, n_tokens, &vk));
+        SSA_TRY(need_view(v, "v", p->dtype, p->D, 0, p->Hkv, n_tokens, &vv));
+    }
+    if (n_tokens > 0 && q) {
+        SSA_TRY(need_view(q, "q", p->dtype, p->D, 0, p->Hq, n_tokens, &vq));
+        SSA_TRY(need_view(q_out, "q_out", p->dtype, p->D, 0, p->Hq, n_tokens, &vqo));
+    }
+    if (n_tokens > 0 && k_out) SSA_TRY(need_view(k_out, "k_out", p->dtype, p->D, 0, p->Hkv, n_tokens, &vko));
+    SSA_TRY(need_ptr(k_pages, "k_pages"));
+    SSA_TRY(need_ptr(v_pages, "v_pages"));
+    SSA_TRY(need_ptr(table, "table"));
+    SSA_TRY(need_ptr(lens, "lens"));
+    SSA_TRY(opt_ptr(new_lens, "new_lens"));
+    SSA_TRY(opt_ptr(q_start, "q_start"));
+    if (rot_dim) SSA_TRY(need_ptr(inv_freq, "inv_freq"));
+    if (new_lens && new_lens != lens && new_lens < lens + p->B && lens < new_lens + p->B)
+        return fail(SSA_ERR_INVALID_ARG, "new_lens overlaps lens (it may be lens itself)");
+    return launch_cache_append(*p, n_tokens, vk, vv, vq, k_pages, v_pages, table, lens, new_lens, q_start,
+                               inv_freq, rot_dim, interleaved, pos_offset, vqo, vko,
+                               static_cast<cudaStream_t>(stream));
+}
+
+static int prefix_shape(const ssa_cache_params_t* p, int prefix_len) {
+    SSA_TRY(validate(p));
+    if (prefix_len < 0) return fail(SSA_ERR_INVALID_ARG, "prefix_len must not be negative (got %d)", prefix_len);
+    if (prefix_len > 0x7fffffff - 256) return fail(SSA_ERR_UNSUPPORTED, "prefix_len must be below 2^31 - 256");
+    return SSA_OK;
+}
+
+size_t ssa_cache_workspace_size(const ssa_cache_params_t* p, int prefix_len) {
+    if (prefix_shape(p, prefix_len) != SSA_OK) return (size_t)-1;
+    return paged_decode_workspace(*p, prefix_len);
+}
+
+int ssa_prefix_decode(const ssa_cache_params_t* p, const ssa_view_t* q, const void* k_pages,
+                      const void* v_pages, const int32_t* prefix_pages, int prefix_len,
+                      const int32_t* table, const int32_t* lens, const ssa_view_t* h, float* lse,
+                      void* ws, size_t ws_bytes, void* stream) {
+    g_last_error[0] = 0;
+    SSA_TRY(prefix_shape(p, prefix_len));
+    if (p->window != 0) return fail(SSA_ERR_UNSUPPORTED, "prefix_decode: window must be 0 (got %d)", p->window);
+    View vq, vh;
+    SSA_TRY(need_view(q, "q", p->dtype, p->D, p->B, p->Hq, 0, &vq));
+    SSA_TRY(need_ptr(k_pages, "k_pages"));
+    SSA_TRY(need_ptr(v_pages, "v_pages"));
+    if (prefix_len > 0) SSA_TRY(need_ptr(prefix_pages, "prefix_pages"));
+    SSA_TRY(need_ptr(table, "table"));
+    SSA_TRY(need_ptr(lens, "lens"));
+    SSA_TRY(need_view(h, "h", p->dtype, p->D, p->B, p->Hq, 0, &vh));
+    SSA_TRY(need_ptr(lse, "lse"));
+    SSA_TRY(need_ws(ws, ws_bytes, paged_decode_workspace(*p, prefix_len), "ssa_prefix_decode"));
+    return launch_paged_decode(*p, vq, k_pages, v_pages, prefix_pages, prefix_len, table, lens, vh, lse, ws,
+                               static_cast<cudaStream_t>(stream));
+}
+
+int ssa_paged_decode(const ssa_cache_params_t* p, const ssa_view_t* q, const void* k_pages,
+                     const void* v_pages, const int32_t* table, const int32_t* lens, const ssa_view_t* h,
+                     float* lse, void* ws, size_t ws_bytes, void* stream) {
+    g_last_error[0] = 0;
+    SSA_TRY(validate(p));
+    View vq, vh;
+    SSA_TRY(need_view(q, "q", p->dtype, p->D, p->B, p->Hq, 0, &vq));
+    SSA_TRY(need_ptr(k_pages, "k_pages"));
+    SSA_TRY(need_ptr(v_pages, "v_pages"));
+    SSA_TRY(need_ptr(table, "table"));
+    SSA_TRY(need_ptr(lens, "lens"));
+    SSA_TRY(need_view(h, "h", p->dtype, p->D, p->B, p->Hq, 0, &vh));
+    SSA_TRY(need_ptr(lse, "lse"));
+    SSA_TRY(need_ws(ws, ws_bytes, paged_decode_workspace(*p, 0), "ssa_paged_decode"));
+    return launch_paged_decode(*p, vq, k_pages, v_pages, nullptr, 0, table, lens, vh, lse, ws,
+                               static_cast<cudaStream_t>(stream));
+}
+
 int ssa_device_status(void* stream) {
     g_last_error[0] = 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -347,6 +562,9 @@ int ssa_device_status(void* stream) {
     if (st == SSA_OK) st = selftest_take_status();
     if (st == SSA_OK) st = decode_take_status();
     if (st == SSA_OK) st = select_take_status();
+    if (st == SSA_OK) st = append_take_status();
+    if (st == SSA_OK) st = paged_take_status();
+    if (st == SSA_OK) st = window_take_status();
     if (st != SSA_OK) return st;
     return check_launch("pending");
 }
@@ -370,7 +588,7 @@ int ssa_kernel_path(const ssa_params_t* p) {
     return use_tc(*p) ? 1 : 0;
 }
 
-int ssa_version(void) { return (1 << 16) | 0; }
+int ssa_version(void) { return (1 << 16) | 1; }
 
 int ssa_bwd_heads_per_group(const ssa_params_t* p) {
     if (validate(p) != SSA_OK || !use_tc(*p)) return -1;

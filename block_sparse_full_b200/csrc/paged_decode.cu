@@ -1,0 +1,805 @@
+// Attention of single query tokens over a paged key/value cache
+// (ssa_paged_decode), and over a prefix that a batch shares followed by each
+// sequence's own pages (ssa_prefix_decode).
+//
+// Each key and value is used by the G = Hq / Hkv query heads of its group
+// only, so the call is bound by reading the cache once.  The work is the list
+// of (sequence, head, row tile of 16 query rows, tile of keys) units, in that
+// order, keys fastest; every CTA takes an equal stretch of the list, whatever
+// the lengths are (they are read on the device, so a captured launch follows
+// them).  Walking its stretch a CTA keeps a running maximum, sum and output
+// (float32) per row and writes them down as a partial result where a
+// (sequence, head, row tile) is split between CTAs; a second kernel joins the
+// partials of each row:  h = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
+// Which CTAs hold a row's partials follows from the lengths alone, so nothing
+// is counted or cleared, and the order of the sums is fixed.
+//
+// Keys and values come in by 16-byte asynchronous copies through a ring of
+// shared-memory stages (3 x 32 KB per CTA and two CTAs per SM keep the
+// bandwidth-delay product in flight); rows that are not seen are zero-filled,
+// so that nothing left behind in a page reaches the products.  bf16: one warp
+// takes 16 keys of a tile, S = Q K^T and O += P V on mma.sync m16n8k16 (a
+// tile of 16 query rows cannot fill a larger tensor tile).  float32: CUDA
+// cores, a warp takes 8 keys.
+#include <cuda_bf16.h>
+
+#include "device_util.cuh"
+#include "ssa_internal.h"
+
+namespace ssa {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kRows = 16;  // query rows of a unit
+constexpr int kStages = 3;
+constexpr float kLn2 = 0.693147180559945309f;
+
+__device__ unsigned int g_paged_status;
+
+template <typename T>
+struct Tile {
+    static constexpr int keys = sizeof(T) == 2 ? 64 : 32;
+};
+
+// One pass over pages: nseq sequences of R query rows per key/value head each
+// (row r of sequence b is batch entry b + r / G, head h*G + r % G).
+struct Pass {
+    const int32_t *table, *lens;  // lens NULL: fixed_len everywhere
+    int nseq, R, RT, width, cap, fixed_len, window, sinks;
+    int C;         // CTAs
+    bool direct;   // rows held by one CTA go to the output, else to its own slot
+    float* part;   // slots [2C + nseq*Hkv*RT] x 16 rows x (D outputs, then m, l)
+};
+
+struct DecodeArgs {
+    const void *k_pages, *v_pages;
+    View q, h;
+    float* lse;
+    int B, Hq, Hkv, G, page_shift, n_pages;
+    long long page_stride;
+    float scale_log2;
+};
+
+// The tiles of keys that a query sees: [0, ns) and [w0t, end), or one stretch.
+struct Seen {
+    int len, w0, ns, w0t, nt;
+};
+__device__ __forceinline__ Seen seen_tiles(const Pass& p, int len, int tk) {
+    Seen s;
+    s.len = len;
+    s.w0 = p.window > 0 && len > p.window ? len - p.window : 0;
+    const int send = min(p.sinks, s.w0);
+    s.ns = (send + tk - 1) / tk;
+    s.w0t = s.w0 / tk;
+    s.w0t = max(s.w0t, s.ns);
+    s.nt = s.ns + (len + tk - 1) / tk - s.w0t;
+    return s;
+}
+__device__ __forceinline__ int tile_key(const Seen& s, int t, int tk) {
+    return (t < s.ns ? t : s.w0t + t - s.ns) * tk;
+}
+__device__ __forceinline__ bool is_seen(const Seen& s, int sinks, int key) {
+    return key < s.len && (key >= s.w0 || key < sinks);
+}
+
+__device__ __forceinline__ int seq_len(const Pass& p, int b) {
+    if (!p.lens) return p.fixed_len;
+    const int n = p.lens[b];
+    if (n < 0 || n > p.cap) {
+        atomicOr(&g_paged_status, 1u);
+        return n < 0 ? 0 : p.cap;
+    }
+    return n;
+}
+
+// Warp-wide: tiles of the sequences before `upto`.
+__device__ __forceinline__ long long tiles_before(const Pass& p, int upto, int tk) {
+    long long n = 0;
+    for (int b0 = 0; b0 < upto; b0 += 32) {
+        const int b = b0 + (int)(threadIdx.x & 31);
+        int x = b < upto ? seen_tiles(p, seq_len(p, b), tk).nt : 0;
+        x = __reduce_add_sync(0xffffffffu, x);
+        n += x;
+    }
+    return n;
+}
+
+// CTAs that take part: each has a unit
+__device__ __forceinline__ int used_ctas(long long total, int C) { return total < C ? (int)total : C; }
+// first unit of CTA c's stretch, and the CTA whose stretch holds unit u
+__device__ __forceinline__ long long stretch(long long total, int C, int c) { return total * c / C; }
+__device__ __forceinline__ int cta_of(long long total, int C, long long u) {
+    return (int)(((u + 1) * C - 1) / total);  // the largest c with total * c / C <= u
+}
+// slot of the partial that CTA c holds of the units [u0, u1)
+__device__ __forceinline__ size_t slot_of(long long total, int C, int c, long long u0) {
+    return 2 * (size_t)c + (stretch(total, C, c) < u0 ? 1 : 0);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+    const int n = valid ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t s_u32(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// A place in the list of units.
+struct Cursor {
+    int b, hr, t;
+    Seen s;
+};
+
+// Rows of a unit and their products, by type.  Every warp holds the 16 (or
+// fewer) rows against its own keys.
+template <typename T, int D, int RG>
+struct Rows;
+
+// bf16: fragments of mma.sync m16n8k16 (RG is 16)
+template <int D, int RG>
+struct Rows<__nv_bfloat16, D, RG> {
+    uint32_t q[D / 16][4];
+    float o[D / 8][4];
+    float m[2], l[2];  // rows lane / 4 and lane / 4 + 8; l is this thread's share
+
+    __device__ __forceinline__ void begin(const DecodeArgs& a, const Pass& p, int b, int h, int r0, float*) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = r0 + (lane >> 2) + 8 * i;
+            const __nv_bfloat16* src = nullptr;
+            if (r < p.R)
+                src = static_cast<const __nv_bfloat16*>(a.q.data) + (size_t)(b + r / a.G) * a.q.sb +
+                      (size_t)(h * a.G + r % a.G) * a.q.sh;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    q[k][i + 2 * x] =
+                        src ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8 * x + 2 * (lane & 3)) : 0u;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    }
+
+    __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int key0, const Seen& s, int sinks,
+                                         float scale_log2, const float*) {
+        constexpr uint32_t pitch = D * 2;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int mi = lane >> 3, mr = lane & 7;
+        float c[2][4] = {};
+        {
+            const int row = warp * 16 + (mi >> 1) * 8 + mr;
+            const uint32_t base = kt + row * pitch;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t f[4];
+                ldsm4(base + (((2 * k + (mi & 1)) ^ (row & 7)) << 4), f);
+                mma16816(c[0], q[k], f[0], f[1]);
+                mma16816(c[1], q[k], f[2], f[3]);
+            }
+        }
+        const int kb = key0 + warp * 16;
+        float mx[2] = {-INFINITY, -INFINITY};
+        const bool whole = kb + 16 <= s.len && (kb >= s.w0 || kb + 16 <= sinks);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = kb + 8 * n + 2 * (lane & 3) + (e & 1);
+                c[n][e] = whole || is_seen(s, sinks, key) ? c[n][e] * scale_log2 : -INFINITY;
+                mx[e >> 1] = fmaxf(mx[e >> 1], c[n][e]);
+            }
+        bool up = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            up = up || mx[i] > m[i];
+        }
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float mn = fmaxf(m[i], mx[i]);
+                const float al = m[i] == mn ? 1.f : ex2f(m[i] - mn);  // m may be -inf
+                m[i] = mn;
+                l[i] *= al;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) o[n][2 * i] *= al, o[n][2 * i + 1] *= al;
+            }
+        }
+        const float mz[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                c[n][e] = ex2f(c[n][e] - mz[e >> 1]);
+                l[e >> 1] += c[n][e];  // the sum takes the weights before they are rounded to bf16
+            }
+        const uint32_t pa[4] = {pack2(c[0][0], c[0][1]), pack2(c[0][2], c[0][3]), pack2(c[1][0], c[1][1]),
+                                pack2(c[1][2], c[1][3])};
+        {
+            const int row = warp * 16 + (mi & 1) * 8 + mr;
+            const uint32_t base = vt + row * pitch;
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+                uint32_t f[4];
+                ldsm4t(base + (((2 * n + (mi >> 1)) ^ (row & 7)) << 4), f);
+                mma16816(o[2 * n], pa, f[0], f[1]);
+                mma16816(o[2 * n + 1], pa, f[2], f[3]);
+            }
+        }
+    }
+
+    // this warp's maxima of its rows -> ml[row]; then its share is added to sum
+    __device__ __forceinline__ void maxima(float* dst) const {
+        const int lane = threadIdx.x & 31;
+        if ((lane & 3) == 0) dst[lane >> 2] = m[0], dst[(lane >> 2) + 8] = m[1];
+    }
+    __device__ __forceinline__ void add(float* sum, float* lsum, const float* top, bool first, int nr) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = (lane >> 2) + 8 * i;
+            float ls = l[i];
+            ls += __shfl_xor_sync(0xffffffffu, ls, 1);
+            ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+            if (r >= nr) continue;
+            const float w = m[i] == -INFINITY ? 0.f : ex2f(m[i] - top[r]);
+            if ((lane & 3) == 0) lsum[r] = (first ? 0.f : lsum[r]) + w * ls;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                float2* p = reinterpret_cast<float2*>(sum + r * D + 8 * n + 2 * (lane & 3));
+                float2 v = first ? make_float2(0.f, 0.f) : *p;
+                v.x += w * o[n][2 * i];
+                v.y += w * o[n][2 * i + 1];
+                *p = v;
+            }
+        }
+    }
+};
+
+// float32: lane = (key of 8, quarter of D) for the scores, 4 columns for the sums
+template <int D, int RG>
+struct Rows<float, D, RG> {
+    float o[RG][4];
+    float m[RG], l[RG];
+    static constexpr int kCol = D / 4;  // lanes that hold the columns (32, or 16 twice)
+
+    __device__ __forceinline__ void begin(const DecodeArgs& a, const Pass& p, int b, int h, int r0, float* qs) {
+        __syncthreads();  // the unit before has done with qs
+        for (int x = threadIdx.x; x < RG * D / 4; x += kThreads) {
+            const int r = r0 + x / (D / 4), c = 4 * (x % (D / 4));
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < p.R)
+                v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q.data) +
+                                                     (size_t)(b + r / a.G) * a.q.sb +
+                                                     (size_t)(h * a.G + r % a.G) * a.q.sh + c);
+            *reinterpret_cast<float4*>(qs + (x / (D / 4)) * D + c) = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+            m[g] = -INFINITY, l[g] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[g][e] = 0.f;
+        }
+    }
+
+    __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int key0, const Seen& s, int sinks,
+                                         float scale_log2, const float* qs) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int row = warp * 8 + (lane & 7);
+        const float* kr = reinterpret_cast<const float*>(__cvta_shared_to_generic(kt)) + row * D;
+        const float* vr = reinterpret_cast<const float*>(__cvta_shared_to_generic(vt));
+        float x[RG];
+#pragma unroll
+        for (int g = 0; g < RG; ++g) x[g] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            const int c = (lane >> 3) + 4 * j;
+            const float4 k4 = *reinterpret_cast<const float4*>(kr + 4 * (c ^ (row & 7)));
+#pragma unroll
+            for (int g = 0; g < RG; ++g) {
+                const float4 q4 = *reinterpret_cast<const float4*>(qs + g * D + 4 * c);
+                x[g] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, x[g]))));
+            }
+        }
+        const bool vis = is_seen(s, sinks, key0 + row);
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+            x[g] += __shfl_xor_sync(0xffffffffu, x[g], 8);
+            x[g] += __shfl_xor_sync(0xffffffffu, x[g], 16);
+            x[g] = vis ? x[g] * scale_log2 : -INFINITY;
+            float mx = x[g];
+#pragma unroll
+            for (int sh = 1; sh < 8; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+            if (mx > m[g]) {  // the same in every lane
+                const float al = ex2f(m[g] - mx);
+                m[g] = mx;
+                l[g] *= al;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[g][e] *= al;
+            }
+            x[g] = ex2f(x[g] - (m[g] == -INFINITY ? 0.f : m[g]));
+            if (lane < 8) l[g] += x[g];
+        }
+        const int cc = lane & (kCol - 1);
+#pragma unroll
+        for (int j = 0; j < 8 * kCol / 32; ++j) {
+            const int key = kCol == 32 ? j : 2 * j + (lane >> 4);
+            const int vrow = warp * 8 + key;
+            const float4 v4 = *reinterpret_cast<const float4*>(vr + vrow * D + 4 * (cc ^ (vrow & 7)));
+#pragma unroll
+            for (int g = 0; g < RG; ++g) {
+                const float w = __shfl_sync(0xffffffffu, x[g], key);
+                o[g][0] = fmaf(w, v4.x, o[g][0]);
+                o[g][1] = fmaf(w, v4.y, o[g][1]);
+                o[g][2] = fmaf(w, v4.z, o[g][2]);
+                o[g][3] = fmaf(w, v4.w, o[g][3]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void maxima(float* dst) const {
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int g = 0; g < RG; ++g) dst[g] = m[g];
+    }
+    __device__ __forceinline__ void add(float* sum, float* lsum, const float* top, bool first, int nr) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+            float ls = l[g];
+#pragma unroll
+            for (int sh = 1; sh < 8; sh <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, sh);
+            if constexpr (kCol == 16)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[g][e] += __shfl_xor_sync(0xffffffffu, o[g][e], 16);
+            if (g >= nr) continue;
+            const float w = m[g] == -INFINITY ? 0.f : ex2f(m[g] - top[g]);
+            if (lane == 0) lsum[g] = (first ? 0.f : lsum[g]) + w * ls;
+            if (lane < kCol) {
+                float4* p = reinterpret_cast<float4*>(sum + g * D + 4 * lane);
+                float4 v = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *p;
+                v.x += w * o[g][0], v.y += w * o[g][1], v.z += w * o[g][2], v.w += w * o[g][3];
+                *p = v;
+            }
+        }
+    }
+};
+
+template <typename T, int D>
+constexpr size_t ring_bytes() {
+    return (size_t)kStages * 2 * Tile<T>::keys * D * sizeof(T);
+}
+template <typename T, int D>
+constexpr size_t decode_smem() {
+    // ring, joined sums [16][D], queries [16][D] (float32 only), maxima [4][16], sums [16], top [16]
+    return ring_bytes<T, D>() + kRows * D * 4 * (sizeof(T) == 4 ? 2 : 1) + (kWarps + 2) * kRows * 4;
+}
+
+template <typename T, int D, int RG>
+__global__ void __launch_bounds__(kThreads, 2)
+decode_kernel(const DecodeArgs a, const Pass p) {
+    constexpr int TK = Tile<T>::keys;
+    constexpr int CH = D * (int)sizeof(T) / 16;       // 16-byte chunks of a row
+    constexpr int RPP = kThreads / CH;                // rows per pass of the CTA
+    constexpr uint32_t TB = TK * D * sizeof(T);       // bytes of a K or V tile
+    extern __shared__ __align__(128) uint8_t smem[];
+    float* sum = reinterpret_cast<float*>(smem + ring_bytes<T, D>());
+    float* qs = sum + kRows * D;
+    float* maxs = sum + kRows * D * (sizeof(T) == 4 ? 2 : 1);  // [warp][row]
+    float* lsum = maxs + kWarps * kRows;
+    float* top = lsum + kRows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int HR = a.Hkv * p.RT;
+
+    const long long total = tiles_before(p, p.nseq, TK) * HR;
+    const int C = used_ctas(total, p.C);
+    if ((int)blockIdx.x >= C) return;
+    const long long ubeg = stretch(total, C, blockIdx.x), uend = stretch(total, C, blockIdx.x + 1);
+
+    // the place of unit ubeg: the sequence by a warp-wide scan
+    Cursor ld;
+    {
+        long long before = 0;
+        int found = -1;
+        for (int b0 = 0; found < 0; b0 += 32) {
+            const int b = b0 + lane;
+            const int n = b < p.nseq ? seen_tiles(p, seq_len(p, b), TK).nt : 0;
+            long long inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const uint32_t in = __ballot_sync(0xffffffffu, (before + inc) * HR > ubeg);
+            if (in) {
+                found = b0 + __ffs(in) - 1;
+                before += __shfl_sync(0xffffffffu, inc - n, __ffs(in) - 1);
+            } else {
+                before += __shfl_sync(0xffffffffu, inc, 31);
+                if (b0 + 32 >= p.nseq) return;  // cannot be: ubeg < total
+            }
+        }
+        ld.b = found;
+        ld.s = seen_tiles(p, seq_len(p, found), TK);
+        const long long r = ubeg - before * HR;
+        ld.hr = (int)(r / ld.s.nt);
+        ld.t = (int)(r % ld.s.nt);
+    }
+    Cursor cu = ld;
+    auto advance = [&](Cursor& c) {
+        if (++c.t < c.s.nt) return;
+        c.t = 0;
+        if (++c.hr < HR) return;
+        c.hr = 0;
+        do {
+            if (++c.b >= p.nseq) return;  // past the last unit
+            c.s = seen_tiles(p, seq_len(p, c.b), TK);
+        } while (c.s.nt == 0);
+    };
+    // The page numbers of a tile: lane g holds that of its g-th 16 keys (a page
+    // holds whole groups of 16), read one unit before the copies need it.
+    auto page_of = [&](const Cursor& c) -> int {
+        int pg = 0;
+        if (lane < TK / 16) {
+            const int k0 = tile_key(c.s, c.t, TK) + 16 * lane;
+            const bool any = k0 < c.s.len && (k0 + 16 > c.s.w0 || k0 < p.sinks);
+            if (any) pg = p.table[(size_t)c.b * p.width + (k0 >> a.page_shift)];
+            if (pg < 0 || pg >= a.n_pages) {
+                atomicOr(&g_paged_status, 2u);
+                pg = 0;
+            }
+        }
+        return pg;
+    };
+    const int crow = threadIdx.x / CH, ccol = threadIdx.x % CH;
+    const uint32_t ring = s_u32(smem);
+    const int pmask = (1 << a.page_shift) - 1;
+    auto copy = [&](const Cursor& c, int stage, int pg) {
+        const int k0 = tile_key(c.s, c.t, TK), hd = c.hr / p.RT;
+        const uint32_t dk = ring + stage * 2 * TB;
+#pragma unroll
+        for (int i = 0; i < TK / RPP; ++i) {
+            const int row = crow + i * RPP, key = k0 + row;
+            const int pid = __shfl_sync(0xffffffffu, pg, row >> 4);
+            const bool ok = is_seen(c.s, p.sinks, key);
+            const size_t off = (size_t)pid * a.page_stride +
+                               ((size_t)hd * (pmask + 1) + (key & pmask)) * D + ccol * (16 / sizeof(T));
+            const uint32_t so = row * (D * (uint32_t)sizeof(T)) + ((ccol ^ (row & 7)) << 4);
+            cp_async16(dk + so, static_cast<const T*>(a.k_pages) + off, ok);
+            cp_async16(dk + TB + so, static_cast<const T*>(a.v_pages) + off, ok);
+        }
+    };
+
+    const long long n = uend - ubeg;
+    int pg = page_of(ld);
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < n) {
+            copy(ld, i, pg);
+            advance(ld);
+            if (i + 1 < n) pg = page_of(ld);
+        }
+        cp_commit();
+    }
+    Rows<T, D, RG> rows;
+    int stage = 0;
+    long long seg0 = ubeg;  // first unit of the current (sequence, head, row tile) here
+    bool fresh = true;
+    for (long long u = ubeg; u < uend; ++u) {
+        if (fresh) {
+            rows.begin(a, p, cu.b, cu.hr / p.RT, (cu.hr % p.RT) * kRows, qs);
+            seg0 = u;
+            fresh = false;
+        }
+        cp_wait<kStages - 2>();
+        __syncthreads();  // the tile is there for all, and the stage before is free
+        {
+            const long long nx = u + kStages - 1;
+            if (nx < uend) {
+                const int st = stage == 0 ? kStages - 1 : stage - 1;
+                copy(ld, st, pg);
+                advance(ld);
+                if (nx + 1 < uend) pg = page_of(ld);
+            }
+            cp_commit();
+        }
+        const uint32_t kt = ring + stage * 2 * TB;
+        rows.tile(kt, kt + TB, tile_key(cu.s, cu.t, TK), cu.s, p.sinks, a.scale_log2, qs);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+
+        const bool last = cu.t + 1 == cu.s.nt;
+        if (last || u + 1 == uend) {
+            // join the warps' shares, in warp order
+            const int r0 = (cu.hr % p.RT) * kRows, nr = min(kRows, p.R - r0);
+            rows.maxima(maxs + warp * kRows);
+            __syncthreads();
+            if (threadIdx.x < kRows) {
+                float t = maxs[threadIdx.x];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) t = fmaxf(t, maxs[w * kRows + threadIdx.x]);
+                top[threadIdx.x] = t;
+            }
+            __syncthreads();
+#pragma unroll 1
+            for (int w = 0; w < kWarps; ++w) {
+                if (w == warp) rows.add(sum, lsum, top, w == 0, nr);
+                __syncthreads();
+            }
+            const bool whole = last && u - seg0 + 1 == cu.s.nt;
+            const int hd = cu.hr / p.RT;
+            if (whole && p.direct) {
+                for (int x = threadIdx.x; x < nr * D / 4; x += kThreads) {
+                    const int r = x / (D / 4), c = 4 * (x % (D / 4));
+                    const float4 v = *reinterpret_cast<const float4*>(sum + r * D + c);
+                    const float inv = 1.f / lsum[r];
+                    T* dst = static_cast<T*>(a.h.data) + (size_t)(cu.b + (r0 + r) / a.G) * a.h.sb +
+                             (size_t)(hd * a.G + (r0 + r) % a.G) * a.h.sh + c;
+                    if constexpr (sizeof(T) == 2) {
+                        *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
+                    } else {
+                        *reinterpret_cast<float4*>(dst) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    }
+                }
+                if ((int)threadIdx.x < nr) {
+                    const int r = r0 + threadIdx.x;
+                    a.lse[(size_t)(cu.b + r / a.G) * a.Hq + hd * a.G + r % a.G] =
+                        (top[threadIdx.x] + log2f(lsum[threadIdx.x])) * kLn2;
+                }
+            } else {
+                const size_t slot = whole ? 2 * (size_t)p.C + (size_t)cu.b * HR + cu.hr
+                                          : 2 * (size_t)blockIdx.x + (seg0 > ubeg ? 1 : 0);
+                float* dst = p.part + slot * kRows * (D + 2);
+                for (int x = threadIdx.x; x < nr * D / 4; x += kThreads)
+                    reinterpret_cast<float4*>(dst)[x] = reinterpret_cast<const float4*>(sum)[x];
+                if ((int)threadIdx.x < nr)
+                    *reinterpret_cast<float2*>(dst + kRows * D + 2 * threadIdx.x) =
+                        make_float2(top[threadIdx.x], lsum[threadIdx.x]);
+            }
+            fresh = true;
+            __syncthreads();  // sum, top and lsum are free again
+        }
+        advance(cu);
+    }
+    cp_wait<0>();
+}
+
+// Where the partials of a row lie: n slots, one from every CTA c0 .. c0 + n - 1,
+// or the row's own slot.
+struct Parts {
+    int c0, n;
+    size_t first, rest;  // slot of the first; the i-th one after it is rest + 2 i
+    __device__ size_t slot(int i) const { return i == 0 ? first : rest + 2 * (size_t)i; }
+};
+__device__ __forceinline__ Parts parts_of(const Pass& p, long long total, long long u0, long long u1, size_t own) {
+    Parts r;
+    const int C = used_ctas(total, p.C);
+    r.c0 = cta_of(total, C, u0);
+    r.n = cta_of(total, C, u1 - 1) - r.c0 + 1;
+    r.first = r.n == 1 ? own : slot_of(total, C, r.c0, u0);
+    r.rest = 2 * (size_t)r.c0;
+    return r;
+}
+
+// Joins the partials of the rows (one warp each) of one sequence and head.
+// pre: the pass over the shared prefix (nseq = 0: none).
+template <typename T, int D>
+__global__ void __launch_bounds__(128)
+join_kernel(const DecodeArgs a, const Pass p, const Pass pre) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int TK = Tile<T>::keys, E = D / 32;  // outputs per lane
+    const int b = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 31;
+    const int HR = a.Hkv * p.RT;
+    const Seen s = seen_tiles(p, seq_len(p, b), TK);
+    const long long before = tiles_before(p, b, TK);
+    const long long total = tiles_before(p, p.nseq, TK) * HR;
+    for (int g = threadIdx.x >> 5; g < a.G; g += blockDim.x >> 5) {
+        Parts own{0, 0, 0, 0}, shared{0, 0, 0, 0};
+        const int rt = g / kRows, r = g % kRows;
+        if (s.nt > 0) {
+            const long long u0 = before * HR + (long long)(h * p.RT + rt) * s.nt;
+            own = parts_of(p, total, u0, u0 + s.nt, 2 * (size_t)p.C + (size_t)b * HR + h * p.RT + rt);
+        }
+        int pr = 0;
+        if (pre.nseq > 0) {
+            const int row = b * a.G + g, hr = h * pre.RT + row / kRows;
+            const Seen ps = seen_tiles(pre, pre.fixed_len, TK);
+            const long long ptotal = (long long)ps.nt * a.Hkv * pre.RT;
+            pr = row % kRows;
+            shared = parts_of(pre, ptotal, (long long)hr * ps.nt, (long long)(hr + 1) * ps.nt, 2 * (size_t)pre.C + hr);
+        } else if (own.n == 1) {
+            continue;  // written by the pass itself
+        }
+        const int np = own.n + shared.n;
+        auto part = [&](int i) -> const float* {
+            return i < own.n ? p.part + own.slot(i) * kRows * (D + 2) : pre.part + shared.slot(i - own.n) * kRows * (D + 2);
+        };
+        float M = -INFINITY;
+        for (int i = lane; i < np; i += 32) M = fmaxf(M, part(i)[kRows * D + 2 * (i < own.n ? r : pr)]);
+        M = warp_max(M);
+        float L = 0.f, acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        for (int i0 = 0; i0 < np; i0 += 32) {
+            float w = 0.f;
+            if (i0 + lane < np) {
+                const int rr = i0 + lane < own.n ? r : pr;
+                const float2 ml = *reinterpret_cast<const float2*>(part(i0 + lane) + kRows * D + 2 * rr);
+                w = ml.x == -INFINITY ? 0.f : ex2f(ml.x - M);
+                L += w * ml.y;
+            }
+            const int m = min(32, np - i0);
+#pragma unroll 8
+            for (int i = 0; i < m; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                const float* src = part(i0 + i) + (i0 + i < own.n ? r : pr) * D + E * lane;
+                float x[E];
+                if constexpr (E == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+                else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, x[e], acc[e]);
+            }
+        }
+        L = warp_sum(L);
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        T* dst = static_cast<T*>(a.h.data) + (size_t)b * a.h.sb + (size_t)(h * a.G + g) * a.h.sh + E * lane;
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<uint32_t*>(dst + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) dst[e] = acc[e] * inv;
+        }
+        if (lane == 0)
+            a.lse[(size_t)b * a.Hq + h * a.G + g] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    }
+}
+
+constexpr int kCtas = 296;  // two CTAs on each of 148 SMs
+
+template <typename T, int D, int RG>
+int launch_pass(const DecodeArgs& a, const Pass& p, cudaStream_t s) {
+    const int st = opt_in_max_smem<decode_kernel<T, D, RG>>("decode_kernel");
+    if (st != SSA_OK) return st;
+    decode_kernel<T, D, RG><<<p.C, kThreads, decode_smem<T, D>(), s>>>(a, p);
+    return check_launch("decode_kernel");
+}
+template <typename T, int D>
+int run_pass(const DecodeArgs& a, const Pass& p, cudaStream_t s) {
+    if constexpr (sizeof(T) == 4)  // few rows: fewer registers and products per key
+        if (p.R <= 4) return launch_pass<T, D, 4>(a, p, s);
+    return launch_pass<T, D, kRows>(a, p, s);
+}
+
+template <typename T, int D>
+int run(const DecodeArgs& a, const Pass& own, const Pass& pre, cudaStream_t s) {
+    int st = SSA_OK;
+    if (pre.nseq) st = run_pass<T, D>(a, pre, s);
+    if (st == SSA_OK) st = run_pass<T, D>(a, own, s);
+    if (st != SSA_OK) return st;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)a.Hkv, (unsigned)a.B);
+    c.blockDim = dim3((unsigned)(32 * (a.G < 4 ? a.G : 4)));
+    c.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&c, join_kernel<T, D>, a, own, pre);
+    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "join_kernel: %s", cudaGetErrorString(e));
+    return check_launch("join_kernel");
+}
+
+int tile_keys(const ssa_cache_params_t& p) { return p.dtype == SSA_BF16 ? 64 : 32; }
+int row_tiles(long long R) { return (int)((R + kRows - 1) / kRows); }
+// CTAs of a pass: no more than the units that its longest sequences could have
+int pass_ctas(long long nseq, long long Hkv, long long RT, long long max_keys, int tk) {
+    const long long u = nseq * Hkv * RT * ((max_keys + tk - 1) / tk + 1);
+    return (int)(u < kCtas ? u : kCtas);
+}
+size_t pass_bytes(int C, long long segments, int D) {
+    return align_up((2 * (size_t)C + (size_t)segments) * kRows * (D + 2) * sizeof(float), 256);
+}
+long long seen_most(const ssa_cache_params_t& p) {
+    const long long cap = (long long)p.max_pages * p.page;
+    const long long w = p.window > 0 ? (long long)p.window + p.sinks + 2 * 64 : cap;
+    return w < cap ? w : cap;
+}
+
+}  // namespace
+
+size_t paged_decode_workspace(const ssa_cache_params_t& p, int prefix_len) {
+    const int G = p.Hq / p.Hkv, RT = row_tiles(G), tk = tile_keys(p);
+    size_t n = pass_bytes(pass_ctas(p.B, p.Hkv, RT, seen_most(p), tk), (long long)p.B * p.Hkv * RT, p.D);
+    if (prefix_len > 0) {
+        const int PT = row_tiles((long long)p.B * G);
+        n += pass_bytes(pass_ctas(1, p.Hkv, PT, prefix_len, tk), (long long)p.Hkv * PT, p.D);
+    }
+    return n;
+}
+
+int launch_paged_decode(const ssa_cache_params_t& p, const View& q, const void* k_pages, const void* v_pages,
+                        const int32_t* prefix_pages, int prefix_len, const int32_t* table,
+                        const int32_t* lens, const View& h, float* lse, void* ws, cudaStream_t s) {
+    const int G = p.Hq / p.Hkv, tk = tile_keys(p);
+    DecodeArgs a{};
+    a.k_pages = k_pages, a.v_pages = v_pages, a.q = q, a.h = h, a.lse = lse;
+    a.B = p.B, a.Hq = p.Hq, a.Hkv = p.Hkv, a.G = G;
+    a.page_shift = __builtin_ctz((unsigned)p.page);
+    a.n_pages = p.n_pages, a.page_stride = p.page_stride;
+    a.scale_log2 = p.sm_scale * 1.4426950408889634f;
+    Pass own{}, pre{};
+    own.table = table, own.lens = lens, own.nseq = p.B, own.R = G, own.RT = row_tiles(G);
+    own.width = p.max_pages, own.cap = p.max_pages * p.page, own.window = p.window;
+    own.sinks = p.window > 0 ? p.sinks : 0;
+    own.C = pass_ctas(p.B, p.Hkv, own.RT, seen_most(p), tk);
+    own.direct = prefix_len == 0;
+    own.part = static_cast<float*>(ws);
+    if (prefix_len > 0) {
+        pre.table = prefix_pages, pre.nseq = 1, pre.R = p.B * G, pre.RT = row_tiles((long long)p.B * G);
+        pre.width = 0, pre.cap = pre.fixed_len = prefix_len;
+        pre.C = pass_ctas(1, p.Hkv, pre.RT, prefix_len, tk);
+        pre.part = reinterpret_cast<float*>(static_cast<char*>(ws) +
+                                            pass_bytes(own.C, (long long)p.B * p.Hkv * own.RT, p.D));
+    }
+    if (p.dtype == SSA_BF16)
+        return p.D == 64 ? run<__nv_bfloat16, 64>(a, own, pre, s) : run<__nv_bfloat16, 128>(a, own, pre, s);
+    return p.D == 64 ? run<float, 64>(a, own, pre, s) : run<float, 128>(a, own, pre, s);
+}
+
+int paged_take_status() {
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_paged_status, sizeof v);
+    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
+    if (v != 0) {
+        const unsigned int zero = 0;
+        cudaMemcpyToSymbol(g_paged_status, &zero, sizeof zero);
+        return fail(SSA_ERR_INVALID_ARG, "paged decode: a %s was out of range", v & 2u ? "page number" : "length");
+    }
+    return SSA_OK;
+}
+
+}  // namespace ssa

@@ -126,6 +126,37 @@ int launch_bwd_tc(const ssa_params_t& p, const void* q, const void* k, const voi
 int bwd_tc_take_status(cudaStream_t s);  // SSA_ERR_TIMEOUT if a wait expired
 int bwd_tc_heads_per_group(const ssa_params_t& p);  // heads sharing the dS workspace
 
+// ---- paged cache and window attention
+// A checked ssa_view_t (data NULL: an optional tensor that is absent).
+struct View {
+    void* data;
+    long long sb, sh, st;  // strides in elements: batch, head, token
+};
+
+// appending to a paged cache (cache_append.cu)
+int launch_cache_append(const ssa_cache_params_t& p, int n, const View& k, const View& v, const View& q,
+                        void* k_pages, void* v_pages, const int32_t* table, const int32_t* lens,
+                        int32_t* new_lens, const int32_t* q_start, const double* inv_freq, int rot,
+                        int interleaved, int pos_offset, const View& q_out, const View& k_out,
+                        cudaStream_t s);
+int append_take_status();  // SSA_ERR_INVALID_ARG if a length, slot or page was out of range
+
+// single tokens over a paged cache, with or without a shared prefix (paged_decode.cu)
+size_t paged_decode_workspace(const ssa_cache_params_t& p, int prefix_len);
+int launch_paged_decode(const ssa_cache_params_t& p, const View& q, const void* k_pages, const void* v_pages,
+                        const int32_t* prefix_pages, int prefix_len, const int32_t* table,
+                        const int32_t* lens, const View& h, float* lse, void* ws, cudaStream_t s);
+int paged_take_status();  // SSA_ERR_INVALID_ARG if a length or page was out of range
+
+// sliding-window attention over sequences, CUDA-core path (window_simt.cu)
+int launch_window_fwd_simt(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
+                           const int32_t* lens, const View& h, float* lse, cudaStream_t s);
+size_t window_bwd_simt_workspace(const ssa_window_params_t& p);
+int launch_window_bwd_simt(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
+                           const int32_t* lens, const View& h, const float* lse, const View& dh,
+                           const View& dq, const View& dk, const View& dv, void* ws, cudaStream_t s);
+int window_take_status();  // SSA_ERR_INVALID_ARG if a length was out of range
+
 // ---- self-tests (selftest.cu)
 int select_take_status();  // SSA_ERR_TIMEOUT if a pooling wait expired
 int decode_take_status();  // SSA_ERR_TIMEOUT if a decode-step wait expired

@@ -1,0 +1,459 @@
+// Sliding-window attention with sinks over whole sequences, CUDA-core path
+// (float32, or SSA_FLAG_FORCE_SIMT): forward, and the gradients.
+//
+//   x_ts = sm_scale q_t . k_s over s <= t with s > t - window or s < sinks,
+//   p_ts = e^(x_ts - lse_t), h_t = sum_s p_ts v_s;
+//   dp_ts = dh_t . v_s, delta_t = dh_t . h_t, ds_ts = p_ts (dp_ts - delta_t) sm_scale,
+//   dq_t = sum_s ds_ts k_s, dk_s = sum_t ds_ts q_t, dv_s = sum_t p_ts dh_t.
+//
+// float32 products run on the FMA pipe, which bounds these kernels: 64 x 64
+// tiles, 256 threads of 4 x 4 scores and 4 x D/16 outputs each, operands in
+// shared memory with rows of D + 4 floats (16 lanes read 16 rows without bank
+// conflicts).  Only the tiles that the window and the sinks reach are
+// visited.  The gradients take two kernels, one CTA per key tile for dk and dv
+// (summing over the query heads of its group in order) and one per query tile
+// for dq, so that every sum has one owner and a fixed order.
+#include "device_util.cuh"
+#include "ssa_internal.h"
+
+namespace ssa {
+namespace {
+
+constexpr int BT = 64;  // tokens of a tile
+constexpr int kThreads = 256;
+constexpr int PP = BT + 4;  // row of a score tile in shared memory
+constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.4426950408889634f;
+
+__device__ unsigned int g_window_status;
+
+struct WinArgs {
+    View q, k, v, h, dh, dq, dk, dv;
+    float* lse;
+    float* delta;
+    const int32_t* lens;
+    int B, Hq, Hkv, G, T, window, sinks;
+    float sm_scale;
+};
+
+__device__ __forceinline__ int seq_len(const WinArgs& a, int b) {
+    if (!a.lens) return a.T;
+    const int n = a.lens[b];
+    if (n < 0 || n > a.T) {
+        atomicOr(&g_window_status, 1u);
+        return n < 0 ? 0 : a.T;
+    }
+    return n;
+}
+__device__ __forceinline__ bool sees(const WinArgs& a, int t, int s) {
+    return s <= t && (t - s < a.window || s < a.sinks);
+}
+template <typename T>
+__device__ __forceinline__ T* at(const View& v, int b, int h, int t) {
+    return static_cast<T*>(v.data) + (size_t)b * v.sb + (size_t)h * v.sh + (size_t)t * v.st;
+}
+
+// 4 consecutive elements as float32
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ void st4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// A tile's rows t0 .. t0 + 63 of one head, on their way through registers; rows
+// from len on are zero, whatever is stored there.
+template <typename T, int D>
+struct Fetch {
+    static constexpr int N = BT * D / 4 / kThreads;
+    float4 x[N];
+    __device__ __forceinline__ void load(const View& v, int b, int h, int t0, int len) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = threadIdx.x + i * kThreads, r = e / (D / 4), c = 4 * (e % (D / 4));
+            x[i] = t0 + r < len ? ld4(at<const T>(v, b, h, t0 + r) + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    __device__ __forceinline__ void store(float* dst) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = threadIdx.x + i * kThreads, r = e / (D / 4), c = 4 * (e % (D / 4));
+            *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = x[i];
+        }
+    }
+};
+
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+
+// s[i][j] = row (4 ty + i) of A . row (tx + 16 j) of B
+template <int D>
+__device__ __forceinline__ void scores(const float* A, const float* Bm, int ty, int tx, float (&s)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = ld4(A + (4 * ty + i) * (D + 4) + d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = ld4(Bm + (tx + 16 * j) * (D + 4) + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
+    }
+}
+
+__device__ __forceinline__ void axpy(float w, float4 v, float4& o) {
+    o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+}
+
+// o[i][c] += sum_n W[4 ty + i][n] X[n][4 tx + 64 c ..]   (W rows of PP, X rows of D + 4)
+template <int D>
+__device__ __forceinline__ void gather(const float* W, const float* X, int ty, int tx, float4 (&o)[4][D / 64]) {
+#pragma unroll 2
+    for (int n = 0; n < BT; n += 4) {
+        float4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = ld4(W + (4 * ty + i) * PP + n);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const float4 x = ld4(X + (n + m) * (D + 4) + 4 * tx + 64 * c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) axpy((&w[i].x)[m], x, o[i][c]);
+            }
+    }
+}
+// o[i][c] += sum_n W[n][4 ty + i] X[n][4 tx + 64 c ..]
+template <int D>
+__device__ __forceinline__ void scatter(const float* W, const float* X, int ty, int tx, float4 (&o)[4][D / 64]) {
+#pragma unroll 4
+    for (int n = 0; n < BT; ++n) {
+        const float4 w = ld4(W + n * PP + 4 * ty);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const float4 x = ld4(X + n * (D + 4) + 4 * tx + 64 * c);
+            axpy(w.x, x, o[0][c]);
+            axpy(w.y, x, o[1][c]);
+            axpy(w.z, x, o[2][c]);
+            axpy(w.w, x, o[3][c]);
+        }
+    }
+}
+
+// Key tiles of the queries t0 .. tl: [0, ns) with sinks only, then [w0, w0 + nw).
+struct KeyTiles {
+    int ns, w0, n;
+    __device__ KeyTiles(const WinArgs& a, int t0, int tl) {
+        const int lo = max(0, t0 - (a.window - 1));
+        ns = (min(a.sinks, lo) + BT - 1) / BT;
+        w0 = max(lo / BT, ns);
+        n = ns + tl / BT + 1 - w0;
+    }
+    __device__ int tile(int j) const { return j < ns ? j : w0 + j - ns; }
+};
+
+template <int D>
+constexpr size_t tile_floats() { return (size_t)BT * (D + 4); }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2)
+window_fwd_simt_kernel(const WinArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    float *Q = sm, *KV = Q + tile_floats<D>(), *P = KV + tile_floats<D>();
+    const int t0 = blockIdx.x * BT, hq = blockIdx.y, b = blockIdx.z, hk = hq / a.G;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int len = seq_len(a, b);
+    float4 o[4][D / 64];
+    float m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (t0 < len) {
+        const float sl2 = a.sm_scale * kLog2e;
+        const KeyTiles kt(a, t0, min(t0 + BT, len) - 1);
+        Fetch<T, D> f;
+        f.load(a.q, b, hq, t0, len);
+        f.store(Q);
+        f.load(a.k, b, hk, kt.tile(0) * BT, len);
+        for (int j = 0; j < kt.n; ++j) {
+            const int s0 = kt.tile(j) * BT;
+            __syncthreads();  // the values of the tile before are used up
+            f.store(KV);
+            f.load(a.v, b, hk, s0, len);
+            __syncthreads();
+            float s[4][4];
+            scores<D>(Q, KV, ty, tx, s);
+            __syncthreads();
+            f.store(KV);
+            if (j + 1 < kt.n) f.load(a.k, b, hk, kt.tile(j + 1) * BT, len);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = t0 + 4 * ty + i;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    s[i][x] = sees(a, t, s0 + tx + 16 * x) ? s[i][x] * sl2 : -INFINITY;
+                    mx = fmaxf(mx, s[i][x]);
+                }
+#pragma unroll
+                for (int sh = 1; sh < 16; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                const float mn = fmaxf(m[i], mx), mz = mn == -INFINITY ? 0.f : mn;
+                const float al = exp2f(m[i] - mz);
+                m[i] = mn;
+                l[i] *= al;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    o[i][c].x *= al, o[i][c].y *= al, o[i][c].z *= al, o[i][c].w *= al;
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float p = exp2f(s[i][x] - mz);
+                    l[i] += p;
+                    P[(4 * ty + i) * PP + tx + 16 * x] = p;
+                }
+            }
+            __syncthreads();
+            gather<D>(P, KV, ty, tx, o);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = t0 + 4 * ty + i;
+        float L = l[i];
+#pragma unroll
+        for (int sh = 1; sh < 16; sh <<= 1) L += __shfl_xor_sync(0xffffffffu, L, sh);
+        if (t >= a.T) continue;
+        const bool row = t < len;
+        const float inv = row ? 1.f / L : 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const float4 x = o[i][c];
+            st4(at<T>(a.h, b, hq, t) + 4 * tx + 64 * c,
+                row ? make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+        if (tx == 0) a.lse[((size_t)b * a.Hq + hq) * a.T + t] = row ? (m[i] + log2f(L)) * kLn2 : -INFINITY;
+    }
+}
+
+// delta_t = dh_t . h_t, one warp per row
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+window_delta_kernel(const WinArgs a) {
+    const int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), hq = blockIdx.y, b = blockIdx.z;
+    const int lane = threadIdx.x & 31;
+    if (t >= a.T) return;
+    float s = 0.f;
+    if (t < seq_len(a, b) && 4 * lane < D)
+        s = dot4(ld4(at<const T>(a.dh, b, hq, t) + 4 * lane), ld4(at<const T>(a.h, b, hq, t) + 4 * lane), 0.f);
+    s = warp_sum(s);
+    if (lane == 0) a.delta[((size_t)b * a.Hq + hq) * a.T + t] = s;
+}
+
+// p and ds of the score tile (queries t0 .., keys s0 ..), s and dp given
+__device__ __forceinline__ void weights(const WinArgs& a, const float* lse, const float* delta, int t0, int s0,
+                                        int len, int ty, int tx, const float (&s)[4][4],
+                                        const float (&dp)[4][4], float* P, float* dS) {
+    const float sl2 = a.sm_scale * kLog2e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = t0 + 4 * ty + i;
+        const float ls = t < len ? lse[t] * kLog2e : 0.f, de = t < len ? delta[t] : 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int key = s0 + tx + 16 * x;
+            const float p = t < len && sees(a, t, key) ? exp2f(fmaf(s[i][x], sl2, -ls)) : 0.f;
+            if (P) P[(4 * ty + i) * PP + tx + 16 * x] = p;
+            dS[(4 * ty + i) * PP + tx + 16 * x] = p * (dp[i][x] - de) * a.sm_scale;
+        }
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_dq_simt_kernel(const WinArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    constexpr size_t N = tile_floats<D>();
+    float *Q = sm, *dO = Q + N, *K = dO + N, *V = K + N, *dS = V + N;
+    const int t0 = blockIdx.x * BT, hq = blockIdx.y, b = blockIdx.z, hk = hq / a.G;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int len = seq_len(a, b);
+    const float* lse = a.lse + ((size_t)b * a.Hq + hq) * a.T;
+    const float* delta = a.delta + ((size_t)b * a.Hq + hq) * a.T;
+    float4 o[4][D / 64];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t0 < len) {
+        const KeyTiles kt(a, t0, min(t0 + BT, len) - 1);
+        Fetch<T, D> f;
+        f.load(a.q, b, hq, t0, len);
+        f.store(Q);
+        f.load(a.dh, b, hq, t0, len);
+        f.store(dO);
+        for (int j = 0; j < kt.n; ++j) {
+            const int s0 = kt.tile(j) * BT;
+            __syncthreads();
+            f.load(a.k, b, hk, s0, len);
+            f.store(K);
+            f.load(a.v, b, hk, s0, len);
+            f.store(V);
+            __syncthreads();
+            float s[4][4], dp[4][4];
+            scores<D>(Q, K, ty, tx, s);
+            scores<D>(dO, V, ty, tx, dp);
+            weights(a, lse, delta, t0, s0, len, ty, tx, s, dp, nullptr, dS);
+            __syncthreads();
+            gather<D>(dS, K, ty, tx, o);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = t0 + 4 * ty + i;
+        if (t >= a.T) continue;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) st4(at<T>(a.dq, b, hq, t) + 4 * tx + 64 * c, o[i][c]);
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_dkdv_simt_kernel(const WinArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    constexpr size_t N = tile_floats<D>();
+    float *Q = sm, *dO = Q + N, *K = dO + N, *V = K + N, *P = V + N, *dS = P + BT * PP;
+    const int s0 = blockIdx.x * BT, hk = blockIdx.y, b = blockIdx.z;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int len = seq_len(a, b);
+    float4 ok[4][D / 64], ov[4][D / 64];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) ok[i][c] = ov[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s0 < len) {
+        Fetch<T, D> f;
+        f.load(a.k, b, hk, s0, len);
+        f.store(K);
+        f.load(a.v, b, hk, s0, len);
+        f.store(V);
+        // the last query that sees a key of the tile (a sink: the last of all)
+        const int tl = s0 < a.sinks ? len - 1 : (int)min((long long)len - 1, (long long)s0 + BT - 1 + a.window - 1);
+        for (int g = 0; g < a.G; ++g) {
+            const int hq = hk * a.G + g;
+            const float* lse = a.lse + ((size_t)b * a.Hq + hq) * a.T;
+            const float* delta = a.delta + ((size_t)b * a.Hq + hq) * a.T;
+            for (int t0 = s0; t0 <= tl; t0 += BT) {
+                __syncthreads();
+                f.load(a.q, b, hq, t0, len);
+                f.store(Q);
+                f.load(a.dh, b, hq, t0, len);
+                f.store(dO);
+                __syncthreads();
+                float s[4][4], dp[4][4];
+                scores<D>(Q, K, ty, tx, s);
+                scores<D>(dO, V, ty, tx, dp);
+                weights(a, lse, delta, t0, s0, len, ty, tx, s, dp, P, dS);
+                __syncthreads();
+                scatter<D>(P, dO, ty, tx, ov);
+                scatter<D>(dS, Q, ty, tx, ok);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = s0 + 4 * ty + i;
+        if (t >= a.T) continue;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            st4(at<T>(a.dk, b, hk, t) + 4 * tx + 64 * c, ok[i][c]);
+            st4(at<T>(a.dv, b, hk, t) + 4 * tx + 64 * c, ov[i][c]);
+        }
+    }
+}
+
+WinArgs args(const ssa_window_params_t& p, const View& q, const View& k, const View& v, const int32_t* lens,
+             const View& h, float* lse) {
+    WinArgs a{};
+    a.q = q, a.k = k, a.v = v, a.h = h, a.lse = lse, a.lens = lens;
+    a.B = p.B, a.Hq = p.Hq, a.Hkv = p.Hkv, a.G = p.Hq / p.Hkv, a.T = p.T;
+    a.window = p.window > 0 && p.window < p.T ? p.window : p.T;  // a window of T tokens leaves none behind
+    a.sinks = a.window < p.T ? (p.sinks < p.T ? p.sinks : p.T) : 0;
+    a.sm_scale = p.sm_scale;
+    return a;
+}
+
+template <typename T, int D>
+int fwd(const WinArgs& a, cudaStream_t s) {
+    constexpr size_t smem = (2 * tile_floats<D>() + BT * PP) * sizeof(float);
+    const int st = opt_in_max_smem<window_fwd_simt_kernel<T, D>>("window_fwd_simt_kernel");
+    if (st != SSA_OK) return st;
+    const dim3 grid((unsigned)((a.T + BT - 1) / BT), (unsigned)a.Hq, (unsigned)a.B);
+    window_fwd_simt_kernel<T, D><<<grid, kThreads, smem, s>>>(a);
+    return check_launch("window_fwd_simt_kernel");
+}
+
+template <typename T, int D>
+int bwd(const WinArgs& a, cudaStream_t s) {
+    constexpr size_t smem_q = (4 * tile_floats<D>() + BT * PP) * sizeof(float);
+    constexpr size_t smem_k = smem_q + BT * PP * sizeof(float);
+    static_assert(smem_k <= kMaxSmemPerCta, "shared memory");
+    int st = opt_in_max_smem<window_dq_simt_kernel<T, D>>("window_dq_simt_kernel");
+    if (st == SSA_OK) st = opt_in_max_smem<window_dkdv_simt_kernel<T, D>>("window_dkdv_simt_kernel");
+    if (st != SSA_OK) return st;
+    const unsigned nt = (unsigned)((a.T + BT - 1) / BT);
+    window_delta_kernel<T, D><<<dim3((unsigned)((a.T + 7) / 8), (unsigned)a.Hq, (unsigned)a.B), kThreads, 0, s>>>(a);
+    window_dkdv_simt_kernel<T, D><<<dim3(nt, (unsigned)a.Hkv, (unsigned)a.B), kThreads, smem_k, s>>>(a);
+    window_dq_simt_kernel<T, D><<<dim3(nt, (unsigned)a.Hq, (unsigned)a.B), kThreads, smem_q, s>>>(a);
+    return check_launch("window backward (CUDA cores)");
+}
+
+}  // namespace
+
+int launch_window_fwd_simt(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
+                           const int32_t* lens, const View& h, float* lse, cudaStream_t s) {
+    const WinArgs a = args(p, q, k, v, lens, h, lse);
+    if (p.dtype == SSA_BF16) return p.D == 64 ? fwd<__nv_bfloat16, 64>(a, s) : fwd<__nv_bfloat16, 128>(a, s);
+    return p.D == 64 ? fwd<float, 64>(a, s) : fwd<float, 128>(a, s);
+}
+
+size_t window_bwd_simt_workspace(const ssa_window_params_t& p) {
+    return align_up((size_t)p.B * p.Hq * p.T * sizeof(float), 256);  // delta
+}
+
+int launch_window_bwd_simt(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
+                           const int32_t* lens, const View& h, const float* lse, const View& dh,
+                           const View& dq, const View& dk, const View& dv, void* ws, cudaStream_t s) {
+    WinArgs a = args(p, q, k, v, lens, h, const_cast<float*>(lse));
+    a.dh = dh, a.dq = dq, a.dk = dk, a.dv = dv, a.delta = static_cast<float*>(ws);
+    if (p.dtype == SSA_BF16) return p.D == 64 ? bwd<__nv_bfloat16, 64>(a, s) : bwd<__nv_bfloat16, 128>(a, s);
+    return p.D == 64 ? bwd<float, 64>(a, s) : bwd<float, 128>(a, s);
+}
+
+int window_take_status() {
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_window_status, sizeof v);
+    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
+    if (v != 0) {
+        const unsigned int zero = 0;
+        cudaMemcpyToSymbol(g_window_status, &zero, sizeof zero);
+        return fail(SSA_ERR_INVALID_ARG, "window attention: a length was out of range");
+    }
+    return SSA_OK;
+}
+
+}  // namespace ssa

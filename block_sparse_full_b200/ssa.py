@@ -6,7 +6,10 @@ Two layers, both argument marshalling only:
   stream are plain integers.
 * ``select_blocks``, ``attn_fwd_dual``, ``align_loss``, ``attn_bwd``,
   ``attn_fwd_sparse``, ``diagnostics`` and ``DecodeCache`` (a key/value cache
-  with its pooled keys, for ``ssa_decode_pool`` / ``ssa_decode_step``): take
+  with its pooled keys, for ``ssa_decode_pool`` / ``ssa_decode_step``);
+  ``window_fwd`` and ``window_bwd`` (sliding-window attention with sinks),
+  ``cache_append``, ``paged_decode``, ``prefix_decode`` and ``PagedCache`` (a
+  paged key/value cache and the attention that reads it): take
   torch CUDA tensors, allocate the outputs and the workspace with torch, pass
   raw device pointers and torch's current stream to the C entry point and
   raise ``SsaError`` on a non-zero status.
@@ -19,7 +22,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from ctypes import POINTER, c_float, c_int, c_size_t, c_uint, c_void_p
+from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_uint, c_void_p
 
 import torch
 
@@ -37,7 +40,10 @@ EXPORTS = (
     "ssa_attn_fwd_dual", "ssa_attn_fwd_sparse", "ssa_attn_diagnostics", "ssa_attn_fwd_dual_diag",
     "ssa_decode_pool",
     "ssa_decode_step", "ssa_align_loss",
-    "ssa_attn_bwd", "ssa_device_status", "ssa_status_string", "ssa_last_error",
+    "ssa_attn_bwd",
+    "ssa_window_workspace_size", "ssa_window_fwd", "ssa_window_bwd",
+    "ssa_cache_append", "ssa_cache_workspace_size", "ssa_paged_decode", "ssa_prefix_decode",
+    "ssa_device_status", "ssa_status_string", "ssa_last_error",
     "ssa_kernel_path", "ssa_bwd_heads_per_group", "ssa_selftest_math", "ssa_selftest_wait_timeout",
     "ssa_debug_set_wait_limit_ns", "ssa_debug_set_ds_budget_bytes", "ssa_debug_set_kernel_events",
     "ssa_version",
@@ -55,11 +61,32 @@ class ssa_params_t(ctypes.Structure):
                 ("topk", c_int), ("dtype", c_int), ("sm_scale", c_float), ("flags", c_uint)]
 
     def __repr__(self):
-        return ("ssa_params_t(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_)
+        return (type(self).__name__ + "(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_)
                 + ")")
 
 
+class ssa_view_t(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("stride_b", c_longlong), ("stride_h", c_longlong),
+                ("stride_t", c_longlong)]
+
+
+class ssa_window_params_t(ctypes.Structure):
+    _fields_ = [("B", c_int), ("Hq", c_int), ("Hkv", c_int), ("T", c_int), ("D", c_int),
+                ("window", c_int), ("sinks", c_int), ("dtype", c_int), ("sm_scale", c_float),
+                ("flags", c_uint)]
+    __repr__ = ssa_params_t.__repr__
+
+
+class ssa_cache_params_t(ctypes.Structure):
+    _fields_ = [("B", c_int), ("Hq", c_int), ("Hkv", c_int), ("D", c_int), ("page", c_int),
+                ("n_pages", c_int), ("max_pages", c_int), ("window", c_int), ("sinks", c_int),
+                ("dtype", c_int), ("sm_scale", c_float), ("flags", c_uint),
+                ("page_stride", c_longlong)]
+    __repr__ = ssa_params_t.__repr__
+
+
 _P = POINTER(ssa_params_t)
+# ssa_window_params_t, ssa_cache_params_t and ssa_view_t arguments take ctypes.byref(...)
 _SIGNATURES = {
     "ssa_workspace_size": (c_size_t, [_P, c_int]),
     "ssa_select_blocks": (c_int, [_P, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
@@ -86,6 +113,13 @@ _SIGNATURES = {
                              c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                              c_float, c_float, c_void_p, c_void_p, c_void_p, c_void_p,
                              c_size_t, c_void_p]),
+    "ssa_window_workspace_size": (c_size_t, [c_void_p]),
+    "ssa_window_fwd": (c_int, [c_void_p] * 8),
+    "ssa_window_bwd": (c_int, [c_void_p] * 12 + [c_size_t, c_void_p]),
+    "ssa_cache_append": (c_int, [c_void_p, c_int] + [c_void_p] * 10 + [c_int] * 3 + [c_void_p] * 3),
+    "ssa_cache_workspace_size": (c_size_t, [c_void_p, c_int]),
+    "ssa_paged_decode": (c_int, [c_void_p] * 9 + [c_size_t, c_void_p]),
+    "ssa_prefix_decode": (c_int, [c_void_p] * 5 + [c_int] + [c_void_p] * 5 + [c_size_t, c_void_p]),
     "ssa_device_status": (c_int, [c_void_p]),
     "ssa_status_string": (ctypes.c_char_p, [c_int]),
     "ssa_last_error": (ctypes.c_char_p, []),
@@ -178,6 +212,45 @@ def ssa_attn_bwd(params, q, k, v, idx, cnt, mask, h_full, h_sparse, lse_full, ls
     return _lib.ssa_attn_bwd(ctypes.byref(params), q, k, v, idx, cnt, mask, h_full, h_sparse,
                              lse_full, lse_sparse, dh_full, dh_sparse, w_sparsity, w_commit,
                              dq, dk, dv, ws, ws_bytes, stream)
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def ssa_window_workspace_size(params):
+    return _lib.ssa_window_workspace_size(_ref(params))
+
+
+def ssa_window_fwd(params, q, k, v, lens, h, lse, stream):
+    return _lib.ssa_window_fwd(_ref(params), _ref(q), _ref(k), _ref(v), lens, _ref(h), lse, stream)
+
+
+def ssa_window_bwd(params, q, k, v, lens, h, lse, dh, dq, dk, dv, ws, ws_bytes, stream):
+    return _lib.ssa_window_bwd(_ref(params), _ref(q), _ref(k), _ref(v), lens, _ref(h), lse, _ref(dh),
+                               _ref(dq), _ref(dk), _ref(dv), ws, ws_bytes, stream)
+
+
+def ssa_cache_append(params, n_tokens, k, v, q, k_pages, v_pages, table, lens, new_lens, q_start,
+                     inv_freq, rot_dim, interleaved, pos_offset, q_out, k_out, stream):
+    return _lib.ssa_cache_append(_ref(params), n_tokens, _ref(k), _ref(v), _ref(q), k_pages, v_pages,
+                                 table, lens, new_lens, q_start, inv_freq, rot_dim, interleaved,
+                                 pos_offset, _ref(q_out), _ref(k_out), stream)
+
+
+def ssa_cache_workspace_size(params, prefix_len):
+    return _lib.ssa_cache_workspace_size(_ref(params), prefix_len)
+
+
+def ssa_paged_decode(params, q, k_pages, v_pages, table, lens, h, lse, ws, ws_bytes, stream):
+    return _lib.ssa_paged_decode(_ref(params), _ref(q), k_pages, v_pages, table, lens, _ref(h), lse,
+                                 ws, ws_bytes, stream)
+
+
+def ssa_prefix_decode(params, q, k_pages, v_pages, prefix_pages, prefix_len, table, lens, h, lse, ws,
+                      ws_bytes, stream):
+    return _lib.ssa_prefix_decode(_ref(params), _ref(q), k_pages, v_pages, prefix_pages, prefix_len,
+                                  table, lens, _ref(h), lse, ws, ws_bytes, stream)
 
 
 def ssa_device_status(stream):
@@ -418,3 +491,284 @@ def attn_bwd(params, q, k, v, mask, fwd, dh_full=None, dh_sparse=None, w_sparsit
 
 def device_status(device=None):
     check(ssa_device_status(_stream(device)), "ssa_device_status")
+
+
+# ------------------------------------------------------------ paged cache and window attention
+
+def window_params(B, Hq, Hkv, T, D, window, sinks, dtype, sm_scale=None, flags=0) -> ssa_window_params_t:
+    """Shape of sliding-window attention (``window`` 0: every earlier token)."""
+    if isinstance(dtype, torch.dtype):
+        dtype = _DT[dtype]
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    return ssa_window_params_t(B, Hq, Hkv, T, D, window, sinks, dtype, sm_scale, flags)
+
+
+def window_params_for(q, k, window, sinks=0, sm_scale=None, flags=0) -> ssa_window_params_t:
+    """For q [B,Hq,T,D] and k [B,Hkv,T,D]."""
+    B, Hq, T, D = q.shape
+    return window_params(B, Hq, k.shape[1], T, D, window, sinks, q.dtype, sm_scale, flags)
+
+
+def cache_params(B, Hq, Hkv, D, page, n_pages, max_pages, dtype, window=0, sinks=0, sm_scale=None,
+                 page_stride=None) -> ssa_cache_params_t:
+    """Shape of a paged cache and of the queries that read it."""
+    if isinstance(dtype, torch.dtype):
+        dtype = _DT[dtype]
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    if page_stride is None:
+        page_stride = Hkv * page * D
+    return ssa_cache_params_t(B, Hq, Hkv, D, page, n_pages, max_pages, window, sinks, dtype, sm_scale, 0,
+                              page_stride)
+
+
+def cache_params_for(q, k_pages, table, window=0, sinks=0, sm_scale=None) -> ssa_cache_params_t:
+    """For q [..., Hq, D], k_pages [n_pages, Hkv, page, D] and table [B, max_pages]."""
+    n_pages, Hkv, page, D = k_pages.shape
+    B, width = table.shape
+    return cache_params(B, q.shape[-2], Hkv, D, page, n_pages, width, k_pages.dtype, window, sinks, sm_scale,
+                        k_pages.stride(0))
+
+
+_I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
+_TORCH_DT = {SSA_F32: torch.float32, SSA_BF16: torch.bfloat16}
+
+
+def _view(t, name, shape, dtype, device):
+    """ssa_view_t of a tensor [B,H,T,D], or [B,H,D] / [T,H,D] (``shape`` says which it must be)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous (stride {st[-1]})")
+    return st
+
+
+def _view4(t, name, shape, dtype, device):
+    st = _view(t, name, shape, dtype, device)
+    return ssa_view_t(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _view_bh(t, name, shape, dtype, device):
+    st = _view(t, name, shape, dtype, device)
+    return ssa_view_t(t.data_ptr(), st[0], st[1], 0)
+
+
+def _view_th(t, name, shape, dtype, device):
+    st = _view(t, name, shape, dtype, device)
+    return ssa_view_t(t.data_ptr(), 0, st[1], st[0])
+
+
+def _plain(t, name, shape, dtype, device):
+    """Pointer of a contiguous tensor of this shape and type (None passes)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _pages(p, t, name, device):
+    shape = (p.n_pages, p.Hkv, p.page, p.D)
+    st = t.stride()
+    if (t.shape != shape or t.dtype != _TORCH_DT[p.dtype] or t.device != device
+            or st[1:] != (p.page * p.D, p.D, 1) or (st[0] != p.page_stride and p.n_pages > 1)):
+        raise ValueError(f"{name} must be {_TORCH_DT[p.dtype]} pages {shape} on {device}, each page contiguous and "
+                         f"{p.page_stride} elements after the one before, got {t.dtype} {tuple(t.shape)} with "
+                         f"strides {st} on {t.device}")
+    return t.data_ptr()
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+class _on:
+    """Makes the tensors' device the current one for a call, if it is not."""
+
+    def __init__(self, device):
+        self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _scratch(nbytes, ws, where, device):
+    if nbytes == ctypes.c_size_t(-1).value:
+        raise SsaError(where, SSA_ERR_INVALID_ARG, ssa_last_error())
+    if ws is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if ws.device != device:
+        raise ValueError(f"ws must be on {device}")
+    return ws
+
+
+def window_fwd(params, q, k, v, lens=None, out=None):
+    """Sliding-window attention with sinks -> dict(h [B,Hq,T,D], lse [B,Hq,T] float32).
+
+    q [B,Hq,T,D], k and v [B,Hkv,T,D] may be strided views (the last axis
+    contiguous); ``lens`` [B] int32 are the lengths of a padded batch, rows
+    behind a length get h = 0 and lse = -inf.  h is laid out like q where q
+    fills its memory, else contiguous.
+    """
+    p, dev = params, _cuda(q, "q")
+    dt = _TORCH_DT[p.dtype]
+    qs, ks = (p.B, p.Hq, p.T, p.D), (p.B, p.Hkv, p.T, p.D)
+    if out is None:
+        out = {"h": torch.empty_like(q), "lse": torch.empty(qs[:3], dtype=_F32, device=dev)}
+    with _on(dev):
+        check(ssa_window_fwd(p, _view4(q, "q", qs, dt, dev), _view4(k, "k", ks, dt, dev),
+                             _view4(v, "v", ks, dt, dev), _plain(lens, "lens", (p.B,), _I32, dev),
+                             _view4(out["h"], "h", qs, dt, dev), _plain(out["lse"], "lse", qs[:3], _F32, dev),
+                             _stream(dev)), "ssa_window_fwd")
+    return out
+
+
+def window_bwd(params, q, k, v, fwd, dh, lens=None, ws=None, out=None):
+    """Gradients (dq, dk, dv) of <dh, h>, from the inputs and the result of ``window_fwd``."""
+    p, dev = params, _cuda(q, "q")
+    dt = _TORCH_DT[p.dtype]
+    qs, ks = (p.B, p.Hq, p.T, p.D), (p.B, p.Hkv, p.T, p.D)
+    dq, dk, dv = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)) if out is None else out
+    ws = _scratch(ssa_window_workspace_size(p), ws, "ssa_window_workspace_size", dev)
+    with _on(dev):
+        check(ssa_window_bwd(p, _view4(q, "q", qs, dt, dev), _view4(k, "k", ks, dt, dev),
+                             _view4(v, "v", ks, dt, dev), _plain(lens, "lens", (p.B,), _I32, dev),
+                             _view4(fwd["h"], "h", qs, dt, dev), _plain(fwd["lse"], "lse", qs[:3], _F32, dev),
+                             _view4(dh, "dh", qs, dt, dev), _view4(dq, "dq", qs, dt, dev),
+                             _view4(dk, "dk", ks, dt, dev), _view4(dv, "dv", ks, dt, dev), _ptr(ws), ws.numel(),
+                             _stream(dev)), "ssa_window_bwd")
+    return dq, dk, dv
+
+
+def cache_append(params, k_pages, v_pages, table, lens, k, v, q=None, inv_freq=None, interleaved=False,
+                 q_start=None, pos_offset=0, new_lens=None, q_out=None, k_out=None):
+    """Rotates new keys (and queries) to their positions and appends keys and values to the pages
+    -> dict(q, lens): the rotated queries and the sequences' new lengths.
+
+    k, v [N,Hkv,D] and q [N,Hq,D] hold the sequences' new tokens one after the
+    other: ``q_start`` [B+1] int32 says where each begins, without it every
+    sequence has N / B.  ``lens`` [B] int32 are the lengths before.  ``inv_freq``
+    [rot/2] float64 holds the rotation's angles per position.  ``new_lens`` may
+    be ``lens`` (advanced in place), ``q_out`` may be q, ``k_out`` (k itself or
+    another tensor) also receives the rotated keys.
+    """
+    p, dev = params, _cuda(k, "k")
+    dt, N = _TORCH_DT[p.dtype], k.shape[0]
+    ks, qs = (N, p.Hkv, p.D), (N, p.Hq, p.D)
+    if new_lens is None:
+        new_lens = torch.empty_like(lens)
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    with _on(dev):
+        check(ssa_cache_append(
+            p, N, _view_th(k, "k", ks, dt, dev), _view_th(v, "v", ks, dt, dev),
+            None if q is None else _view_th(q, "q", qs, dt, dev), _pages(p, k_pages, "k_pages", dev),
+            _pages(p, v_pages, "v_pages", dev), _plain(table, "table", (p.B, p.max_pages), _I32, dev),
+            _plain(lens, "lens", (p.B,), _I32, dev), _plain(new_lens, "new_lens", (p.B,), _I32, dev),
+            _plain(q_start, "q_start", (p.B + 1,), _I32, dev),
+            _plain(inv_freq, "inv_freq", (rot // 2,), _F64, dev), rot, int(bool(interleaved)), pos_offset,
+            None if q is None else _view_th(q_out, "q_out", qs, dt, dev),
+            None if k_out is None else _view_th(k_out, "k_out", ks, dt, dev), _stream(dev)), "ssa_cache_append")
+    return {"q": q_out, "lens": new_lens}
+
+
+def _decode_out(p, out, dev, dt):
+    if out is None:
+        out = {"h": torch.empty((p.B, p.Hq, p.D), dtype=dt, device=dev),
+               "lse": torch.empty((p.B, p.Hq), dtype=_F32, device=dev)}
+    return out
+
+
+def paged_decode(params, q, k_pages, v_pages, table, lens, ws=None, out=None):
+    """Attention of one token per sequence, q [B,Hq,D], over the paged cache
+    -> dict(h [B,Hq,D], lse [B,Hq] float32).  ``lens`` count the token itself."""
+    p, dev = params, _cuda(q, "q")
+    dt, hs = _TORCH_DT[p.dtype], (p.B, p.Hq, p.D)
+    out = _decode_out(p, out, dev, dt)
+    ws = _scratch(ssa_cache_workspace_size(p, 0), ws, "ssa_cache_workspace_size", dev)
+    with _on(dev):
+        check(ssa_paged_decode(p, _view_bh(q, "q", hs, dt, dev), _pages(p, k_pages, "k_pages", dev),
+                               _pages(p, v_pages, "v_pages", dev),
+                               _plain(table, "table", (p.B, p.max_pages), _I32, dev),
+                               _plain(lens, "lens", (p.B,), _I32, dev), _view_bh(out["h"], "h", hs, dt, dev),
+                               _plain(out["lse"], "lse", hs[:2], _F32, dev), _ptr(ws), ws.numel(),
+                               _stream(dev)), "ssa_paged_decode")
+    return out
+
+
+def prefix_decode(params, q, k_pages, v_pages, prefix_pages, prefix_len, table, lens, ws=None, out=None):
+    """``paged_decode`` for a batch behind one shared prefix: every query sees the first
+    ``prefix_len`` tokens of ``prefix_pages`` and the ``lens`` tokens of its own pages."""
+    p, dev = params, _cuda(q, "q")
+    dt, hs = _TORCH_DT[p.dtype], (p.B, p.Hq, p.D)
+    out = _decode_out(p, out, dev, dt)
+    ws = _scratch(ssa_cache_workspace_size(p, prefix_len), ws, "ssa_cache_workspace_size", dev)
+    n = -(-prefix_len // p.page)
+    with _on(dev):
+        check(ssa_prefix_decode(p, _view_bh(q, "q", hs, dt, dev), _pages(p, k_pages, "k_pages", dev),
+                                _pages(p, v_pages, "v_pages", dev),
+                                _plain(prefix_pages, "prefix_pages", (n,), _I32, dev) if n else None, prefix_len,
+                                _plain(table, "table", (p.B, p.max_pages), _I32, dev),
+                                _plain(lens, "lens", (p.B,), _I32, dev), _view_bh(out["h"], "h", hs, dt, dev),
+                                _plain(out["lse"], "lse", hs[:2], _F32, dev), _ptr(ws), ws.numel(),
+                                _stream(dev)), "ssa_prefix_decode")
+    return out
+
+
+class PagedCache:
+    """Pages for B sequences of up to ``capacity`` tokens each, their table and
+    lengths.  ``append`` advances the lengths in place and ``attend`` reads the
+    cache up to them, so that one captured decode step can be replayed.  The
+    table gives every sequence pages of its own, in order; ``table`` may be
+    overwritten with other page numbers.  ``prefix_pages`` (of the same pool) and
+    ``prefix_len`` put one shared prefix before every sequence."""
+
+    def __init__(self, B, Hq, Hkv, D, capacity, dtype, device, page=64, window=0, sinks=0, sm_scale=None,
+                 inv_freq=None, interleaved=False, prefix_len=0):
+        width, shared = max(1, -(-capacity // page)), -(-prefix_len // page)
+        self.params = cache_params(B, Hq, Hkv, D, page, B * width + shared, width, dtype, window, sinks, sm_scale)
+        shape = (B * width + shared, Hkv, page, D)
+        self.k_pages = torch.zeros(shape, dtype=dtype, device=device)
+        self.v_pages = torch.zeros_like(self.k_pages)
+        self.table = torch.arange(B * width, dtype=_I32, device=device).view(B, width)
+        self.lens = torch.zeros(B, dtype=_I32, device=device)
+        self.prefix_len = prefix_len
+        self.prefix_pages = B * width + torch.arange(shared, dtype=_I32, device=device)
+        self.inv_freq, self.interleaved = inv_freq, interleaved
+        n = ssa_cache_workspace_size(self.params, prefix_len)
+        self.ws = _scratch(n, None, "ssa_cache_workspace_size", self.k_pages.device)
+
+    def append(self, k, v, q=None, q_start=None, q_out=None, k_out=None):
+        """Appends new tokens (see ``cache_append``) -> the rotated queries."""
+        return cache_append(self.params, self.k_pages, self.v_pages, self.table, self.lens, k, v, q, self.inv_freq,
+                            self.interleaved, q_start, self.prefix_len, self.lens, q_out, k_out)["q"]
+
+    def fill_prefix(self, k, v, k_out=None):
+        """Writes the shared prefix's keys and values [prefix_len, Hkv, D], rotated to 0, 1, ..."""
+        if not self.prefix_len:
+            raise ValueError("this cache has no shared prefix")
+        p, dev = self.params, self.k_pages.device
+        one = cache_params(1, p.Hq, p.Hkv, p.D, p.page, p.n_pages, max(1, self.prefix_pages.numel()), p.dtype)
+        cache_append(one, self.k_pages, self.v_pages, self.prefix_pages.view(1, -1),
+                     torch.zeros(1, dtype=_I32, device=dev), k, v, None, self.inv_freq, self.interleaved,
+                     k_out=k_out)
+
+    def attend(self, q, out=None):
+        """Attention of each sequence's newest token, q [B,Hq,D] rotated -> dict(h, lse)."""
+        if self.prefix_len:
+            return prefix_decode(self.params, q, self.k_pages, self.v_pages, self.prefix_pages, self.prefix_len,
+                                 self.table, self.lens, self.ws, out)
+        return paged_decode(self.params, q, self.k_pages, self.v_pages, self.table, self.lens, self.ws, out)

@@ -278,9 +278,158 @@ int ssa_attn_bwd(const ssa_params_t* params, const void* q, const void* k,
                  void* dq, void* dk, void* dv,
                  void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * ---- Paged key/value cache and sliding-window attention --------------------
+ * Not part of the paper: the local layers, shared heads and paged caches that
+ * models keep beside their sparse layers.  Key/value heads may be shared:
+ * query head h reads key/value head h / (Hq / Hkv).
+ *
+ * ssa_view_t: a device tensor of rows of D contiguous elements.  Element
+ * (b, h, t, c) is at data[b*stride_b + h*stride_h + t*stride_t + c]; strides
+ * count elements.  data and every stride are multiples of 16 bytes, and the
+ * strides of axes longer than 1 are at least D (no broadcast axes).
+ * Where a call has no batch or no token axis that stride is not read.
+ */
+typedef struct {
+    void* data;
+    long long stride_b, stride_h, stride_t;
+} ssa_view_t;
+
+/*
+ * Sliding-window attention over whole sequences.
+ *   B, Hq, Hkv, T, D : batch, query heads, key/value heads (Hq % Hkv == 0),
+ *                tokens (any T >= 1), head dim 64 or 128.
+ *   window     : a token sees itself and the window - 1 tokens before it;
+ *                0 = every token before it.
+ *   sinks      : the first `sinks` tokens (0..128) stay visible to every
+ *                later token; not read when window is 0.
+ *   dtype      : ssa_dtype_t of every tensor of D-element rows.
+ *   sm_scale   : softmax scale, > 0.
+ *   flags      : 0 or SSA_FLAG_FORCE_SIMT.
+ */
+typedef struct {
+    int B, Hq, Hkv, T, D, window, sinks;
+    int dtype;
+    float sm_scale;
+    unsigned flags;
+} ssa_window_params_t;
+
+/* Bytes of scratch ssa_window_bwd needs ((size_t)-1 on invalid params);
+ * ssa_window_fwd needs none. */
+size_t ssa_window_workspace_size(const ssa_window_params_t* params);
+
+/*
+ * For query t < len of sequence b and the keys s it sees
+ * (s <= t and (s > t - window or s < sinks)), x = sm_scale * q_t . k_s:
+ *   h_t = sum_s e^x v_s / sum_s e^x,  lse_t = log sum_s e^x (float32 [B,Hq,T]).
+ * lens (int32 [B], device, may be NULL = T everywhere) gives each sequence's
+ * length, 0..T (values outside are read as the nearer end and recorded, see
+ * ssa_device_status).  Rows t >= len are empty: h = 0, lse = -inf; q, k, v of
+ * those rows may hold anything, NaN included.  The rows before must be
+ * finite.  q, k, v, h are views with all three strides.
+ */
+int ssa_window_fwd(const ssa_window_params_t* params, const ssa_view_t* q, const ssa_view_t* k,
+                   const ssa_view_t* v, const int32_t* lens, const ssa_view_t* h, float* lse,
+                   void* stream);
+
+/*
+ * Gradients of <dh, h> with respect to q, k and v; h and lse are the
+ * forward's outputs for the same inputs.  dq, dk, dv are written (not
+ * accumulated); dk and dv sum over the query heads that share a head, in a
+ * fixed order (bitwise repeatable).  Rows t >= len get zero gradients; dh of
+ * those rows is not used.
+ */
+int ssa_window_bwd(const ssa_window_params_t* params, const ssa_view_t* q, const ssa_view_t* k,
+                   const ssa_view_t* v, const int32_t* lens, const ssa_view_t* h, const float* lse,
+                   const ssa_view_t* dh, const ssa_view_t* dq, const ssa_view_t* dk,
+                   const ssa_view_t* dv, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * A paged key/value cache: k_pages and v_pages are [n_pages, Hkv, page, D]
+ * with each page's Hkv*page*D elements contiguous and consecutive pages
+ * page_stride elements apart (>= Hkv*page*D, a multiple of 16 bytes).  Token
+ * p of sequence b is row p % page of page table[b][p / page]; table is int32
+ * [B, max_pages].  The entries of pages that hold no token of a sequence are
+ * not read.
+ *   page       : tokens per page: 16, 32, 64 or 128.
+ *   window, sinks : as above, for ssa_paged_decode (the newest token is the
+ *                query's own); not read by the other calls.
+ *   Hq         : query heads.  dtype, sm_scale: as above.  flags: 0.
+ * A length, page number or row count read on the device that is outside its
+ * range is skipped and recorded; ssa_device_status then reports it.
+ */
+typedef struct {
+    int B, Hq, Hkv, D, page, n_pages, max_pages, window, sinks;
+    int dtype;
+    float sm_scale;
+    unsigned flags;
+    long long page_stride;
+} ssa_cache_params_t;
+
+/*
+ * Appends n_tokens new tokens to the cache and rotates keys and queries to
+ * their positions on the way.
+ *   k, v, q    : views [token, head] (stride_b not read) with Hkv, Hkv and Hq
+ *                heads; q may be NULL.
+ *   q_start    : int32 [B+1], device: tokens q_start[b] .. q_start[b+1]-1
+ *                belong to sequence b, in order.  NULL: n_tokens / B each.
+ *   lens       : int32 [B], tokens of each sequence before the call; token i
+ *                of sequence b gets slot lens[b] + i.
+ *   new_lens   : int32 [B] or NULL: receives lens[b] + new tokens, at most
+ *                max_pages*page.  May be lens itself.
+ *   inv_freq   : float64 [rot_dim/2], device: at position p = pos_offset +
+ *                slot, pair i is turned by the angle p * inv_freq[i], formed
+ *                in float64.  rot_dim is even, 0 <= rot_dim <= D; the other
+ *                elements pass unturned.  NULL when rot_dim is 0.
+ *   interleaved: 0: pair i is elements (i, i + rot_dim/2); 1: (2i, 2i+1).
+ *   q_out, k_out : where the turned q and k go (may be q and k themselves);
+ *                k_out may be NULL, q_out is NULL exactly when q is.
+ * Rows before q_start[0] and from q_start[B] on belong to no sequence: the
+ * cache is not written for them, and q_out, k_out get them unturned.  A token
+ * whose slot is past max_pages*page, or whose page number is outside
+ * 0..n_pages-1, is not written and recorded.  The slots written in one call
+ * must be distinct: two sequences may share pages only where neither writes.
+ */
+int ssa_cache_append(const ssa_cache_params_t* params, int n_tokens, const ssa_view_t* k,
+                     const ssa_view_t* v, const ssa_view_t* q, void* k_pages, void* v_pages,
+                     const int32_t* table, const int32_t* lens, int32_t* new_lens,
+                     const int32_t* q_start, const double* inv_freq, int rot_dim, int interleaved,
+                     int pos_offset, const ssa_view_t* q_out, const ssa_view_t* k_out,
+                     void* stream);
+
+/* Bytes of scratch for ssa_paged_decode (prefix_len = 0) or ssa_prefix_decode
+ * ((size_t)-1 on invalid arguments).  Nothing in it needs clearing. */
+size_t ssa_cache_workspace_size(const ssa_cache_params_t* params, int prefix_len);
+
+/*
+ * Attention of one query token per sequence over the cache.  lens[b] counts
+ * the tokens of sequence b including the query's own; the query sees slot s
+ * iff s < lens[b] and (window == 0 or s >= lens[b] - window or s < sinks).
+ * q and h are views [b, head] (stride_t not read), lse is float32 [B,Hq]; a
+ * sequence of length 0 gets h = 0, lse = -inf.  Slots that are not seen are
+ * not read.
+ */
+int ssa_paged_decode(const ssa_cache_params_t* params, const ssa_view_t* q, const void* k_pages,
+                     const void* v_pages, const int32_t* table, const int32_t* lens,
+                     const ssa_view_t* h, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The same for a batch whose sequences all begin with the same prefix of
+ * prefix_len tokens (>= 0), held once in pages prefix_pages (int32, device,
+ * ceil(prefix_len / page) entries; NULL when prefix_len is 0): every query sees the whole prefix and the
+ * lens[b] tokens of its own pages.  The prefix is read once for the batch,
+ * not once per sequence.  params->window must be 0.
+ */
+int ssa_prefix_decode(const ssa_cache_params_t* params, const ssa_view_t* q, const void* k_pages,
+                      const void* v_pages, const int32_t* prefix_pages, int prefix_len,
+                      const int32_t* table, const int32_t* lens, const ssa_view_t* h, float* lse,
+                      void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, then returns SSA_ERR_TIMEOUT if any kernel since the
- * previous call recorded an expired wait (and clears the record), else
- * SSA_ERR_CUDA on a pending CUDA error, else SSA_OK. */
+ * previous call recorded an expired wait (and clears the record),
+ * SSA_ERR_INVALID_ARG if one recorded a page number, slot or length out of
+ * range (and clears that record), else SSA_ERR_CUDA on a pending CUDA error,
+ * else SSA_OK. */
 int ssa_device_status(void* stream);
 
 /* Static text for a status code. */
