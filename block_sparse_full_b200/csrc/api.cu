@@ -436,7 +436,9 @@ int ssa_window_fwd(const ssa_window_params_t* p, const ssa_view_t* q, const ssa_
     SSA_TRY(opt_ptr(lens, "lens"));
     SSA_TRY(need_view(h, "h", p->dtype, p->D, p->B, p->Hq, p->T, &vh));
     SSA_TRY(need_ptr(lse, "lse"));
-    return launch_window_fwd_simt(*p, vq, vk, vv, lens, vh, lse, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (window_tc_supported(*p)) return launch_window_fwd_tc(*p, vq, vk, vv, lens, vh, lse, s);
+    return launch_window_fwd_simt(*p, vq, vk, vv, lens, vh, lse, s);
 }
 
 int ssa_window_bwd(const ssa_window_params_t* p, const ssa_view_t* q, const ssa_view_t* k,
@@ -562,6 +564,7 @@ int ssa_device_status(void* stream) {
     if (st == SSA_OK) st = selftest_take_status();
     if (st == SSA_OK) st = decode_take_status();
     if (st == SSA_OK) st = select_take_status();
+    if (st == SSA_OK) st = attn_tc_take_status();
     if (st == SSA_OK) st = append_take_status();
     if (st == SSA_OK) st = paged_take_status();
     if (st == SSA_OK) st = window_take_status();

@@ -155,6 +155,11 @@ size_t window_bwd_simt_workspace(const ssa_window_params_t& p);
 int launch_window_bwd_simt(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
                            const int32_t* lens, const View& h, const float* lse, const View& dh,
                            const View& dq, const View& dk, const View& dv, void* ws, cudaStream_t s);
+// the same on the tensor cores (window_fwd_tc.cu)
+bool window_tc_supported(const ssa_window_params_t& p);
+int launch_window_fwd_tc(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
+                         const int32_t* lens, const View& h, float* lse, cudaStream_t s);
+int attn_tc_take_status();  // SSA_ERR_TIMEOUT, or SSA_ERR_INVALID_ARG as below
 int window_take_status();  // SSA_ERR_INVALID_ARG if a length was out of range
 
 // ---- self-tests (selftest.cu)
