@@ -6,14 +6,18 @@
 //   S = Q K_j^T, P = 2^(S sm_scale log2 e - m), l += rowsum P, O += P V_j
 // over the key tiles j of 128 that some row of the tile sees.
 //
-// CTA = one query tile of one head, 192 threads, two CTAs on an SM:
-//   warp 0      TMA producer: Q once, then K_j and V_j, one buffer each (K_j+1
-//               is on its way while the weights of tile j are formed, V_j+1
-//               while those of tile j+1 are)
-//   warp 1      TMEM owner and MMA issuer (one thread)
-//   warps 2..5  softmax, a thread per row: it reads its 128 scores from TMEM
-//               into registers, forms P there and writes it back as bf16 over
-//               the scores.
+// CTA = one query tile of one head, 288 threads, two CTAs on an SM:
+//   warp 0      TMEM owner; issues the copies (Q once, then K_j and V_j, one
+//               buffer each: K_j+1 is on its way while the weights of tile j
+//               are formed, V_j+1 while those of tile j+1 are) and the MMAs.
+//               One warp for both, so that two CTAs leave 112 registers for a
+//               thread and a row's 64 scores stay in them.
+//   warps 1..8  softmax, two threads per row with 64 keys of the tile each:
+//               they read their scores from TMEM into registers, form P there
+//               and write it back as bf16 over the scores.  (One thread per row
+//               took 1.6 times as long per tile: four warps cannot hide each
+//               other's latencies.)  The two warps of a row agree on its
+//               running maximum by a vote, and exchange it only when it moves.
 // TMEM: 256 of the 512 columns, S/P in [0, 128), O in [128, 128 + D); shared
 // memory: 3 x 32 KB.  Within a CTA the products and the softmax of a tile
 // follow one another; the two CTAs of an SM take turns, so the tensor cores
@@ -43,6 +47,7 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "ssa_internal.h"
 #include "tc_util.cuh"
@@ -54,13 +59,15 @@ namespace {
 using namespace tc;
 
 constexpr int BM = 128, BN = 128;
-constexpr int kThreads = 192;
+constexpr int kThreads = 288;
+constexpr int kSoftmax = 256;
 constexpr uint32_t HALF_BYTES = 128 * 128;  // [128 rows x 64 columns] bf16 box
 constexpr uint32_t TILE_BYTES = 2 * HALF_BYTES;
 constexpr uint32_t OFF_Q = 0, OFF_K = TILE_BYTES, OFF_V = 2 * TILE_BYTES, OFF_BAR = 3 * TILE_BYTES;
-enum : int { B_QFULL, B_KFULL, B_KEMPTY, B_VFULL, B_VEMPTY, B_SREADY, B_PREADY, B_DRAIN, B_COUNT };
+enum : int { B_QFULL, B_KFULL, B_VFULL, B_VEMPTY, B_SREADY, B_PREADY, B_DRAIN, B_COUNT };
 constexpr uint32_t OFF_MISC = OFF_BAR + B_COUNT * 8;  // [0] tmem base, [1] abort flag
-constexpr uint32_t SMEM_BYTES = OFF_MISC + 16 + 1024;  // slack for 1024-byte alignment
+constexpr uint32_t OFF_XCH = OFF_MISC + 16;  // [parity][half][row] float: maxima, at the end sums
+constexpr uint32_t SMEM_BYTES = OFF_XCH + 512 * 4 + 1024;  // slack for 1024-byte alignment
 constexpr uint32_t TM_S = 0, TM_O = 128, kTmemCols = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.693147180559945309f;
@@ -149,11 +156,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     auto tile_key = [&](int j) { return (j < ns ? 0 : w0 + j - ns) * BN; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(BAR(i), i == B_PREADY ? 128 : 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(BAR(i), i == B_PREADY ? kSoftmax : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == 0) {
         tmem_alloc(base + OFF_MISC, kTmemCols);
         tmem_relinquish();
     }
@@ -164,7 +171,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const unsigned FULL = 0xffffffffu;
 
     if (warp == 0) {
-        // ------------------------------------------------ TMA producer
+        // ------------------------------------------------ copies and MMAs
         if (elect_one() && nt > 0) {
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
@@ -214,33 +221,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             __syncwarp();
         };
-        int nk = 0, nv = 0;
-        for (int j = 0; j < nt; ++j) {
-            if (j > 0 && !__all_sync(FULL, mbar_wait(BAR(B_KEMPTY), (j - 1) & 1, abort_flag, status, lim))) break;
-            load(true, j);
-            nk = j + 1;
-            if (j > 0 && !__all_sync(FULL, mbar_wait(BAR(B_VEMPTY), (j - 1) & 1, abort_flag, status, lim))) break;
-            load(false, j);
-            nv = j + 1;
-        }
-        // copies in flight land before the CTA ends, also where a wait gave up
-        if (nt > 0) wait_drain(BAR(B_QFULL), 0);
-        if (nk > 0) wait_drain(BAR(B_KFULL), (nk - 1) & 1);
-        if (nv > 0) wait_drain(BAR(B_VFULL), (nv - 1) & 1);
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer
+        auto wait = [&](int bar, uint32_t ph) -> bool {
+            return __all_sync(FULL, mbar_wait(BAR(bar), ph, abort_flag, status, lim));
+        };
         const uint64_t qdesc = smem_desc_sw128(base + OFF_Q, 16, 1024);          // K-major
         const uint64_t kdesc = smem_desc_sw128(base + OFF_K, 16, 1024);          // K-major
         const uint64_t vdesc = smem_desc_sw128(base + OFF_V, HALF_BYTES, 1024);  // MN-major
         constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, true);
-        bool ok = nt == 0 || __all_sync(FULL, mbar_wait(BAR(B_QFULL), 0, abort_flag, status, lim));
-        for (int j = 0; ok && j < nt; ++j) {
-            const uint32_t ph = j & 1;
-            const int keys = j < ns ? sink_rows : BN;
-            const uint32_t idesc_qk = idesc_bf16_f32(BM, keys, false);
-            ok = __all_sync(FULL, mbar_wait(BAR(B_KFULL), ph, abort_flag, status, lim));
-            if (!ok) break;
-            fence_after_sync();
+        auto tile_keys = [&](int j) { return j < ns ? sink_rows : BN; };
+        auto scores = [&](int j) {  // S = Q K_j^T
+            const uint32_t idesc_qk = idesc_bf16_f32(BM, tile_keys(j), false);
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
@@ -248,46 +238,95 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     mma_ss(tmem + TM_S, desc_add(qdesc, off), desc_add(kdesc, off), idesc_qk, kk > 0 ? 1u : 0u);
                 }
                 mma_commit(BAR(B_SREADY));
-                mma_commit(BAR(B_KEMPTY));
             }
             __syncwarp();
-            ok = __all_sync(FULL, mbar_wait(BAR(B_PREADY), ph, abort_flag, status, lim)) &&
-                 __all_sync(FULL, mbar_wait(BAR(B_VFULL), ph, abort_flag, status, lim));
+        };
+        int nk = 0, nv = 0;  // tiles whose copies have been issued
+        if (nt > 0) {
+            load(true, 0);
+            load(false, 0);
+            nk = nv = 1;
+        }
+        bool ok = nt == 0 || (wait(B_QFULL, 0) && wait(B_KFULL, 0));
+        if (ok && nt > 0) {
+            fence_after_sync();
+            scores(0);
+        }
+        for (int j = 0; ok && j < nt; ++j) {
+            const uint32_t ph = j & 1;
+            if (j + 1 < nt) {  // K is free once the scores are there
+                ok = wait(B_SREADY, ph);
+                if (!ok) break;
+                load(true, j + 1);
+                nk = j + 2;
+            }
+            ok = wait(B_PREADY, ph) && wait(B_VFULL, ph);
             if (!ok) break;
             fence_after_sync();
+            const int steps = tile_keys(j) / 16;
             if (elect_one()) {
-                if (keys == BN) {
-#pragma unroll
-                    for (int kk = 0; kk < BN / 16; ++kk)
-                        mma_ts(tmem + TM_O, tmem + TM_S + 8 * kk, desc_add(vdesc, kk * 2048), idesc_pv,
-                               j > 0 || kk > 0 ? 1u : 0u);
-                } else {
-                    for (int kk = 0; kk < keys / 16; ++kk)
-                        mma_ts(tmem + TM_O, tmem + TM_S + 8 * kk, desc_add(vdesc, kk * 2048), idesc_pv,
-                               j > 0 || kk > 0 ? 1u : 0u);
-                }
+                for (int kk = 0; kk < steps; ++kk)
+                    mma_ts(tmem + TM_O, tmem + TM_S + 64 * (kk >> 2) + 8 * (kk & 3), desc_add(vdesc, kk * 2048), idesc_pv,
+                           j > 0 || kk > 0 ? 1u : 0u);
                 mma_commit(BAR(B_VEMPTY));
             }
             __syncwarp();
+            if (j + 1 < nt) {
+                ok = wait(B_KFULL, ph ^ 1);
+                if (!ok) break;
+                fence_after_sync();
+                scores(j + 1);  // in order behind the product that reads P from the same columns
+                ok = wait(B_VEMPTY, ph);
+                if (!ok) break;
+                load(false, j + 1);
+                nv = j + 2;
+            }
         }
         if (elect_one()) mma_commit(BAR(B_DRAIN));
         __syncwarp();
         wait_drain(BAR(B_DRAIN), 0);
+        // copies in flight land before the CTA ends, also where a wait gave up
+        if (nt > 0) wait_drain(BAR(B_QFULL), 0);
+        if (nk > 0) wait_drain(BAR(B_KFULL), (nk - 1) & 1);
+        if (nv > 0) wait_drain(BAR(B_VFULL), (nv - 1) & 1);
     } else {
-        // ------------------------------------------------ softmax, a thread per row
-        const int q4 = warp & 3;  // the warp's quarter of the TMEM lanes
+        // ------------------------------------------------ softmax, two threads per row
+        const int q4 = warp & 3, half = (warp - 1) >> 2;  // the warp's TMEM lanes; its half of the keys
         const int r = q4 * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+        const uint32_t sb = trow + TM_S + 64 * half;       // 64 scores; P over the first 32 of these columns
+        const uint32_t ob = trow + TM_O + (D / 2) * half;  // the thread's share of O
+        const int c0 = 64 * half;
+        float* xch = reinterpret_cast<float*>(gbase + OFF_XCH);
         const int t = t0 + r;
         const float sl2 = a.scale_log2;
         float m2 = -INFINITY, l = 0.f;
         bool ok = true;
-        // the running maximum (log2 units) after scores up to mx, and O rescaled where it moved
-        auto raise = [&](float mx, bool first) {
-            const float mn = mx * sl2;
-            if (first) {
+        // or-vote of the two warps that hold the same rows
+        auto pair_vote = [q4](bool flag) -> bool {
+            uint32_t out;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.u32 q, %1, 0;\n\t"
+                "bar.red.or.pred p, %2, 64, q;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(out)
+                : "r"((uint32_t)flag), "r"(2 + q4)
+                : "memory");
+            return out != 0;
+        };
+        // The running maximum (log2 units) after scores up to mx in this half, and
+        // O rescaled where it moved.  False: a wait gave up in either warp.
+        auto raise = [&](float mx, int j, bool got) -> bool {
+            const bool moved = j == 0 || mx * sl2 > m2 + kRescaleThreshold;
+            if (!pair_vote(moved || !got)) return true;
+            float* xm = xch + (j & 1) * 256;
+            xm[half * 128 + r] = mx;
+            if (pair_vote(!got)) return false;
+            const float mn = fmaxf(mx, xm[(1 - half) * 128 + r]) * sl2;
+            if (j == 0) {
                 m2 = mn;
-                return;
+                return true;
             }
             const bool need = mn > m2 + kRescaleThreshold;
             if (__any_sync(FULL, need)) {  // O is complete: its last product came before these scores
@@ -296,97 +335,94 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 m2 = up;
                 l *= al;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(trow + TM_O + 32 * c, o);
+                for (int c = 0; c < D / 32; ++c) {  // (16 at a time: the scores stay in registers)
+                    uint32_t o[16];
+                    tmem_ld<16>(ob + 16 * c, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                    tmem_st32(trow + TM_O + 32 * c, o);
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                    tmem_st<16>(ob + 16 * c, o);
                 }
             }
+            return true;
         };
         for (int j = 0; j < nt; ++j) {
-            const int s0 = tile_key(j);
-            ok = __all_sync(FULL, mbar_wait(BAR(B_SREADY), j & 1, abort_flag, status, lim));
-            if (!ok) break;
+            const int s0 = tile_key(j) + c0;  // the first of the thread's keys
+            bool got = __all_sync(FULL, mbar_wait(BAR(B_SREADY), j & 1, abort_flag, status, lim));
             fence_after_sync();
             // rows that end in this tile: nothing stored behind the end may reach the product
             const int end = len - s0;
-            if (end < BN && (kPrefix || a.lens)) {
-                ok = __all_sync(FULL, mbar_wait(BAR(B_VFULL), j & 1, abort_flag, status, lim));
-                if (!ok) break;
-                if (r >= end) {
+            if (end + c0 < BN && (kPrefix || a.lens)) {
+                got = got && __all_sync(FULL, mbar_wait(BAR(B_VFULL), j & 1, abort_flag, status, lim));
+                if (got && r >= end + c0 && half < D / 64) {
+                    uint4* p = reinterpret_cast<uint4*>(gbase + OFF_V + half * HALF_BYTES + r * 128);
 #pragma unroll
-                    for (int x = 0; x < D / 64; ++x) {
-                        uint4* p = reinterpret_cast<uint4*>(gbase + OFF_V + x * HALF_BYTES + r * 128);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) p[i] = make_uint4(0u, 0u, 0u, 0u);
-                    }
+                    for (int i = 0; i < 8; ++i) p[i] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             if (j < ns) {
                 // the sinks on their own: every row is past all of them
+                const int cols = min(64, sink_rows - c0);
                 float mx = -INFINITY;
-                for (int c0 = 0; c0 < sink_rows; c0 += 16) {
+                for (int c1 = 0; c1 < cols; c1 += 16) {
                     uint32_t u[16];
-                    tmem_ld<16>(trow + TM_S + c0, u);
+                    tmem_ld<16>(sb + c1, u);
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
-                        if (c0 + c < a.sinks) mx = fmaxf(mx, __uint_as_float(u[c]));
+                        if (c0 + c1 + c < a.sinks) mx = fmaxf(mx, __uint_as_float(u[c]));
                 }
-                raise(mx, j == 0);
-                for (int c0 = 0; c0 < sink_rows; c0 += 16) {
+                ok = raise(mx, j, got);
+                if (!ok) break;
+                for (int c1 = 0; c1 < cols; c1 += 16) {
                     uint32_t u[16], pk[8];
-                    tmem_ld<16>(trow + TM_S + c0, u);
+                    tmem_ld<16>(sb + c1, u);
                     tmem_wait_ld();
                     float p[16];
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        p[c] = c0 + c < a.sinks ? ex2(fmaf(__uint_as_float(u[c]), sl2, -m2)) : 0.f;
+                        p[c] = c0 + c1 + c < a.sinks ? ex2(fmaf(__uint_as_float(u[c]), sl2, -m2)) : 0.f;
                         l += p[c];
                     }
 #pragma unroll
                     for (int c = 0; c < 8; ++c) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
-                    // P of columns c0 .. lies over scores c0 / 2 .., which have been read
-                    tmem_st<8>(trow + TM_S + c0 / 2, pk);
+                    // P of columns c1 .. lies over scores c1 / 2 .., which have been read
+                    tmem_st<8>(sb + c1 / 2, pk);
                 }
             } else {
-                float s[BN];
+                float s[64];
+                {
+                    uint32_t u0[32], u1[32];
+                    tmem_ld32(sb, u0);
+                    tmem_ld32(sb + 32, u1);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < BN / 32; ++c) {
-                    uint32_t u[32];
-                    tmem_ld32(trow + TM_S + 32 * c, u);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) s[32 * c + i] = __uint_as_float(u[i]);
+                    for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(u0[c]), s[32 + c] = __uint_as_float(u1[c]);
                 }
-                tmem_wait_ld();
-                // keys of this tile that the row sees: lo <= c <= hi, or a sink c < sk
+                // keys of this half that the row sees: lo <= c <= hi, or a sink c <= sh
                 bool masked;
                 if constexpr (kPrefix) {
-                    masked = end < BN;
+                    masked = end < 64;
                     if (masked) {
 #pragma unroll
-                        for (int c = 0; c < BN; ++c)
+                        for (int c = 0; c < 64; ++c)
                             if (c >= end) s[c] = -INFINITY;
                     }
                 } else {
-                    masked = s0 + BN - 1 > t0 || end < BN || s0 <= t0 + BM - 1 - a.window;
+                    masked = s0 + 63 > t0 || end < 64 || s0 <= t0 + BM - 1 - a.window;
                     if (masked) {
                         const int hi = min(t, len - 1) - s0, lo = max(t - a.window + 1 - s0, 0);
-                        const int sk = a.sinks - s0;
                         const unsigned span = hi >= lo ? (unsigned)(hi - lo) : 0u;
-                        const int off = hi >= lo ? lo : BN;  // an empty range lies past the tile
-                        if (sk <= 0) {
+                        const int off = hi >= lo ? lo : 64;  // an empty range lies past the half
+                        const int sh = min(a.sinks - s0 - 1, hi);
+                        if (a.sinks <= s0) {
 #pragma unroll
-                            for (int c = 0; c < BN; ++c)
+                            for (int c = 0; c < 64; ++c)
                                 if ((unsigned)(c - off) > span) s[c] = -INFINITY;
                         } else {
-                            const int sh = min(sk - 1, hi);
 #pragma unroll
-                            for (int c = 0; c < BN; ++c)
+                            for (int c = 0; c < 64; ++c)
                                 if ((unsigned)(c - off) > span && c > sh) s[c] = -INFINITY;
                         }
                     }
@@ -396,33 +432,37 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 for (int k = 0; k < 4; ++k) {
                     mx4[k] = fmaxf(s[k], s[4 + k]);
 #pragma unroll
-                    for (int c = 8; c < BN; c += 8) mx4[k] = max3(mx4[k], s[c + k], s[c + 4 + k]);
+                    for (int c = 8; c < 64; c += 8) mx4[k] = max3(mx4[k], s[c + k], s[c + 4 + k]);
                 }
-                raise(max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3])), j == 0);
+                ok = raise(max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3])), j, got);
+                if (!ok) break;
                 const float neg = m2 == -INFINITY ? 0.f : -m2;  // a row that has seen nothing: 2^-inf = 0
                 const f32x2 sl = mk2(sl2, sl2), nm = mk2(neg, neg);
                 f32x2 acc[4] = {mk2(0.f, 0.f), mk2(0.f, 0.f), mk2(0.f, 0.f), mk2(0.f, 0.f)};
+                auto weights = [&](auto poly) {
 #pragma unroll
-                for (int cc = 0; cc < BN / 32; ++cc) {
-                    uint32_t pk[16];
+                    for (int c1 = 0; c1 < 32; c1 += 8) {
+                        uint32_t pk[8];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int c = 32 * cc + 2 * i;
-                        const f32x2 x2 = fma2(mk2(s[c], s[c + 1]), sl, nm);
-                        float p0, p1;
-                        if (!masked && ((i & 7) == 1 || (i & 7) == 4 || (i & 7) == 6)) {
-                            un2(exp2_poly4_2(x2), p0, p1);
-                        } else {
-                            float x0, x1;
-                            un2(x2, x0, x1);
-                            p0 = ex2(x0);
-                            p1 = ex2(x1);
+                        for (int i = c1; i < c1 + 8; ++i) {
+                            const f32x2 x2 = fma2(mk2(s[2 * i], s[2 * i + 1]), sl, nm);
+                            float p0, p1;
+                            if (decltype(poly)::value && ((i & 7) == 1 || (i & 7) == 4 || (i & 7) == 6)) {
+                                un2(exp2_poly4_2(x2), p0, p1);
+                            } else {
+                                float x0, x1;
+                                un2(x2, x0, x1);
+                                p0 = ex2(x0);
+                                p1 = ex2(x1);
+                            }
+                            acc[i & 3] = add2(acc[i & 3], mk2(p0, p1));
+                            pk[i - c1] = pack_bf16(p0, p1);
                         }
-                        acc[i & 3] = add2(acc[i & 3], mk2(p0, p1));
-                        pk[i] = pack_bf16(p0, p1);
+                        tmem_st<8>(sb + c1, pk);
                     }
-                    tmem_st<16>(trow + TM_S + 16 * cc, pk);
-                }
+                };
+                if (masked) weights(std::false_type{});
+                else weights(std::true_type{});
                 float x0, x1, y0, y1;
                 un2(add2(acc[0], acc[1]), x0, x1);
                 un2(add2(acc[2], acc[3]), y0, y1);
@@ -433,35 +473,40 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_arrive(BAR(B_PREADY));
         }
         if (ok) ok = __all_sync(FULL, mbar_wait(BAR(B_DRAIN), 0, abort_flag, status, lim));
-        ok = bar_and(ok && !*abort_flag, 1, 128);
+        // the two halves' sums (the maxima of the last two tiles may still be read: a barrier first)
+        ok = bar_and(ok && !*abort_flag, 1, kSoftmax);
+        xch[half * 128 + r] = l;
+        bar_sync(1, kSoftmax);
+        l += xch[(1 - half) * 128 + r];
         fence_after_sync();
         if constexpr (kPrefix) {
             // unnormalised outputs, then the maximum and the sum, in float32
             const int row_b = I * a.nb + r / a.G;
-            if (ok && r < a.nb * a.G && row_b < a.B) {
+            if (ok) {
+                const bool row = r < a.nb * a.G && row_b < a.B;
                 float* slot = a.part + ((size_t)(h * a.ntq + I) * a.splits + split) * BM * (D + 2);
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; c < D / 64; ++c) {
                     uint32_t u[32];
-                    tmem_ld32(trow + TM_O + 32 * c, u);
+                    tmem_ld32(ob + 32 * c, u);
                     tmem_wait_ld();
+                    if (row)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<uint4*>(slot + (size_t)r * D + 32 * c)[i] =
-                            make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                        for (int i = 0; i < 8; ++i)
+                            reinterpret_cast<uint4*>(slot + (size_t)r * D + (D / 2) * half + 32 * c)[i] =
+                                make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
                 }
-                *reinterpret_cast<float2*>(slot + BM * D + 2 * r) = make_float2(m2, l);
+                if (row && half == 0) *reinterpret_cast<float2*>(slot + BM * D + 2 * r) = make_float2(m2, l);
             }
         } else {
             const bool row = t < len;
             const float inv = row ? 1.f / l : 0.f;
-            uint8_t* tile = gbase + OFF_Q;  // the queries are used up
-            const uint32_t rowoff = (uint32_t)r * 128;
+            uint8_t* tile = gbase + OFF_Q + (uint32_t)r * 128;  // the queries are used up
             if (ok) {
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; c < D / 64; ++c) {
                     uint32_t u[32];
-                    if (nt > 0) tmem_ld32(trow + TM_O + 32 * c, u);
+                    if (nt > 0) tmem_ld32(ob + 32 * c, u);
                     tmem_wait_ld();
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
@@ -471,16 +516,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             o[e] = row ? pack_bf16(__uint_as_float(u[8 * v + 2 * e]) * inv,
                                                    __uint_as_float(u[8 * v + 2 * e + 1]) * inv)
                                        : 0u;
-                        const uint32_t chunk = (uint32_t)(((32 * c & 63) >> 3) + v) ^ (uint32_t)(r & 7);
-                        *reinterpret_cast<uint4*>(tile + (c >> 1) * HALF_BYTES + rowoff + chunk * 16) =
+                        const int col = (D / 2) * half + 32 * c + 8 * v;
+                        const uint32_t chunk = (uint32_t)((col & 63) >> 3) ^ (uint32_t)(r & 7);
+                        *reinterpret_cast<uint4*>(tile + (col >> 6) * HALF_BYTES + chunk * 16) =
                             make_uint4(o[0], o[1], o[2], o[3]);
                     }
                 }
-                if (t < a.T) a.lse[((size_t)b * a.H + h) * a.T + t] = row ? (m2 + log2f(l)) * kLn2 : -INFINITY;
+                if (half == 0 && t < a.T)
+                    a.lse[((size_t)b * a.H + h) * a.T + t] = row ? (m2 + log2f(l)) * kLn2 : -INFINITY;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            bar_sync(1, 128);
-            if (warp == 2 && lane == 0 && ok) {
+            bar_sync(1, kSoftmax);
+            if (warp == 1 && lane == 0 && ok) {
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x)
                     tma_store_4d(&tm_h, base + OFF_Q + x * HALF_BYTES, 64 * x, t0, h, b);
@@ -491,7 +538,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 0) {
         fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
