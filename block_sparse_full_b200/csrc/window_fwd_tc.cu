@@ -4,34 +4,30 @@
 // cache (the first half of ssa_prefix_decode).
 //
 //   S = Q K_j^T, P = 2^(S sm_scale log2 e - m), l += rowsum P, O += P V_j
-// over the key tiles j of 128 that some row of the tile sees.
+// over the key tiles j of 64 that some row of the tile sees.
 //
-// CTA = one query tile of one head, 288 threads, two CTAs on an SM:
-//   warp 0      TMEM owner; issues the copies (Q once, then K_j and V_j, one
-//               buffer each: K_j+1 is on its way while the weights of tile j
-//               are formed, V_j+1 while those of tile j+1 are) and the MMAs.
-//               One warp for both, so that two CTAs leave 112 registers for a
-//               thread and a row's 64 scores stay in them.
-//   warps 1..8  softmax, two threads per row with 64 keys of the tile each:
-//               they read their scores from TMEM into registers, form P there
-//               and write it back as bf16 over the scores.  (One thread per row
-//               took 1.6 times as long per tile: four warps cannot hide each
-//               other's latencies.)  The two warps of a row agree on its
-//               running maximum by a vote, and exchange it only when it moves.
-// TMEM: 256 of the 512 columns, S/P in [0, 128), O in [128, 128 + D); shared
-// memory: 3 x 32 KB.  Within a CTA the products and the softmax of a tile
-// follow one another; the two CTAs of an SM take turns, so the tensor cores
-// work on one tile while the other's weights are formed.  (One CTA of two query
-// tiles would need its roles to hand over more often for the same overlap, and
-// with a window the work of a CTA is short: two CTAs also hide each other's
-// first loads and last stores.)
+// CTA = one query tile of one head, 192 threads, two CTAs on an SM:
+//   warp 0      TMA producer: Q once, then K_j and V_j into rings of two
+//   warp 1      TMEM owner and MMA issuer (one thread)
+//   warps 2..5  softmax, a thread per row: it reads its 64 scores from TMEM
+//               into registers, forms P there and writes it back as bf16 over
+//               the scores.
+// TMEM: 256 of the 512 columns: S/P in two buffers of 64, O in [128, 128 + D);
+// shared memory: 96 KB.  The scores of tile j+1 are formed while the weights
+// of tile j are, and the product with V_j while those of tile j+1 are, so a
+// CTA's softmax does not wait for its products; the second CTA of the SM fills
+// the softmax's own latencies, the first loads and the last stores.  Tiles are
+// 64 keys wide because two buffers of 128 beside O would leave TMEM for one
+// CTA only; a score product 64 wide re-reads Q from shared memory at 3/4 of
+// the tensor rate, which costs less than it gains: with one buffer of 128 keys
+// (products and softmax of a CTA taking turns) T = 65536, 8 heads, window 2048
+// took 578 us.
 //
 // A row's running maximum is raised, and O rescaled, only when a tile exceeds
 // it by more than 2^8; the sums are taken against the same maximum, so the
-// result does not change.  Off the masked tiles three eighths of the weights
-// come from a polynomial on the FMA pipe (2.7e-6), because the 16 exponentials
-// per clock of an SM's special-function units would take as long as both
-// products together.
+// result does not change.  All weights come from the special-function units; a
+// polynomial on the FMA pipe for a part of them measured slower at every share
+// from an eighth to a half (the softmax is bound by latency and issue slots).
 //
 // Sinks that the window has left behind are a key tile of their own, of
 // 16-row steps: loads, products and weights cover ceil(sinks / 16) steps only.
@@ -47,7 +43,6 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
-#include <type_traits>
 
 #include "ssa_internal.h"
 #include "tc_util.cuh"
@@ -58,16 +53,18 @@ namespace {
 
 using namespace tc;
 
-constexpr int BM = 128, BN = 128;
-constexpr int kThreads = 288;
-constexpr int kSoftmax = 256;
-constexpr uint32_t HALF_BYTES = 128 * 128;  // [128 rows x 64 columns] bf16 box
-constexpr uint32_t TILE_BYTES = 2 * HALF_BYTES;
-constexpr uint32_t OFF_Q = 0, OFF_K = TILE_BYTES, OFF_V = 2 * TILE_BYTES, OFF_BAR = 3 * TILE_BYTES;
-enum : int { B_QFULL, B_KFULL, B_VFULL, B_VEMPTY, B_SREADY, B_PREADY, B_DRAIN, B_COUNT };
+constexpr int BM = 128, BN = 64;
+constexpr int kThreads = 192;
+constexpr uint32_t Q_BOX = BM * 128;  // [128 rows x 64 columns] bf16 box
+constexpr uint32_t KV_BOX = BN * 128; // [64 rows x 64 columns]
+constexpr uint32_t KV_BYTES = 2 * KV_BOX;
+constexpr uint32_t OFF_Q = 0, OFF_K = 2 * Q_BOX, OFF_V = OFF_K + 2 * KV_BYTES, OFF_BAR = OFF_V + 2 * KV_BYTES;
+enum : int {  // two of each but the first and the last: tile j uses number j % 2
+    B_QFULL, B_KFULL, B_KEMPTY = B_KFULL + 2, B_VFULL = B_KEMPTY + 2, B_VEMPTY = B_VFULL + 2, B_SREADY = B_VEMPTY + 2,
+    B_PREADY = B_SREADY + 2, B_DRAIN = B_PREADY + 2, B_COUNT
+};
 constexpr uint32_t OFF_MISC = OFF_BAR + B_COUNT * 8;  // [0] tmem base, [1] abort flag
-constexpr uint32_t OFF_XCH = OFF_MISC + 16;  // [parity][half][row] float: maxima, at the end sums
-constexpr uint32_t SMEM_BYTES = OFF_XCH + 512 * 4 + 1024;  // slack for 1024-byte alignment
+constexpr uint32_t SMEM_BYTES = OFF_MISC + 16 + 1024;  // slack for 1024-byte alignment
 constexpr uint32_t TM_S = 0, TM_O = 128, kTmemCols = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.693147180559945309f;
@@ -116,7 +113,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
     // ---- the CTA's rows and key tiles
     int b = 0, h, t0 = 0, len, I;  // I: query tile / row tile
-    int ns = 0, w0, nt;            // tiles: ns sink tiles (0 or 1), then w0 .. w0 + nt - ns - 1
+    int ns = 0, w0, nt;            // tiles: ns sink tiles (0 to 2), then w0 .. w0 + nt - ns - 1
     int split = 0;
     if constexpr (kPrefix) {
         split = (int)(blockIdx.x % a.splits);
@@ -147,20 +144,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         } else {
             const int lo = max(0, t0 - (a.window - 1));
             w0 = lo / BN;
-            ns = w0 > 0 && a.sinks > 0 ? 1 : 0;  // sinks fit into one tile; in reach of the window: no tile of their own
-            nt = ns + I + 1 - w0;
+            ns = min((a.sinks + BN - 1) / BN, w0);  // tiles of sinks that every row's window has left behind
+            nt = ns + (min(t0 + BM, len) - 1) / BN + 1 - w0;
         }
     }
     const int hk = kPrefix ? h : h / a.G;
-    const int sink_rows = (a.sinks + 15) & ~15;  // keys that a sink tile loads and multiplies
-    auto tile_key = [&](int j) { return (j < ns ? 0 : w0 + j - ns) * BN; };
+    auto tile_key = [&](int j) { return (j < ns ? j : w0 + j - ns) * BN; };
+    // keys that tile j loads and multiplies: of a sink tile whole steps of 16
+    auto tile_keys = [&](int j) { return j < ns ? min(BN, (a.sinks - j * BN + 15) & ~15) : BN; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(BAR(i), i == B_PREADY ? kSoftmax : 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(BAR(i), i >= B_PREADY && i < B_DRAIN ? 128 : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 0) {
+    if (warp == 1) {
         tmem_alloc(base + OFF_MISC, kTmemCols);
         tmem_relinquish();
     }
@@ -171,7 +169,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const unsigned FULL = 0xffffffffu;
 
     if (warp == 0) {
-        // ------------------------------------------------ copies and MMAs
+        // ------------------------------------------------ TMA producer
         if (elect_one() && nt > 0) {
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
@@ -179,183 +177,161 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_expect_tx(BAR(B_QFULL), (uint32_t)rows * D * 2);
 #pragma unroll
             for (int x = 0; x < D / 64; ++x) {
-                if constexpr (kPrefix) tma_load_4d(base + OFF_Q + x * HALF_BYTES, &tm_q, BAR(B_QFULL), 64 * x, 0, h, I * a.nb);
-                else tma_load_4d(base + OFF_Q + x * HALF_BYTES, &tm_q, BAR(B_QFULL), 64 * x, t0, h, b);
+                if constexpr (kPrefix) tma_load_4d(base + OFF_Q + x * Q_BOX, &tm_q, BAR(B_QFULL), 64 * x, 0, h, I * a.nb);
+                else tma_load_4d(base + OFF_Q + x * Q_BOX, &tm_q, BAR(B_QFULL), 64 * x, t0, h, b);
             }
         }
         __syncwarp();
         // one K or V tile: whole boxes, the sinks' 16-row steps, or a box per page
         auto load = [&](bool is_k, int j) {
             const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-            const uint32_t bar = BAR(is_k ? B_KFULL : B_VFULL), dst = base + (is_k ? OFF_K : OFF_V);
-            const int s0 = tile_key(j);
+            const uint32_t bar = BAR((is_k ? B_KFULL : B_VFULL) + (j & 1));
+            const uint32_t dst = base + (is_k ? OFF_K : OFF_V) + (j & 1) * KV_BYTES;
+            const int s0 = tile_key(j), keys = tile_keys(j);
             if constexpr (kPrefix) {
-                const int np = min(BN / a.page, (len - s0 + a.page - 1) / a.page);
+                const int step = min(BN, a.page);  // rows of a box
+                const int np = min(BN / step, (len - s0 + step - 1) / step);
                 int pg = 0;
                 if (lane < np) {
-                    pg = a.pages[s0 / a.page + lane];
+                    pg = a.pages[(s0 + lane * step) / a.page];
                     if (pg < 0 || pg >= a.n_pages) {
                         atomicOr(&g_attn_tc_range, 2u);
                         pg = 0;
                     }
                 }
-                if (lane == 0) mbar_expect_tx(bar, (uint32_t)(np * a.page) * D * 2);
+                if (lane == 0) mbar_expect_tx(bar, (uint32_t)(np * step) * D * 2);
                 __syncwarp();
                 if (lane < np) {
 #pragma unroll
                     for (int x = 0; x < D / 64; ++x)
-                        tma_load_4d(dst + x * HALF_BYTES + lane * a.page * 128, tm, bar, 64 * x, 0, hk, pg);
-                }
-            } else if (j < ns) {
-                if (elect_one()) {
-                    mbar_expect_tx(bar, (uint32_t)sink_rows * D * 2);
-                    for (int r = 0; r < sink_rows; r += 16)
-#pragma unroll
-                        for (int x = 0; x < D / 64; ++x)
-                            tma_load_4d(dst + x * HALF_BYTES + r * 128, is_k ? &tm_k16 : &tm_v16, bar, 64 * x, r, hk, b);
+                        tma_load_4d(dst + x * KV_BOX + lane * step * 128, tm, bar, 64 * x, s0 % a.page, hk, pg);
                 }
             } else if (elect_one()) {
-                mbar_expect_tx(bar, BN * D * 2);
+                mbar_expect_tx(bar, (uint32_t)keys * D * 2);
+                if (keys < BN) {
+                    for (int r = 0; r < keys; r += 16)
 #pragma unroll
-                for (int x = 0; x < D / 64; ++x) tma_load_4d(dst + x * HALF_BYTES, tm, bar, 64 * x, s0, hk, b);
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load_4d(dst + x * KV_BOX + r * 128, is_k ? &tm_k16 : &tm_v16, bar, 64 * x, s0 + r, hk, b);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) tma_load_4d(dst + x * KV_BOX, tm, bar, 64 * x, s0, hk, b);
+                }
             }
             __syncwarp();
         };
-        auto wait = [&](int bar, uint32_t ph) -> bool {
-            return __all_sync(FULL, mbar_wait(BAR(bar), ph, abort_flag, status, lim));
-        };
-        const uint64_t qdesc = smem_desc_sw128(base + OFF_Q, 16, 1024);          // K-major
-        const uint64_t kdesc = smem_desc_sw128(base + OFF_K, 16, 1024);          // K-major
-        const uint64_t vdesc = smem_desc_sw128(base + OFF_V, HALF_BYTES, 1024);  // MN-major
+        int nk = 0, nv = 0;
+        for (int j = 0; j < nt; ++j) {
+            const uint32_t ph = ((j >> 1) + 1) & 1;
+            if (j > 1 && !__all_sync(FULL, mbar_wait(BAR(B_KEMPTY + (j & 1)), ph, abort_flag, status, lim))) break;
+            load(true, j);
+            nk = j + 1;
+            if (j > 1 && !__all_sync(FULL, mbar_wait(BAR(B_VEMPTY + (j & 1)), ph, abort_flag, status, lim))) break;
+            load(false, j);
+            nv = j + 1;
+        }
+        // copies in flight land before the CTA ends, also where a wait gave up
+        if (nt > 0) wait_drain(BAR(B_QFULL), 0);
+        for (int j = max(0, nk - 2); j < nk; ++j) wait_drain(BAR(B_KFULL + (j & 1)), (j >> 1) & 1);
+        for (int j = max(0, nv - 2); j < nv; ++j) wait_drain(BAR(B_VFULL + (j & 1)), (j >> 1) & 1);
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        const uint64_t qdesc = smem_desc_sw128(base + OFF_Q, 16, 1024);      // K-major
+        const uint64_t kdesc = smem_desc_sw128(base + OFF_K, 16, 1024);      // K-major
+        const uint64_t vdesc = smem_desc_sw128(base + OFF_V, KV_BOX, 1024);  // MN-major
         constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, true);
-        auto tile_keys = [&](int j) { return j < ns ? sink_rows : BN; };
-        auto scores = [&](int j) {  // S = Q K_j^T
+        auto wait = [&](int bar, int j) -> bool {
+            return __all_sync(FULL, mbar_wait(BAR(bar + (j & 1)), (j >> 1) & 1, abort_flag, status, lim));
+        };
+        auto scores = [&](int j) -> bool {  // S = Q K_j^T, behind the product that reads P from the same columns
+            if (!wait(B_KFULL, j)) return false;
+            fence_after_sync();
             const uint32_t idesc_qk = idesc_bf16_f32(BM, tile_keys(j), false);
+            const uint64_t kd = desc_add(kdesc, (j & 1) * KV_BYTES);
             if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
-                    mma_ss(tmem + TM_S, desc_add(qdesc, off), desc_add(kdesc, off), idesc_qk, kk > 0 ? 1u : 0u);
-                }
-                mma_commit(BAR(B_SREADY));
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss(tmem + TM_S + BN * (j & 1), desc_add(qdesc, (kk >> 2) * Q_BOX + (kk & 3) * 32),
+                           desc_add(kd, (kk >> 2) * KV_BOX + (kk & 3) * 32), idesc_qk, kk > 0 ? 1u : 0u);
+                mma_commit(BAR(B_SREADY + (j & 1)));
+                mma_commit(BAR(B_KEMPTY + (j & 1)));
             }
             __syncwarp();
+            return true;
         };
-        int nk = 0, nv = 0;  // tiles whose copies have been issued
-        if (nt > 0) {
-            load(true, 0);
-            load(false, 0);
-            nk = nv = 1;
-        }
-        bool ok = nt == 0 || (wait(B_QFULL, 0) && wait(B_KFULL, 0));
-        if (ok && nt > 0) {
-            fence_after_sync();
-            scores(0);
-        }
+        bool ok = nt == 0 || __all_sync(FULL, mbar_wait(BAR(B_QFULL), 0, abort_flag, status, lim));
+        for (int j = 0; ok && j < min(nt, 2); ++j) ok = scores(j);
         for (int j = 0; ok && j < nt; ++j) {
-            const uint32_t ph = j & 1;
-            if (j + 1 < nt) {  // K is free once the scores are there
-                ok = wait(B_SREADY, ph);
-                if (!ok) break;
-                load(true, j + 1);
-                nk = j + 2;
-            }
-            ok = wait(B_PREADY, ph) && wait(B_VFULL, ph);
+            ok = wait(B_PREADY, j) && wait(B_VFULL, j);
             if (!ok) break;
             fence_after_sync();
+            const uint64_t vd = desc_add(vdesc, (j & 1) * KV_BYTES);
+            const uint32_t p = tmem + TM_S + BN * (j & 1);
             const int steps = tile_keys(j) / 16;
             if (elect_one()) {
                 for (int kk = 0; kk < steps; ++kk)
-                    mma_ts(tmem + TM_O, tmem + TM_S + 64 * (kk >> 2) + 8 * (kk & 3), desc_add(vdesc, kk * 2048), idesc_pv,
-                           j > 0 || kk > 0 ? 1u : 0u);
-                mma_commit(BAR(B_VEMPTY));
+                    mma_ts(tmem + TM_O, p + 8 * kk, desc_add(vd, kk * 2048), idesc_pv, j > 0 || kk > 0 ? 1u : 0u);
+                mma_commit(BAR(B_VEMPTY + (j & 1)));
             }
             __syncwarp();
-            if (j + 1 < nt) {
-                ok = wait(B_KFULL, ph ^ 1);
-                if (!ok) break;
-                fence_after_sync();
-                scores(j + 1);  // in order behind the product that reads P from the same columns
-                ok = wait(B_VEMPTY, ph);
-                if (!ok) break;
-                load(false, j + 1);
-                nv = j + 2;
-            }
+            if (j + 2 < nt) ok = scores(j + 2);
         }
         if (elect_one()) mma_commit(BAR(B_DRAIN));
         __syncwarp();
         wait_drain(BAR(B_DRAIN), 0);
-        // copies in flight land before the CTA ends, also where a wait gave up
-        if (nt > 0) wait_drain(BAR(B_QFULL), 0);
-        if (nk > 0) wait_drain(BAR(B_KFULL), (nk - 1) & 1);
-        if (nv > 0) wait_drain(BAR(B_VFULL), (nv - 1) & 1);
     } else {
-        // ------------------------------------------------ softmax, two threads per row
-        const int q4 = warp & 3, half = (warp - 1) >> 2;  // the warp's TMEM lanes; its half of the keys
+        // ------------------------------------------------ softmax, a thread per row
+        const int q4 = warp & 3;  // the warp's quarter of the TMEM lanes
         const int r = q4 * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
-        const uint32_t sb = trow + TM_S + 64 * half;       // 64 scores; P over the first 32 of these columns
-        const uint32_t ob = trow + TM_O + (D / 2) * half;  // the thread's share of O
-        const int c0 = 64 * half;
-        float* xch = reinterpret_cast<float*>(gbase + OFF_XCH);
         const int t = t0 + r;
         const float sl2 = a.scale_log2;
         float m2 = -INFINITY, l = 0.f;
         bool ok = true;
-        // or-vote of the two warps that hold the same rows
-        auto pair_vote = [q4](bool flag) -> bool {
-            uint32_t out;
-            asm volatile(
-                "{\n\t.reg .pred p, q;\n\t"
-                "setp.ne.u32 q, %1, 0;\n\t"
-                "bar.red.or.pred p, %2, 64, q;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(out)
-                : "r"((uint32_t)flag), "r"(2 + q4)
-                : "memory");
-            return out != 0;
-        };
-        // The running maximum (log2 units) after scores up to mx in this half, and
-        // O rescaled where it moved.  False: a wait gave up in either warp.
-        auto raise = [&](float mx, int j, bool got) -> bool {
-            const bool moved = j == 0 || mx * sl2 > m2 + kRescaleThreshold;
-            if (!pair_vote(moved || !got)) return true;
-            float* xm = xch + (j & 1) * 256;
-            xm[half * 128 + r] = mx;
-            if (pair_vote(!got)) return false;
-            const float mn = fmaxf(mx, xm[(1 - half) * 128 + r]) * sl2;
+        // the running maximum (log2 units) after scores up to mx, and O rescaled where it moved
+        auto raise = [&](float mx, int j) {
+            const float mn = mx * sl2;
             if (j == 0) {
                 m2 = mn;
-                return true;
+                return;
             }
             const bool need = mn > m2 + kRescaleThreshold;
-            if (__any_sync(FULL, need)) {  // O is complete: its last product came before these scores
+            // the last product must have landed in O (if that wait gives up so does the next one)
+            if (__any_sync(FULL, need) &&
+                __all_sync(FULL, mbar_wait(BAR(B_VEMPTY + ((j - 1) & 1)), ((j - 1) >> 1) & 1, abort_flag, status, lim))) {
+                fence_after_sync();
                 const float up = need ? mn : m2;
                 const float al = up == m2 ? 1.f : ex2(m2 - up);  // m2 may be -inf
                 m2 = up;
                 l *= al;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {  // (16 at a time: the scores stay in registers)
-                    uint32_t o[16];
-                    tmem_ld<16>(ob + 16 * c, o);
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(trow + TM_O + 32 * c, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                    tmem_st<16>(ob + 16 * c, o);
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                    tmem_st32(trow + TM_O + 32 * c, o);
                 }
             }
-            return true;
+        };
+        auto wait = [&](int bar, int j) -> bool {
+            return __all_sync(FULL, mbar_wait(BAR(bar + (j & 1)), (j >> 1) & 1, abort_flag, status, lim));
         };
         for (int j = 0; j < nt; ++j) {
-            const int s0 = tile_key(j) + c0;  // the first of the thread's keys
-            bool got = __all_sync(FULL, mbar_wait(BAR(B_SREADY), j & 1, abort_flag, status, lim));
+            const int s0 = tile_key(j);
+            const uint32_t sb = trow + TM_S + BN * (j & 1);
+            ok = wait(B_SREADY, j);
+            if (!ok) break;
             fence_after_sync();
             // rows that end in this tile: nothing stored behind the end may reach the product
             const int end = len - s0;
-            if (end + c0 < BN && (kPrefix || a.lens)) {
-                got = got && __all_sync(FULL, mbar_wait(BAR(B_VFULL), j & 1, abort_flag, status, lim));
-                if (got && r >= end + c0 && half < D / 64) {
-                    uint4* p = reinterpret_cast<uint4*>(gbase + OFF_V + half * HALF_BYTES + r * 128);
+            if (end < BN && (kPrefix || a.lens)) {
+                ok = wait(B_VFULL, j);
+                if (!ok) break;
+                const int vr = r & (BN - 1), box = r / BN;  // 128 threads: 64 rows of two boxes
+                if (vr >= end && box < D / 64) {
+                    uint4* p = reinterpret_cast<uint4*>(gbase + OFF_V + (j & 1) * KV_BYTES + box * KV_BOX + vr * 128);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) p[i] = make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -363,35 +339,34 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             if (j < ns) {
                 // the sinks on their own: every row is past all of them
-                const int cols = min(64, sink_rows - c0);
+                const int keys = tile_keys(j);
                 float mx = -INFINITY;
-                for (int c1 = 0; c1 < cols; c1 += 16) {
+                for (int c0 = 0; c0 < keys; c0 += 16) {
                     uint32_t u[16];
-                    tmem_ld<16>(sb + c1, u);
+                    tmem_ld<16>(sb + c0, u);
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
-                        if (c0 + c1 + c < a.sinks) mx = fmaxf(mx, __uint_as_float(u[c]));
+                        if (s0 + c0 + c < a.sinks) mx = fmaxf(mx, __uint_as_float(u[c]));
                 }
-                ok = raise(mx, j, got);
-                if (!ok) break;
-                for (int c1 = 0; c1 < cols; c1 += 16) {
+                raise(mx, j);
+                for (int c0 = 0; c0 < keys; c0 += 16) {
                     uint32_t u[16], pk[8];
-                    tmem_ld<16>(sb + c1, u);
+                    tmem_ld<16>(sb + c0, u);
                     tmem_wait_ld();
                     float p[16];
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        p[c] = c0 + c1 + c < a.sinks ? ex2(fmaf(__uint_as_float(u[c]), sl2, -m2)) : 0.f;
+                        p[c] = s0 + c0 + c < a.sinks ? ex2(fmaf(__uint_as_float(u[c]), sl2, -m2)) : 0.f;
                         l += p[c];
                     }
 #pragma unroll
                     for (int c = 0; c < 8; ++c) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
-                    // P of columns c1 .. lies over scores c1 / 2 .., which have been read
-                    tmem_st<8>(sb + c1 / 2, pk);
+                    // P of columns c0 .. lies over scores c0 / 2 .., which have been read
+                    tmem_st<8>(sb + c0 / 2, pk);
                 }
             } else {
-                float s[64];
+                float s[BN];
                 {
                     uint32_t u0[32], u1[32];
                     tmem_ld32(sb, u0);
@@ -400,31 +375,26 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                     for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(u0[c]), s[32 + c] = __uint_as_float(u1[c]);
                 }
-                // keys of this half that the row sees: lo <= c <= hi, or a sink c <= sh
-                bool masked;
+                // keys of this tile that the row sees: lo <= c <= hi, or a sink c <= sh
                 if constexpr (kPrefix) {
-                    masked = end < 64;
-                    if (masked) {
+                    if (end < BN) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
+                        for (int c = 0; c < BN; ++c)
                             if (c >= end) s[c] = -INFINITY;
                     }
-                } else {
-                    masked = s0 + 63 > t0 || end < 64 || s0 <= t0 + BM - 1 - a.window;
-                    if (masked) {
-                        const int hi = min(t, len - 1) - s0, lo = max(t - a.window + 1 - s0, 0);
-                        const unsigned span = hi >= lo ? (unsigned)(hi - lo) : 0u;
-                        const int off = hi >= lo ? lo : 64;  // an empty range lies past the half
-                        const int sh = min(a.sinks - s0 - 1, hi);
-                        if (a.sinks <= s0) {
+                } else if (s0 + BN - 1 > t0 || end < BN || s0 <= t0 + BM - 1 - a.window) {
+                    const int hi = min(t, len - 1) - s0, lo = max(t - a.window + 1 - s0, 0);
+                    const unsigned span = hi >= lo ? (unsigned)(hi - lo) : 0u;
+                    const int off = hi >= lo ? lo : BN;  // an empty range lies past the tile
+                    const int sh = min(a.sinks - s0 - 1, hi);
+                    if (a.sinks <= s0) {
 #pragma unroll
-                            for (int c = 0; c < 64; ++c)
-                                if ((unsigned)(c - off) > span) s[c] = -INFINITY;
-                        } else {
+                        for (int c = 0; c < BN; ++c)
+                            if ((unsigned)(c - off) > span) s[c] = -INFINITY;
+                    } else {
 #pragma unroll
-                            for (int c = 0; c < 64; ++c)
-                                if ((unsigned)(c - off) > span && c > sh) s[c] = -INFINITY;
-                        }
+                        for (int c = 0; c < BN; ++c)
+                            if ((unsigned)(c - off) > span && c > sh) s[c] = -INFINITY;
                     }
                 }
                 float mx4[4];
@@ -432,37 +402,26 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 for (int k = 0; k < 4; ++k) {
                     mx4[k] = fmaxf(s[k], s[4 + k]);
 #pragma unroll
-                    for (int c = 8; c < 64; c += 8) mx4[k] = max3(mx4[k], s[c + k], s[c + 4 + k]);
+                    for (int c = 8; c < BN; c += 8) mx4[k] = max3(mx4[k], s[c + k], s[c + 4 + k]);
                 }
-                ok = raise(max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3])), j, got);
-                if (!ok) break;
+                raise(max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3])), j);
                 const float neg = m2 == -INFINITY ? 0.f : -m2;  // a row that has seen nothing: 2^-inf = 0
                 const f32x2 sl = mk2(sl2, sl2), nm = mk2(neg, neg);
                 f32x2 acc[4] = {mk2(0.f, 0.f), mk2(0.f, 0.f), mk2(0.f, 0.f), mk2(0.f, 0.f)};
-                auto weights = [&](auto poly) {
 #pragma unroll
-                    for (int c1 = 0; c1 < 32; c1 += 8) {
-                        uint32_t pk[8];
+                for (int cc = 0; cc < BN / 32; ++cc) {
+                    uint32_t pk[16];
 #pragma unroll
-                        for (int i = c1; i < c1 + 8; ++i) {
-                            const f32x2 x2 = fma2(mk2(s[2 * i], s[2 * i + 1]), sl, nm);
-                            float p0, p1;
-                            if (decltype(poly)::value && ((i & 7) == 1 || (i & 7) == 4 || (i & 7) == 6)) {
-                                un2(exp2_poly4_2(x2), p0, p1);
-                            } else {
-                                float x0, x1;
-                                un2(x2, x0, x1);
-                                p0 = ex2(x0);
-                                p1 = ex2(x1);
-                            }
-                            acc[i & 3] = add2(acc[i & 3], mk2(p0, p1));
-                            pk[i - c1] = pack_bf16(p0, p1);
-                        }
-                        tmem_st<8>(sb + c1, pk);
+                    for (int i = 0; i < 16; ++i) {
+                        const int c = 32 * cc + 2 * i;
+                        float x0, x1;
+                        un2(fma2(mk2(s[c], s[c + 1]), sl, nm), x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        acc[i & 3] = add2(acc[i & 3], mk2(p0, p1));
+                        pk[i] = pack_bf16(p0, p1);
                     }
-                };
-                if (masked) weights(std::false_type{});
-                else weights(std::true_type{});
+                    tmem_st<16>(sb + 16 * cc, pk);
+                }
                 float x0, x1, y0, y1;
                 un2(add2(acc[0], acc[1]), x0, x1);
                 un2(add2(acc[2], acc[3]), y0, y1);
@@ -470,43 +429,38 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             tmem_wait_st();
             fence_before_sync();
-            mbar_arrive(BAR(B_PREADY));
+            mbar_arrive(BAR(B_PREADY + (j & 1)));
         }
         if (ok) ok = __all_sync(FULL, mbar_wait(BAR(B_DRAIN), 0, abort_flag, status, lim));
-        // the two halves' sums (the maxima of the last two tiles may still be read: a barrier first)
-        ok = bar_and(ok && !*abort_flag, 1, kSoftmax);
-        xch[half * 128 + r] = l;
-        bar_sync(1, kSoftmax);
-        l += xch[(1 - half) * 128 + r];
+        ok = bar_and(ok && !*abort_flag, 1, 128);
         fence_after_sync();
         if constexpr (kPrefix) {
             // unnormalised outputs, then the maximum and the sum, in float32
             const int row_b = I * a.nb + r / a.G;
-            if (ok) {
-                const bool row = r < a.nb * a.G && row_b < a.B;
+            if (ok && r < a.nb * a.G && row_b < a.B) {
                 float* slot = a.part + ((size_t)(h * a.ntq + I) * a.splits + split) * BM * (D + 2);
 #pragma unroll 1
-                for (int c = 0; c < D / 64; ++c) {
+                for (int c = 0; c < D / 32; ++c) {
                     uint32_t u[32];
-                    tmem_ld32(ob + 32 * c, u);
+                    tmem_ld32(trow + TM_O + 32 * c, u);
                     tmem_wait_ld();
-                    if (row)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            reinterpret_cast<uint4*>(slot + (size_t)r * D + (D / 2) * half + 32 * c)[i] =
-                                make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                    for (int i = 0; i < 8; ++i)
+                        reinterpret_cast<uint4*>(slot + (size_t)r * D + 32 * c)[i] =
+                            make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
                 }
-                if (row && half == 0) *reinterpret_cast<float2*>(slot + BM * D + 2 * r) = make_float2(m2, l);
+                *reinterpret_cast<float2*>(slot + BM * D + 2 * r) = make_float2(m2, l);
             }
         } else {
             const bool row = t < len;
             const float inv = row ? 1.f / l : 0.f;
-            uint8_t* tile = gbase + OFF_Q + (uint32_t)r * 128;  // the queries are used up
+            uint8_t* tile = gbase + OFF_Q;  // the queries are used up
+            const uint32_t rowoff = (uint32_t)r * 128;
             if (ok) {
 #pragma unroll 1
-                for (int c = 0; c < D / 64; ++c) {
+                for (int c = 0; c < D / 32; ++c) {
                     uint32_t u[32];
-                    if (nt > 0) tmem_ld32(ob + 32 * c, u);
+                    if (nt > 0) tmem_ld32(trow + TM_O + 32 * c, u);
                     tmem_wait_ld();
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
@@ -516,21 +470,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             o[e] = row ? pack_bf16(__uint_as_float(u[8 * v + 2 * e]) * inv,
                                                    __uint_as_float(u[8 * v + 2 * e + 1]) * inv)
                                        : 0u;
-                        const int col = (D / 2) * half + 32 * c + 8 * v;
-                        const uint32_t chunk = (uint32_t)((col & 63) >> 3) ^ (uint32_t)(r & 7);
-                        *reinterpret_cast<uint4*>(tile + (col >> 6) * HALF_BYTES + chunk * 16) =
+                        const uint32_t chunk = (uint32_t)(((32 * c & 63) >> 3) + v) ^ (uint32_t)(r & 7);
+                        *reinterpret_cast<uint4*>(tile + (c >> 1) * Q_BOX + rowoff + chunk * 16) =
                             make_uint4(o[0], o[1], o[2], o[3]);
                     }
                 }
-                if (half == 0 && t < a.T)
-                    a.lse[((size_t)b * a.H + h) * a.T + t] = row ? (m2 + log2f(l)) * kLn2 : -INFINITY;
+                if (t < a.T) a.lse[((size_t)b * a.H + h) * a.T + t] = row ? (m2 + log2f(l)) * kLn2 : -INFINITY;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            bar_sync(1, kSoftmax);
-            if (warp == 1 && lane == 0 && ok) {
+            bar_sync(1, 128);
+            if (warp == 2 && lane == 0 && ok) {
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x)
-                    tma_store_4d(&tm_h, base + OFF_Q + x * HALF_BYTES, 64 * x, t0, h, b);
+                    tma_store_4d(&tm_h, base + OFF_Q + x * Q_BOX, 64 * x, t0, h, b);
                 bulk_commit_group();
                 bulk_wait_group_read0();
             }
@@ -538,7 +490,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 1) {
         fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
