@@ -60,6 +60,17 @@ int opt_ptr(const void* ptr, const char* name) {
     return SSA_OK;
 }
 
+// Arrays of numbers that the kernels read one by one need their own alignment only.
+int need_array(const void* ptr, const char* name, unsigned bytes) {
+    if (!ptr) return fail(SSA_ERR_INVALID_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(ptr) % bytes != 0)
+        return fail(SSA_ERR_INVALID_ARG, "%s is not %u-byte aligned", name, bytes);
+    return SSA_OK;
+}
+int opt_array(const void* ptr, const char* name, unsigned bytes) {
+    return ptr ? need_array(ptr, name, bytes) : SSA_OK;
+}
+
 int need_ws(void* ws, size_t have, size_t need, const char* what) {
     if (need == 0) return SSA_OK;
     if (have < need)
@@ -433,9 +444,9 @@ int ssa_window_fwd(const ssa_window_params_t* p, const ssa_view_t* q, const ssa_
     SSA_TRY(need_view(q, "q", p->dtype, p->D, p->B, p->Hq, p->T, &vq));
     SSA_TRY(need_view(k, "k", p->dtype, p->D, p->B, p->Hkv, p->T, &vk));
     SSA_TRY(need_view(v, "v", p->dtype, p->D, p->B, p->Hkv, p->T, &vv));
-    SSA_TRY(opt_ptr(lens, "lens"));
+    SSA_TRY(opt_array(lens, "lens", 4));
     SSA_TRY(need_view(h, "h", p->dtype, p->D, p->B, p->Hq, p->T, &vh));
-    SSA_TRY(need_ptr(lse, "lse"));
+    SSA_TRY(need_array(lse, "lse", 4));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (window_tc_supported(*p)) return launch_window_fwd_tc(*p, vq, vk, vv, lens, vh, lse, s);
     return launch_window_fwd_simt(*p, vq, vk, vv, lens, vh, lse, s);
@@ -451,9 +462,9 @@ int ssa_window_bwd(const ssa_window_params_t* p, const ssa_view_t* q, const ssa_
     SSA_TRY(need_view(q, "q", p->dtype, p->D, p->B, p->Hq, p->T, &vq));
     SSA_TRY(need_view(k, "k", p->dtype, p->D, p->B, p->Hkv, p->T, &vk));
     SSA_TRY(need_view(v, "v", p->dtype, p->D, p->B, p->Hkv, p->T, &vv));
-    SSA_TRY(opt_ptr(lens, "lens"));
+    SSA_TRY(opt_array(lens, "lens", 4));
     SSA_TRY(need_view(h, "h", p->dtype, p->D, p->B, p->Hq, p->T, &vh));
-    SSA_TRY(need_ptr(lse, "lse"));
+    SSA_TRY(need_array(lse, "lse", 4));
     SSA_TRY(need_view(dh, "dh", p->dtype, p->D, p->B, p->Hq, p->T, &vdh));
     SSA_TRY(need_view(dq, "dq", p->dtype, p->D, p->B, p->Hq, p->T, &vdq));
     SSA_TRY(need_view(dk, "dk", p->dtype, p->D, p->B, p->Hkv, p->T, &vdk));
@@ -491,11 +502,11 @@ int ssa_cache_append(const ssa_cache_params_t* p, int n_tokens, const ssa_view_t
     if (n_tokens > 0 && k_out) SSA_TRY(need_view(k_out, "k_out", p->dtype, p->D, 0, p->Hkv, n_tokens, &vko));
     SSA_TRY(need_ptr(k_pages, "k_pages"));
     SSA_TRY(need_ptr(v_pages, "v_pages"));
-    SSA_TRY(need_ptr(table, "table"));
-    SSA_TRY(need_ptr(lens, "lens"));
-    SSA_TRY(opt_ptr(new_lens, "new_lens"));
-    SSA_TRY(opt_ptr(q_start, "q_start"));
-    if (rot_dim) SSA_TRY(need_ptr(inv_freq, "inv_freq"));
+    SSA_TRY(need_array(table, "table", 4));
+    SSA_TRY(need_array(lens, "lens", 4));
+    SSA_TRY(opt_array(new_lens, "new_lens", 4));
+    SSA_TRY(opt_array(q_start, "q_start", 4));
+    if (rot_dim) SSA_TRY(need_array(inv_freq, "inv_freq", 8));
     if (new_lens && new_lens != lens && new_lens < lens + p->B && lens < new_lens + p->B)
         return fail(SSA_ERR_INVALID_ARG, "new_lens overlaps lens (it may be lens itself)");
     return launch_cache_append(*p, n_tokens, vk, vv, vq, k_pages, v_pages, table, lens, new_lens, q_start,
@@ -526,11 +537,11 @@ int ssa_prefix_decode(const ssa_cache_params_t* p, const ssa_view_t* q, const vo
     SSA_TRY(need_view(q, "q", p->dtype, p->D, p->B, p->Hq, 0, &vq));
     SSA_TRY(need_ptr(k_pages, "k_pages"));
     SSA_TRY(need_ptr(v_pages, "v_pages"));
-    if (prefix_len > 0) SSA_TRY(need_ptr(prefix_pages, "prefix_pages"));
-    SSA_TRY(need_ptr(table, "table"));
-    SSA_TRY(need_ptr(lens, "lens"));
+    if (prefix_len > 0) SSA_TRY(need_array(prefix_pages, "prefix_pages", 4));
+    SSA_TRY(need_array(table, "table", 4));
+    SSA_TRY(need_array(lens, "lens", 4));
     SSA_TRY(need_view(h, "h", p->dtype, p->D, p->B, p->Hq, 0, &vh));
-    SSA_TRY(need_ptr(lse, "lse"));
+    SSA_TRY(need_array(lse, "lse", 4));
     SSA_TRY(need_ws(ws, ws_bytes, paged_decode_workspace(*p, prefix_len), "ssa_prefix_decode"));
     return launch_paged_decode(*p, vq, k_pages, v_pages, prefix_pages, prefix_len, table, lens, vh, lse, ws,
                                static_cast<cudaStream_t>(stream));
@@ -545,10 +556,10 @@ int ssa_paged_decode(const ssa_cache_params_t* p, const ssa_view_t* q, const voi
     SSA_TRY(need_view(q, "q", p->dtype, p->D, p->B, p->Hq, 0, &vq));
     SSA_TRY(need_ptr(k_pages, "k_pages"));
     SSA_TRY(need_ptr(v_pages, "v_pages"));
-    SSA_TRY(need_ptr(table, "table"));
-    SSA_TRY(need_ptr(lens, "lens"));
+    SSA_TRY(need_array(table, "table", 4));
+    SSA_TRY(need_array(lens, "lens", 4));
     SSA_TRY(need_view(h, "h", p->dtype, p->D, p->B, p->Hq, 0, &vh));
-    SSA_TRY(need_ptr(lse, "lse"));
+    SSA_TRY(need_array(lse, "lse", 4));
     SSA_TRY(need_ws(ws, ws_bytes, paged_decode_workspace(*p, 0), "ssa_paged_decode"));
     return launch_paged_decode(*p, vq, k_pages, v_pages, nullptr, 0, table, lens, vh, lse, ws,
                                static_cast<cudaStream_t>(stream));

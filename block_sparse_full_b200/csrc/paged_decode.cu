@@ -19,7 +19,8 @@
 // bandwidth-delay product in flight); rows that are not seen are zero-filled,
 // so that nothing left behind in a page reaches the products.  bf16: one warp
 // takes 16 keys of a tile, S = Q K^T and O += P V on mma.sync m16n8k16 (a
-// tile of 16 query rows cannot fill a larger tensor tile).  float32: CUDA
+// tile of 16 query rows cannot fill a larger tensor tile; the prefix of a batch
+// of more rows goes to the 128-row kernel of window_fwd_tc.cu).  float32: CUDA
 // cores, a warp takes 8 keys.
 #include <cuda_bf16.h>
 
@@ -622,41 +623,69 @@ __device__ __forceinline__ Parts parts_of(const Pass& p, long long total, long l
     return r;
 }
 
+// The partials that a row of the tensor-core pass over the prefix left: one of
+// every split, 128 rows (nb batch entries) to a slot.  splits = 0: none.
+struct PrefixTc {
+    const float* part;
+    int splits, ntq, nb;
+};
+
 // Joins the partials of the rows (one warp each) of one sequence and head.
-// pre: the pass over the shared prefix (nseq = 0: none).
+// pre: the pass over the shared prefix (nseq = 0: none), or ptc.
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
-join_kernel(const DecodeArgs a, const Pass p, const Pass pre) {
+join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int TK = Tile<T>::keys, E = D / 32;  // outputs per lane
+    constexpr size_t kSlot = (size_t)kRows * (D + 2);
     const int b = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 31;
     const int HR = a.Hkv * p.RT;
     const Seen s = seen_tiles(p, seq_len(p, b), TK);
     const long long before = tiles_before(p, b, TK);
     const long long total = tiles_before(p, p.nseq, TK) * HR;
     for (int g = threadIdx.x >> 5; g < a.G; g += blockDim.x >> 5) {
-        Parts own{0, 0, 0, 0}, shared{0, 0, 0, 0};
+        // own partials: a first one, then every `step` floats; then the prefix's likewise
+        const float *own0 = nullptr, *own1 = nullptr, *pre0 = nullptr, *pre1 = nullptr;
+        int n_own = 0, n_pre = 0, pr = 0, prows = kRows;
+        size_t pstep = 2 * kSlot;
         const int rt = g / kRows, r = g % kRows;
         if (s.nt > 0) {
             const long long u0 = before * HR + (long long)(h * p.RT + rt) * s.nt;
-            own = parts_of(p, total, u0, u0 + s.nt, 2 * (size_t)p.C + (size_t)b * HR + h * p.RT + rt);
+            const Parts x = parts_of(p, total, u0, u0 + s.nt, 2 * (size_t)p.C + (size_t)b * HR + h * p.RT + rt);
+            n_own = x.n;
+            own0 = p.part + x.first * kSlot;
+            own1 = p.part + x.rest * kSlot;
         }
-        int pr = 0;
         if (pre.nseq > 0) {
             const int row = b * a.G + g, hr = h * pre.RT + row / kRows;
             const Seen ps = seen_tiles(pre, pre.fixed_len, TK);
             const long long ptotal = (long long)ps.nt * a.Hkv * pre.RT;
             pr = row % kRows;
-            shared = parts_of(pre, ptotal, (long long)hr * ps.nt, (long long)(hr + 1) * ps.nt, 2 * (size_t)pre.C + hr);
-        } else if (own.n == 1) {
+            const Parts x = parts_of(pre, ptotal, (long long)hr * ps.nt, (long long)(hr + 1) * ps.nt, 2 * (size_t)pre.C + hr);
+            n_pre = x.n;
+            pre0 = pre.part + x.first * kSlot;
+            pre1 = pre.part + x.rest * kSlot;
+        } else if (ptc.splits > 0) {
+            prows = 128;
+            pr = (b % ptc.nb) * a.G + g;
+            n_pre = ptc.splits;
+            pstep = (size_t)128 * (D + 2);
+            pre0 = pre1 = ptc.part + (size_t)(h * ptc.ntq + b / ptc.nb) * ptc.splits * pstep;
+        } else if (n_own == 1) {
             continue;  // written by the pass itself
         }
-        const int np = own.n + shared.n;
+        const int np = n_own + n_pre;
         auto part = [&](int i) -> const float* {
-            return i < own.n ? p.part + own.slot(i) * kRows * (D + 2) : pre.part + shared.slot(i - own.n) * kRows * (D + 2);
+            if (i < n_own) return i == 0 ? own0 : own1 + i * (2 * kSlot);
+            i -= n_own;
+            return i == 0 ? pre0 : pre1 + i * pstep;
+        };
+        auto sums = [&](int i) -> float2 {  // (maximum, sum)
+            const float* x = part(i) + (i < n_own ? kRows * D + 2 * r : prows * D + 2 * pr);
+            return *reinterpret_cast<const float2*>(x);
         };
         float M = -INFINITY;
-        for (int i = lane; i < np; i += 32) M = fmaxf(M, part(i)[kRows * D + 2 * (i < own.n ? r : pr)]);
+        for (int i = lane; i < np; i += 32) M = fmaxf(M, sums(i).x);
         M = warp_max(M);
         float L = 0.f, acc[E];
 #pragma unroll
@@ -664,8 +693,7 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre) {
         for (int i0 = 0; i0 < np; i0 += 32) {
             float w = 0.f;
             if (i0 + lane < np) {
-                const int rr = i0 + lane < own.n ? r : pr;
-                const float2 ml = *reinterpret_cast<const float2*>(part(i0 + lane) + kRows * D + 2 * rr);
+                const float2 ml = sums(i0 + lane);
                 w = ml.x == -INFINITY ? 0.f : ex2f(ml.x - M);
                 L += w * ml.y;
             }
@@ -673,7 +701,7 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre) {
 #pragma unroll 8
             for (int i = 0; i < m; ++i) {
                 const float wi = __shfl_sync(0xffffffffu, w, i);
-                const float* src = part(i0 + i) + (i0 + i < own.n ? r : pr) * D + E * lane;
+                const float* src = part(i0 + i) + (i0 + i < n_own ? r : pr) * D + E * lane;
                 float x[E];
                 if constexpr (E == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
                 else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
@@ -714,7 +742,7 @@ int run_pass(const DecodeArgs& a, const Pass& p, cudaStream_t s) {
 }
 
 template <typename T, int D>
-int run(const DecodeArgs& a, const Pass& own, const Pass& pre, cudaStream_t s) {
+int run(const DecodeArgs& a, const Pass& own, const Pass& pre, const PrefixTc& ptc, cudaStream_t s) {
     int st = SSA_OK;
     if (pre.nseq) st = run_pass<T, D>(a, pre, s);
     if (st == SSA_OK) st = run_pass<T, D>(a, own, s);
@@ -728,7 +756,7 @@ int run(const DecodeArgs& a, const Pass& own, const Pass& pre, cudaStream_t s) {
     at.val.programmaticStreamSerializationAllowed = 1;
     c.attrs = &at;
     c.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&c, join_kernel<T, D>, a, own, pre);
+    const cudaError_t e = cudaLaunchKernelEx(&c, join_kernel<T, D>, a, own, pre, ptc);
     if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "join_kernel: %s", cudaGetErrorString(e));
     return check_launch("join_kernel");
 }
@@ -754,7 +782,9 @@ long long seen_most(const ssa_cache_params_t& p) {
 size_t paged_decode_workspace(const ssa_cache_params_t& p, int prefix_len) {
     const int G = p.Hq / p.Hkv, RT = row_tiles(G), tk = tile_keys(p);
     size_t n = pass_bytes(pass_ctas(p.B, p.Hkv, RT, seen_most(p), tk), (long long)p.B * p.Hkv * RT, p.D);
-    if (prefix_len > 0) {
+    if (prefix_len > 0 && prefix_tc_supported(p)) {
+        n += align_up(prefix_tc_plan(p, prefix_len).bytes, 256);
+    } else if (prefix_len > 0) {
         const int PT = row_tiles((long long)p.B * G);
         n += pass_bytes(pass_ctas(1, p.Hkv, PT, prefix_len, tk), (long long)p.Hkv * PT, p.D);
     }
@@ -778,16 +808,23 @@ int launch_paged_decode(const ssa_cache_params_t& p, const View& q, const void* 
     own.C = pass_ctas(p.B, p.Hkv, own.RT, seen_most(p), tk);
     own.direct = prefix_len == 0;
     own.part = static_cast<float*>(ws);
-    if (prefix_len > 0) {
+    PrefixTc ptc{};
+    void* pre_ws = static_cast<char*>(ws) + pass_bytes(own.C, (long long)p.B * p.Hkv * own.RT, p.D);
+    if (prefix_len > 0 && prefix_tc_supported(p)) {
+        const PrefixPlan plan = prefix_tc_plan(p, prefix_len);
+        ptc.part = static_cast<const float*>(pre_ws);
+        ptc.splits = plan.splits, ptc.ntq = plan.ntq, ptc.nb = plan.nb;
+        const int st = launch_prefix_tc(p, q, k_pages, v_pages, prefix_pages, prefix_len, pre_ws, s);
+        if (st != SSA_OK) return st;
+    } else if (prefix_len > 0) {
         pre.table = prefix_pages, pre.nseq = 1, pre.R = p.B * G, pre.RT = row_tiles((long long)p.B * G);
         pre.width = 0, pre.cap = pre.fixed_len = prefix_len;
         pre.C = pass_ctas(1, p.Hkv, pre.RT, prefix_len, tk);
-        pre.part = reinterpret_cast<float*>(static_cast<char*>(ws) +
-                                            pass_bytes(own.C, (long long)p.B * p.Hkv * own.RT, p.D));
+        pre.part = static_cast<float*>(pre_ws);
     }
     if (p.dtype == SSA_BF16)
-        return p.D == 64 ? run<__nv_bfloat16, 64>(a, own, pre, s) : run<__nv_bfloat16, 128>(a, own, pre, s);
-    return p.D == 64 ? run<float, 64>(a, own, pre, s) : run<float, 128>(a, own, pre, s);
+        return p.D == 64 ? run<__nv_bfloat16, 64>(a, own, pre, ptc, s) : run<__nv_bfloat16, 128>(a, own, pre, ptc, s);
+    return p.D == 64 ? run<float, 64>(a, own, pre, ptc, s) : run<float, 128>(a, own, pre, ptc, s);
 }
 
 int paged_take_status() {

@@ -159,6 +159,17 @@ int launch_window_bwd_simt(const ssa_window_params_t& p, const View& q, const Vi
 bool window_tc_supported(const ssa_window_params_t& p);
 int launch_window_fwd_tc(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
                          const int32_t* lens, const View& h, float* lse, cudaStream_t s);
+// the pass of a batch over its shared prefix on the tensor cores (window_fwd_tc.cu):
+// `splits` partials for each of Hkv x ntq row tiles of nb batch entries, 128 rows of D
+// outputs, then 128 (maximum, sum) pairs, float32
+struct PrefixPlan {
+    int splits, ntq, nb;
+    size_t bytes;
+};
+bool prefix_tc_supported(const ssa_cache_params_t& p);
+PrefixPlan prefix_tc_plan(const ssa_cache_params_t& p, int prefix_len);
+int launch_prefix_tc(const ssa_cache_params_t& p, const View& q, const void* k_pages, const void* v_pages,
+                     const int32_t* prefix_pages, int prefix_len, void* ws, cudaStream_t s);
 int attn_tc_take_status();  // SSA_ERR_TIMEOUT, or SSA_ERR_INVALID_ARG as below
 int window_take_status();  // SSA_ERR_INVALID_ARG if a length was out of range
 

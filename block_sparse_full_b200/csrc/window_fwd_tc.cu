@@ -65,6 +65,7 @@ enum : int {  // two of each but the first and the last: tile j uses number j % 
 };
 constexpr uint32_t OFF_MISC = OFF_BAR + B_COUNT * 8;  // [0] tmem base, [1] abort flag
 constexpr uint32_t SMEM_BYTES = OFF_MISC + 16 + 1024;  // slack for 1024-byte alignment
+constexpr int kPrefixCtas = 296, kPrefixTiles = 2;  // CTAs of a pass over a prefix, at least so many key tiles each
 constexpr uint32_t TM_S = 0, TM_O = 128, kTmemCols = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.693147180559945309f;
@@ -336,6 +337,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     for (int i = 0; i < 8; ++i) p[i] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
             }
             if (j < ns) {
                 // the sinks on their own: every row is past all of them
@@ -436,20 +438,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         fence_after_sync();
         if constexpr (kPrefix) {
             // unnormalised outputs, then the maximum and the sum, in float32
-            const int row_b = I * a.nb + r / a.G;
-            if (ok && r < a.nb * a.G && row_b < a.B) {
+            // (TMEM is read by whole warps, rows that do not exist among them)
+            const bool row = r < a.nb * a.G && I * a.nb + r / a.G < a.B;
+            if (ok) {
                 float* slot = a.part + ((size_t)(h * a.ntq + I) * a.splits + split) * BM * (D + 2);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t u[32];
                     tmem_ld32(trow + TM_O + 32 * c, u);
                     tmem_wait_ld();
+                    if (row)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<uint4*>(slot + (size_t)r * D + 32 * c)[i] =
-                            make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                        for (int i = 0; i < 8; ++i)
+                            reinterpret_cast<uint4*>(slot + (size_t)r * D + 32 * c)[i] =
+                                make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                    __syncwarp();
                 }
-                *reinterpret_cast<float2*>(slot + BM * D + 2 * r) = make_float2(m2, l);
+                if (row) *reinterpret_cast<float2*>(slot + BM * D + 2 * r) = make_float2(m2, l);
             }
         } else {
             const bool row = t < len;
@@ -559,6 +564,52 @@ int launch_window_fwd_tc(const ssa_window_params_t& p, const View& q, const View
     a.timeout_ns = wait_limit_ns();
     const long long grid = (long long)p.B * p.Hq * a.ntq;
     return p.D == 64 ? launch<64, false>(m, a, grid, s) : launch<128, false>(m, a, grid, s);
+}
+
+// One row tile reads the prefix once; up to 16 rows a head the kernel for single
+// tokens does the same with less work per key.
+bool prefix_tc_supported(const ssa_cache_params_t& p) {
+    const int G = p.Hq / p.Hkv;
+    return p.dtype == SSA_BF16 && G <= BM && (long long)p.B * G > 16;
+}
+
+PrefixPlan prefix_tc_plan(const ssa_cache_params_t& p, int prefix_len) {
+    PrefixPlan x{};
+    const int G = p.Hq / p.Hkv, tiles = (prefix_len + BN - 1) / BN;
+    x.nb = BM / G;
+    x.ntq = (p.B + x.nb - 1) / x.nb;
+    const long long rows = (long long)p.Hkv * x.ntq;
+    long long n = kPrefixCtas / rows;  // one round of CTAs
+    if (n > tiles / kPrefixTiles) n = tiles / kPrefixTiles;
+    x.splits = n < 1 ? 1 : (int)n;
+    x.bytes = (size_t)rows * x.splits * BM * (p.D + 2) * sizeof(float);
+    return x;
+}
+
+int launch_prefix_tc(const ssa_cache_params_t& p, const View& q, const void* k_pages, const void* v_pages,
+                     const int32_t* prefix_pages, int prefix_len, void* ws, cudaStream_t s) {
+    const PrefixPlan x = prefix_tc_plan(p, prefix_len);
+    const int G = p.Hq / p.Hkv;
+    using U = unsigned long long;
+    CUtensorMap m[6];
+    int st = make_map4(&m[0], q.data, {(U)p.D, (U)G, (U)p.Hkv, (U)p.B}, {q.sh, q.sh * G, q.sb},
+                       {64, (unsigned)G, 1, (unsigned)x.nb});
+    const U dims[4] = {(U)p.D, (U)p.page, (U)p.Hkv, (U)p.n_pages};
+    const long long strides[3] = {p.D, (long long)p.page * p.D, p.page_stride};
+    const unsigned box[4] = {64, (unsigned)(p.page < BN ? p.page : BN), 1, 1};
+    if (st == SSA_OK) st = make_map4(&m[1], const_cast<void*>(k_pages), dims, strides, box);
+    if (st == SSA_OK) st = make_map4(&m[2], const_cast<void*>(v_pages), dims, strides, box);
+    if (st != SSA_OK) return st;
+    m[3] = m[1], m[4] = m[2], m[5] = m[0];  // not used by this pass
+    AttnArgs a{};
+    a.pages = prefix_pages, a.part = static_cast<float*>(ws);
+    a.H = p.Hkv, a.B = p.B, a.G = G, a.T = prefix_len;
+    a.ntq = x.ntq, a.splits = x.splits, a.page = p.page, a.n_pages = p.n_pages, a.nb = x.nb;
+    a.scale_log2 = p.sm_scale * 1.4426950408889634f;
+    a.timeout_ns = wait_limit_ns();
+    const long long grid = (long long)p.Hkv * x.ntq * x.splits;
+    if (grid > 0x7fffffffll) return fail(SSA_ERR_UNSUPPORTED, "prefix_decode: too many row tiles");
+    return p.D == 64 ? launch<64, true>(m, a, grid, s) : launch<128, true>(m, a, grid, s);
 }
 
 int attn_tc_take_status() {

@@ -289,6 +289,7 @@ int ssa_attn_bwd(const ssa_params_t* params, const void* q, const void* k,
  * count elements.  data and every stride are multiples of 16 bytes, and the
  * strides of axes longer than 1 are at least D (no broadcast axes).
  * Where a call has no batch or no token axis that stride is not read.
+ * Lengths, tables, lse and inv_freq need the alignment of their own type only.
  */
 typedef struct {
     void* data;

@@ -299,6 +299,30 @@ def test_large_scores(dtype):
     R.check(out, _reference(q, [(k, v, 0)], 0, None, 1 / math.sqrt(D), q.dtype), ["h", "lse"])
 
 
+def test_slices_of_index_arrays():
+    # table, lengths, prefix pages, token ranges and lse inside larger arrays, 4 bytes off any wider alignment
+    B, Hq, Hkv, D, page, P = 3, 4, 2, 64, 16, 37
+    g = torch.Generator().manual_seed(4)
+    ints = torch.arange(64, dtype=torch.int32, device=DEV)
+    kp = torch.randn(16, Hkv, page, D, generator=g).bfloat16().to(DEV)
+    vp = torch.randn(16, Hkv, page, D, generator=g).bfloat16().to(DEV)
+    table, pre = ints[1:7].view(3, 2), ints[9:12]
+    some = torch.tensor([99, 20, 1, 32, 99, 0, 1, 2, 3], dtype=torch.int32, device=DEV)
+    lens, start = some[1:4], some[5:9]
+    q = torch.randn(B, Hq, D, generator=g).bfloat16().to(DEV)
+    p = ssa.cache_params_for(q, kp, table)
+    lse = torch.empty(B * Hq + 1, device=DEV)
+    out = {"h": torch.empty_like(q), "lse": lse[1:].view(B, Hq)}
+    want = ssa.prefix_decode(p, q, kp, vp, pre.clone(), P, table.clone(), lens.clone())
+    ssa.prefix_decode(p, q, kp, vp, pre, P, table, lens, out=out)
+    k = torch.randn(B, Hkv, D, generator=g).bfloat16().to(DEV)
+    new = ssa.cache_append(p, kp, vp, table, lens - 1, k, k, q_start=start, inv_freq=_freq(66).to(DEV)[1:])["lens"]
+    torch.cuda.synchronize()
+    ssa.device_status()
+    assert torch.equal(out["h"], want["h"]) and torch.equal(out["lse"], want["lse"])
+    assert new.tolist() == [20, 1, 32]
+
+
 def test_bad_lengths_and_pages_are_reported():
     B, Hq, Hkv, D, page = 2, 2, 1, 64, 16
     pool = torch.zeros(3, Hkv, page, D, dtype=torch.bfloat16, device=DEV)

@@ -109,7 +109,8 @@ def test_cache_params(kw, code):
 @pytest.mark.parametrize("kw", [
     dict(n=-1), dict(n=3), dict(rot=63), dict(rot=130), dict(rot=-2), dict(off=-1), dict(f=None), dict(q=view()),
     dict(qo=view()), dict(k=None), dict(v=view(None)), dict(kp=None), dict(vp=A + 4), dict(table=None), dict(lens=None),
-    dict(new=A + 16, lens=A + 20), dict(k=view(t=0)), dict(ko=view(h=4)), dict(start=A + 4),
+    dict(new=A + 16, lens=A + 20), dict(k=view(t=0)), dict(ko=view(h=4)), dict(start=A + 2),
+    dict(f=A + 4), dict(lens=A + 1),
 ])
 def test_append_arguments(kw):
     p = cp(B=2) if "new" not in kw else cp(B=100)
@@ -128,7 +129,7 @@ def test_decode_arguments():
     def dec(q=v, kp=A, vp=A, t=A, lens=A, h=v, lse=A, ws=A, nb=n):
         return ssa.ssa_paged_decode(p, q, kp, vp, t, lens, h, lse, ws, nb, None)
 
-    for kw in (dict(q=None), dict(kp=None), dict(vp=None), dict(t=None), dict(lens=None), dict(h=None), dict(lse=None),
+    for kw in (dict(lens=A + 2), dict(lse=A + 1), dict(t=A + 3), dict(q=None), dict(kp=None), dict(vp=None), dict(t=None), dict(lens=None), dict(h=None), dict(lse=None),
                dict(q=view(h=64)), dict(h=view(b=0)), dict(ws=A + 16)):
         assert dec(**kw) == ssa.SSA_ERR_INVALID_ARG, kw
     assert dec(nb=n - 1) == ssa.SSA_ERR_WORKSPACE and dec(ws=None) == ssa.SSA_ERR_WORKSPACE
