@@ -134,6 +134,10 @@ int validate(const ssa_window_params_t* p) {
     return SSA_OK;
 }
 
+size_t window_bwd_workspace(const ssa_window_params_t& p) {
+    return window_bwd_tc_supported(p) ? window_bwd_tc_workspace(p) : window_bwd_simt_workspace(p);
+}
+
 int validate(const ssa_cache_params_t* p) {
     if (!p) return fail(SSA_ERR_INVALID_ARG, "params is NULL");
     const int st = validate_heads(p->B, p->Hq, p->Hkv, p->D, p->window, p->sinks, p->dtype, p->sm_scale);
@@ -433,7 +437,7 @@ int ssa_attn_bwd(const ssa_params_t* p, const void* q, const void* k, const void
 
 size_t ssa_window_workspace_size(const ssa_window_params_t* p) {
     if (validate(p) != SSA_OK) return (size_t)-1;
-    return window_bwd_simt_workspace(*p);
+    return window_bwd_workspace(*p);
 }
 
 int ssa_window_fwd(const ssa_window_params_t* p, const ssa_view_t* q, const ssa_view_t* k,
@@ -469,7 +473,10 @@ int ssa_window_bwd(const ssa_window_params_t* p, const ssa_view_t* q, const ssa_
     SSA_TRY(need_view(dq, "dq", p->dtype, p->D, p->B, p->Hq, p->T, &vdq));
     SSA_TRY(need_view(dk, "dk", p->dtype, p->D, p->B, p->Hkv, p->T, &vdk));
     SSA_TRY(need_view(dv, "dv", p->dtype, p->D, p->B, p->Hkv, p->T, &vdv));
-    SSA_TRY(need_ws(ws, ws_bytes, window_bwd_simt_workspace(*p), "ssa_window_bwd"));
+    SSA_TRY(need_ws(ws, ws_bytes, window_bwd_workspace(*p), "ssa_window_bwd"));
+    if (window_bwd_tc_supported(*p))
+        return launch_window_bwd_tc(*p, vq, vk, vv, lens, vh, lse, vdh, vdq, vdk, vdv, ws,
+                                    static_cast<cudaStream_t>(stream));
     return launch_window_bwd_simt(*p, vq, vk, vv, lens, vh, lse, vdh, vdq, vdk, vdv, ws,
                                   static_cast<cudaStream_t>(stream));
 }
@@ -576,6 +583,7 @@ int ssa_device_status(void* stream) {
     if (st == SSA_OK) st = decode_take_status();
     if (st == SSA_OK) st = select_take_status();
     if (st == SSA_OK) st = attn_tc_take_status();
+    if (st == SSA_OK) st = window_bwd_take_status();
     if (st == SSA_OK) st = append_take_status();
     if (st == SSA_OK) st = paged_take_status();
     if (st == SSA_OK) st = window_take_status();

@@ -611,7 +611,6 @@ decode_kernel(const DecodeArgs a, const Pass p) {
 struct Parts {
     int c0, n;
     size_t first, rest;  // slot of the first; the i-th one after it is rest + 2 i
-    __device__ size_t slot(int i) const { return i == 0 ? first : rest + 2 * (size_t)i; }
 };
 __device__ __forceinline__ Parts parts_of(const Pass& p, long long total, long long u0, long long u1, size_t own) {
     Parts r;

@@ -159,6 +159,12 @@ int launch_window_bwd_simt(const ssa_window_params_t& p, const View& q, const Vi
 bool window_tc_supported(const ssa_window_params_t& p);
 int launch_window_fwd_tc(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
                          const int32_t* lens, const View& h, float* lse, cudaStream_t s);
+bool window_bwd_tc_supported(const ssa_window_params_t& p);  // (window_bwd_tc.cu)
+size_t window_bwd_tc_workspace(const ssa_window_params_t& p);
+int launch_window_bwd_tc(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
+                         const int32_t* lens, const View& h, const float* lse, const View& dh, const View& dq,
+                         const View& dk, const View& dv, void* ws, cudaStream_t s);
+int window_bwd_take_status();  // SSA_ERR_TIMEOUT, or SSA_ERR_INVALID_ARG as below
 // the pass of a batch over its shared prefix on the tensor cores (window_fwd_tc.cu):
 // `splits` partials for each of Hkv x ntq row tiles of nb batch entries, 128 rows of D
 // outputs, then 128 (maximum, sum) pairs, float32

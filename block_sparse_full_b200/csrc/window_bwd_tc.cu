@@ -1,0 +1,789 @@
+// Gradients of sliding-window attention with sinks on the sm_100a tensor cores
+// (bf16 in, float32 accumulate; ssa_window_bwd).
+//
+//   P = 2^(S sm_scale log2 e - lse log2 e), S = Q K^T
+//   dV = P^T dO,  dS = P (dO V^T - delta),  delta = rowsum(dO h)
+//   dQ = sm_scale dS K,  dK = sm_scale dS^T Q
+//
+// Four launches (five with sinks that the window leaves behind):
+//   window_rows_kernel   -lse log2 e and -delta of every row, padded to whole
+//                        tiles: one pass over dO and h, bound by reading them
+//   window_dkdv_kernel   a CTA per key tile of 128 and key/value head walks the
+//                        query tiles of 64 that see it, for each query head of
+//                        its group in turn: four products per tile
+//   window_dq_kernel     a CTA per query tile of 128 walks the key tiles of 64:
+//                        three products per tile
+//   window_sink_kernel   sums the parts of the first key tile (below)
+// S and dP are formed in both kernels: seven products instead of five, but every sum
+// has one owner and a fixed order, without atomics, and without a dS of T x
+// window elements in memory: writing and reading that costs more than forming
+// it again (at T = 4096, window 1024, 128 heads 2.4 GB, 0.37 ms, against two
+// products of 0.1 ms each).
+//
+// dK/dV: S^T = K Q^T and dP^T = V dO^T (M = 128 keys, N = 64 queries) land in two
+// TMEM buffers each (256 columns), dK and dV take the other 256 (D = 128), so
+// one CTA fills the SM: the scores of tile i+1 are formed while the weights of
+// tile i are, the two products into dK and dV of tile i while those of tile
+// i+1 are.  P^T and dS^T go back to TMEM as bf16 (over the scores) and are the A
+// operands, Q and dO tiles (used K-major for the scores) the MN-major B
+// operands.  Eight softmax warps, two threads per key with 32 queries each.
+// A 128-key tile that holds sinks is seen by every later query; the queries
+// past the window's reach are split into stretches of about a CTA's usual
+// work, whose float32 parts are summed in order by window_sink_kernel.
+//
+// dQ: 256 TMEM columns (S 64, dP 64, dQ 128) and 112 KB, so two CTAs share the SM
+// and take turns on the tensor cores.
+//
+// Rows and keys behind a sequence's length may be NaN: weights are selected, not
+// multiplied, to zero, and such rows of a tile are cleared in shared memory
+// before they are an operand along the summed axis.
+#include <cuda.h>
+
+#include "device_util.cuh"
+#include "ssa_internal.h"
+#include "tc_util.cuh"
+#include "tmap.h"
+
+namespace ssa {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128;  // rows of a CTA's tile
+constexpr int BN = 64;   // rows of a tile that it walks
+constexpr int kThreads = 320, kSoftmax = 256;
+constexpr uint32_t BOX_M = BM * 128, BOX_N = BN * 128;  // boxes of 64 columns
+constexpr uint32_t TILE_M = 2 * BOX_M, TILE_N = 2 * BOX_N;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ unsigned int g_bwd_status;  // bit 0: a wait expired
+__device__ unsigned int g_bwd_range;   // a length was out of range
+
+struct BwdArgs {
+    const int32_t* lens;
+    const float* nlse;    // [B, Hq, Tp]: -lse log2 e
+    const float* ndelta;  // [B, Hq, Tp]: -delta
+    float* part;          // [B, Hkv, 1 + splits][dK, dV][128][D], with sinks out of reach
+    int B, Hq, Hkv, G, T, Tp, window, sinks, nt;  // nt: tiles of 128
+    int splits;           // stretches of queries past the reach of key tile 0
+    float scale, scale_log2;
+    unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ int seq_len(const BwdArgs& a, int b) {
+    if (!a.lens) return a.T;
+    const int n = a.lens[b];
+    if (n < 0 || n > a.T) {
+        if (threadIdx.x == 0) atomicOr(&g_bwd_range, 1u);
+        return n < 0 ? 0 : a.T;
+    }
+    return n;
+}
+
+__device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer() - t0 > kDrainLimitNs) return false;
+    return true;
+}
+// Untiled copy of `bytes` (a multiple of 16) from global memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 TMEM columns of a row, times mul, as bf16 columns [col, col + 32) of a
+// staged [128 rows x 64] x 2 tile (128-byte swizzle)
+__device__ __forceinline__ void stage32(uint32_t taddr, float mul, bool some, uint8_t* tile, int col0, int r) {
+    uint32_t u[32];
+    tmem_ld32(taddr, u);
+    tmem_wait_ld();
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[e] = some ? pack_bf16(__uint_as_float(u[8 * v + 2 * e]) * mul, __uint_as_float(u[8 * v + 2 * e + 1]) * mul)
+                        : 0u;
+        const int col = col0 + 8 * v;
+        const uint32_t chunk = (uint32_t)((col & 63) >> 3) ^ (uint32_t)(r & 7);
+        *reinterpret_cast<uint4*>(tile + (col >> 6) * BOX_M + r * 128 + chunk * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// ---------------------------------------------------------------- rows
+
+template <int D>
+__global__ void __launch_bounds__(256)
+window_rows_kernel(const View h, const View dh, const float* lse, float* nlse, float* ndelta, const BwdArgs a) {
+    constexpr int L = D / 8;  // lanes of a row, 16 bytes each
+    const int t = blockIdx.x * (256 / L) + (int)threadIdx.x / L, c = 8 * ((int)threadIdx.x % L);
+    const int hq = blockIdx.y, b = blockIdx.z;
+    if (t >= a.Tp) return;  // (Tp is a multiple of the rows of a block: whole blocks)
+    const bool row = t < seq_len(a, b);
+    float s = 0.f;
+    if (row) {
+        const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(h.data) + (size_t)b * h.sb +
+                                                        (size_t)hq * h.sh + (size_t)t * h.st + c);
+        const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(dh.data) + (size_t)b * dh.sb +
+                                                        (size_t)hq * dh.sh + (size_t)t * dh.st + c);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), s);
+            s = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), s);
+        }
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (c == 0) {
+        const size_t i = ((size_t)b * a.Hq + hq) * a.Tp + t;
+        nlse[i] = row ? -kLog2e * lse[((size_t)b * a.Hq + hq) * a.T + t] : 0.f;
+        ndelta[i] = -s;
+    }
+}
+
+// ---------------------------------------------------------------- dK, dV
+
+constexpr int kStages = 3;
+constexpr uint32_t STAGE = 2 * TILE_N;  // Q, dO
+constexpr uint32_t K_OFF_K = 0, K_OFF_V = TILE_M, K_OFF_ST = 2 * TILE_M, K_OFF_ROW = K_OFF_ST + kStages * STAGE;
+constexpr uint32_t K_OFF_BAR = K_OFF_ROW + kStages * 2 * BN * 4;  // nlse, ndelta of a tile's 64 queries
+enum : int { KB_KV, KB_FULL, KB_EMPTY = KB_FULL + kStages, KB_SREADY = KB_EMPTY + kStages, KB_PREADY = KB_SREADY + 2,
+             KB_DRAIN = KB_PREADY + 2, KB_COUNT };
+constexpr uint32_t K_OFF_MISC = K_OFF_BAR + KB_COUNT * 8;
+constexpr uint32_t K_SMEM = K_OFF_MISC + 16 + 1024;
+static_assert(K_SMEM <= kMaxSmemPerCta, "shared memory");
+constexpr uint32_t TK_S = 0, TK_DP = 128, TK_DK = 256, TK_DV = 384;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
+                   const BwdArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + K_OFF_MISC + 4);
+    unsigned int* status = &g_bwd_status;
+    const uint64_t lim = a.timeout_ns;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto BAR = [&](int i) { return base + K_OFF_BAR + 8u * (uint32_t)i; };
+
+    // ---- the key tile and the flattened list [i0, i1) of (query head of the group, query tile)
+    const int BH = a.B * a.Hkv;
+    const int item = (int)(blockIdx.x / BH), bh = (int)(blockIdx.x % BH);  // early tiles first: the longest without a window
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int J = item < a.nt ? item : 0;
+    const int k0 = J * BM;
+    const int len = seq_len(a, b);
+    const int last = (len - 1) / BN;  // last query tile (len 0: none, below)
+    const int reach = (int)min((long long)last, ((long long)k0 + BM - 1 + a.window - 1) / BN);
+    int q_first = k0 / BN, q_count, i0 = 0, i1;
+    if (item < a.nt) {
+        q_count = k0 < len ? reach - q_first + 1 : 0;
+        i1 = a.G * q_count;
+    } else {
+        q_first = reach + 1;
+        q_count = len > 0 ? last - reach : 0;
+        const long long n = (long long)a.G * q_count;
+        const int sp = item - a.nt;
+        i0 = (int)(n * sp / a.splits);
+        i1 = (int)(n * (sp + 1) / a.splits);
+    }
+    const int n = i1 - i0;
+    auto head_of = [&](int i) { return hk * a.G + (i0 + i) / q_count; };
+    auto query_of = [&](int i) { return (q_first + (i0 + i) % q_count) * BN; };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < KB_COUNT; ++i) mbar_init(BAR(i), i >= KB_PREADY && i < KB_DRAIN ? kSoftmax : 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(base + K_OFF_MISC, 512);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<uint32_t*>(gbase + K_OFF_MISC);
+    const unsigned FULL = 0xffffffffu;
+    auto wait = [&](int bar, uint32_t ph) -> bool {
+        return __all_sync(FULL, mbar_wait(BAR(bar), ph & 1, abort_flag, status, lim));
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (n > 0 && elect_one()) {
+            prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_do);
+            mbar_expect_tx(BAR(KB_KV), 2 * BM * D * 2);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+                tma_load_4d(base + K_OFF_K + x * BOX_M, &tm_k, BAR(KB_KV), 64 * x, k0, hk, b);
+                tma_load_4d(base + K_OFF_V + x * BOX_M, &tm_v, BAR(KB_KV), 64 * x, k0, hk, b);
+            }
+        }
+        __syncwarp();
+        int issued = 0;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % kStages;
+            if (i >= kStages && !wait(KB_EMPTY + s, i / kStages + 1)) break;
+            const int hq = head_of(i), q0 = query_of(i);
+            if (elect_one()) {
+                const uint32_t bar = BAR(KB_FULL + s), st = base + K_OFF_ST + s * STAGE;
+                mbar_expect_tx(bar, 2 * BN * D * 2 + 2 * BN * 4);
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x) {
+                    tma_load_4d(st + x * BOX_N, &tm_q, bar, 64 * x, q0, hq, b);
+                    tma_load_4d(st + TILE_N + x * BOX_N, &tm_do, bar, 64 * x, q0, hq, b);
+                }
+                const size_t row = ((size_t)b * a.Hq + hq) * a.Tp + q0;
+                const uint32_t rows = base + K_OFF_ROW + s * 2 * BN * 4;
+                bulk_load(rows, a.nlse + row, BN * 4, bar);
+                bulk_load(rows + BN * 4, a.ndelta + row, BN * 4, bar);
+            }
+            __syncwarp();
+            issued = i + 1;
+        }
+        if (n > 0) wait_drain(BAR(KB_KV), 0);
+        for (int i = max(0, issued - kStages); i < issued; ++i) wait_drain(BAR(KB_FULL + i % kStages), (i / kStages) & 1);
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false), idesc_g = idesc_bf16_f32(BM, D, true);
+        const uint64_t kdesc = smem_desc_sw128(base + K_OFF_K, 16, 1024), vdesc = smem_desc_sw128(base + K_OFF_V, 16, 1024);
+        const uint64_t sdesc = smem_desc_sw128(base + K_OFF_ST, 16, 1024);      // Q and dO tiles, K-major
+        const uint64_t mdesc = smem_desc_sw128(base + K_OFF_ST, BOX_N, 1024);   // the same, MN-major
+        auto scores = [&](int i) -> bool {
+            const int s = i % kStages;
+            if (!wait(KB_FULL + s, i / kStages)) return false;
+            fence_after_sync();
+            const uint64_t qd = desc_add(sdesc, s * STAGE);
+            const uint32_t ts = tmem + TK_S + BN * (i & 1), td = tmem + TK_DP + BN * (i & 1);
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t m = (kk >> 2) * BOX_M + (kk & 3) * 32, o = (kk >> 2) * BOX_N + (kk & 3) * 32;
+                    mma_ss(ts, desc_add(kdesc, m), desc_add(qd, o), idesc_s, kk > 0 ? 1u : 0u);
+                }
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t m = (kk >> 2) * BOX_M + (kk & 3) * 32, o = (kk >> 2) * BOX_N + (kk & 3) * 32;
+                    mma_ss(td, desc_add(vdesc, m), desc_add(qd, TILE_N + o), idesc_s, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(BAR(KB_SREADY + (i & 1)));
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = n == 0 || wait(KB_KV, 0);
+        for (int i = 0; ok && i < min(n, 2); ++i) ok = scores(i);
+        for (int i = 0; ok && i < n; ++i) {
+            ok = wait(KB_PREADY + (i & 1), i >> 1);
+            if (!ok) break;
+            fence_after_sync();
+            const int s = i % kStages;
+            const uint64_t qd = desc_add(mdesc, s * STAGE);
+            const uint32_t ts = tmem + TK_S + BN * (i & 1), td = tmem + TK_DP + BN * (i & 1);
+            if (elect_one()) {
+                // 16 queries a step: the halves' weights lie 32 columns apart
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    mma_ts(tmem + TK_DV, ts + 32 * (kk >> 1) + 8 * (kk & 1), desc_add(qd, TILE_N + kk * 2048), idesc_g,
+                           i > 0 || kk > 0 ? 1u : 0u);
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    mma_ts(tmem + TK_DK, td + 32 * (kk >> 1) + 8 * (kk & 1), desc_add(qd, kk * 2048), idesc_g,
+                           i > 0 || kk > 0 ? 1u : 0u);
+                mma_commit(BAR(KB_EMPTY + s));
+            }
+            __syncwarp();
+            if (i + 2 < n) ok = scores(i + 2);
+        }
+        if (elect_one()) mma_commit(BAR(KB_DRAIN));
+        __syncwarp();
+        wait_drain(BAR(KB_DRAIN), 0);
+    } else {
+        // ------------------------------------------------ weights, two threads per key
+        const int q4 = warp & 3, half = (warp - 2) >> 2;
+        const int r = q4 * 32 + lane;
+        const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+        const int key = k0 + r, c0 = 32 * half;
+        const float sl2 = a.scale_log2;
+        // the last query that sees the key
+        const int seen = key < a.sinks ? len - 1 : (int)min((long long)len - 1, (long long)key + a.window - 1);
+        const f32x2 sl = mk2(sl2, sl2);
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % kStages, q0 = query_of(i);
+            ok = wait(KB_SREADY + (i & 1), i >> 1) && wait(KB_FULL + s, i / kStages);
+            if (!ok) break;
+            fence_after_sync();
+            if (a.lens && q0 + BN > len) {
+                // queries behind the end: cleared before they are summed over
+                const int x = (int)threadIdx.x - 64, row = x & 63, box = (x >> 6) & 1, which = x >> 7;
+                if (q0 + row >= len && box < D / 64) {
+                    uint4* p = reinterpret_cast<uint4*>(gbase + K_OFF_ST + s * STAGE + which * TILE_N + box * BOX_N + row * 128);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) p[e] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_async();
+                __syncwarp();
+            }
+            const uint32_t ts = trow + TK_S + BN * (i & 1) + c0, td = trow + TK_DP + BN * (i & 1) + c0;
+            uint32_t u[32];
+            tmem_ld32(ts, u);
+            tmem_wait_ld();
+            const float4* nl = reinterpret_cast<const float4*>(gbase + K_OFF_ROW + s * 2 * BN * 4) + c0 / 4;
+            const bool masked = q0 < k0 + BM - 1 || q0 + BN - 1 - k0 >= a.window || q0 + BN > len;
+            const int lo = key - q0 - c0, hi = seen - q0 - c0;  // columns lo .. hi see the key
+            float p[32];
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+                const float4 w = nl[c / 4];
+                un2(fma2(mk2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), sl, mk2(w.x, w.y)), p[c], p[c + 1]);
+                un2(fma2(mk2(__uint_as_float(u[c + 2]), __uint_as_float(u[c + 3])), sl, mk2(w.z, w.w)), p[c + 2], p[c + 3]);
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) p[c] = ex2(p[c]);
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (c < lo || c > hi) p[c] = 0.f;
+            }
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
+            tmem_st<16>(ts, pk);
+            tmem_ld32(td, u);
+            tmem_wait_ld();
+            const float4* nd = nl + BN / 4;
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+                const float4 w = nd[c / 4];
+                const f32x2 d0 = add2(mk2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), mk2(w.x, w.y));
+                const f32x2 d1 = add2(mk2(__uint_as_float(u[c + 2]), __uint_as_float(u[c + 3])), mk2(w.z, w.w));
+                float e0, e1, e2, e3;
+                un2(mul2(d0, mk2(p[c], p[c + 1])), e0, e1);
+                un2(mul2(d1, mk2(p[c + 2], p[c + 3])), e2, e3);
+                if (masked) {  // selected: dP of what nobody sees may be NaN
+                    if (c < lo || c > hi) e0 = 0.f;
+                    if (c + 1 < lo || c + 1 > hi) e1 = 0.f;
+                    if (c + 2 < lo || c + 2 > hi) e2 = 0.f;
+                    if (c + 3 < lo || c + 3 > hi) e3 = 0.f;
+                }
+                pk[c / 2] = pack_bf16(e0, e1);
+                pk[c / 2 + 1] = pack_bf16(e2, e3);
+            }
+            tmem_st<16>(td, pk);
+            tmem_wait_st();
+            fence_before_sync();
+            mbar_arrive(BAR(KB_PREADY + (i & 1)));
+        }
+        if (ok) ok = wait(KB_DRAIN, 0);
+        ok = bar_and(ok && !*abort_flag, 1, kSoftmax);
+        fence_after_sync();
+        const bool parts = a.splits > 0 && J == 0;
+        if (ok && parts) {
+            float* slot = a.part + ((size_t)bh * (1 + a.splits) + (item < a.nt ? 0 : 1 + item - a.nt)) * 2 * BM * D;
+#pragma unroll 1
+            for (int x = 0; x < 2 * (D / 64); ++x) {  // this half's columns of dK, then of dV
+                const int w = x / (D / 64), col = (D / 2) * half + 32 * (x % (D / 64));
+                uint32_t u[32];
+                tmem_ld32(trow + (w ? TK_DV : TK_DK) + col, u);
+                tmem_wait_ld();
+                float4* dst = reinterpret_cast<float4*>(slot + ((size_t)w * BM + r) * D + col);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dst[e] = n > 0 ? make_float4(__uint_as_float(u[4 * e]), __uint_as_float(u[4 * e + 1]),
+                                                 __uint_as_float(u[4 * e + 2]), __uint_as_float(u[4 * e + 3]))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        } else if (!parts) {
+            if (ok) {
+#pragma unroll 1
+                for (int x = 0; x < D / 64; ++x) {  // K and V are used up
+                    const int col = (D / 2) * half + 32 * x;
+                    stage32(trow + TK_DK + col, a.scale, n > 0, gbase + K_OFF_K, col, r);
+                    stage32(trow + TK_DV + col, 1.f, n > 0, gbase + K_OFF_V, col, r);
+                }
+            }
+            fence_async();
+            bar_sync(1, kSoftmax);
+            if (warp == 2 && lane == 0 && ok) {
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x) {
+                    tma_store_4d(&tm_dk, base + K_OFF_K + x * BOX_M, 64 * x, k0, hk, b);
+                    tma_store_4d(&tm_dv, base + K_OFF_V + x * BOX_M, 64 * x, k0, hk, b);
+                }
+                bulk_commit_group();
+                bulk_wait_group_read0();
+            }
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// dk and dv of the first key tile: its parts in order
+template <int D>
+__global__ void __launch_bounds__(256)
+window_sink_kernel(const View dk, const View dv, const BwdArgs a) {
+    const int x = blockIdx.y * 256 + threadIdx.x, r = x / (D / 4), c = 4 * (x % (D / 4));
+    const int w = blockIdx.x & 1, bh = blockIdx.x >> 1, b = bh / a.Hkv, hk = bh % a.Hkv;
+    if (r >= min(BM, a.T)) return;
+    const float* src = a.part + ((size_t)bh * (1 + a.splits) * 2 + w) * BM * D + (size_t)r * D + c;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i <= a.splits; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(src + (size_t)i * 2 * BM * D);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    const float m = w ? 1.f : a.scale;
+    const View& o = w ? dv : dk;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.data) + (size_t)b * o.sb + (size_t)hk * o.sh +
+                              (size_t)r * o.st + c) = make_uint2(pack_bf16(s.x * m, s.y * m), pack_bf16(s.z * m, s.w * m));
+}
+
+// ---------------------------------------------------------------- dQ
+
+constexpr uint32_t Q_OFF_Q = 0, Q_OFF_DO = TILE_M, Q_OFF_K = 2 * TILE_M, Q_OFF_V = Q_OFF_K + 2 * TILE_N;
+constexpr uint32_t Q_OFF_BAR = Q_OFF_V + TILE_N;
+enum : int { QB_Q, QB_KFULL, QB_KEMPTY = QB_KFULL + 2, QB_VFULL = QB_KEMPTY + 2, QB_VEMPTY, QB_SREADY, QB_PREADY, QB_DRAIN, QB_COUNT };
+constexpr uint32_t Q_OFF_MISC = Q_OFF_BAR + QB_COUNT * 8;
+constexpr uint32_t Q_SMEM = Q_OFF_MISC + 16;
+// two CTAs and their 1 KB of system memory each in the SM's 228 KB: no room to
+// round the base up, it is 1024-byte aligned by declaration (and checked)
+static_assert(2 * (Q_SMEM + 1024) <= 233472, "two CTAs per SM");
+constexpr uint32_t TQ_S = 0, TQ_DP = 64, TQ_DQ = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
+                 const __grid_constant__ CUtensorMap tm_dq, const BwdArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem_q[];
+    uint8_t* gbase = smem_q;
+    const uint32_t base = smem_u32(smem_q);
+    if (base & 1023u) {  // not reached: the tiles' swizzle needs the alignment
+        if (threadIdx.x == 0) atomicOr(&g_bwd_status, 2u);
+        return;
+    }
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + Q_OFF_MISC + 4);
+    unsigned int* status = &g_bwd_status;
+    const uint64_t lim = a.timeout_ns;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto BAR = [&](int i) { return base + Q_OFF_BAR + 8u * (uint32_t)i; };
+
+    const int BH = a.B * a.Hq;
+    const int I = a.nt - 1 - (int)(blockIdx.x / BH), bh = (int)(blockIdx.x % BH);
+    const int b = bh / a.Hq, hq = bh % a.Hq, hk = hq / a.G;
+    const int t0 = I * BM, len = seq_len(a, b);
+    int ns = 0, w0 = 0, nt = 0;  // as in the forward: tiles of sinks alone, then those the window reaches
+    if (t0 < len) {
+        const int lo = max(0, t0 - (a.window - 1));
+        w0 = lo / BN;
+        ns = min((a.sinks + BN - 1) / BN, w0);
+        nt = ns + (min(t0 + BM, len) - 1) / BN + 1 - w0;
+    }
+    auto tile_key = [&](int j) { return (j < ns ? j : w0 + j - ns) * BN; };
+    auto tile_keys = [&](int j) { return j < ns ? min(BN, (a.sinks - j * BN + 15) & ~15) : BN; };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < QB_COUNT; ++i) mbar_init(BAR(i), i == QB_PREADY ? kSoftmax : 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(base + Q_OFF_MISC, 256);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<uint32_t*>(gbase + Q_OFF_MISC);
+    const unsigned FULL = 0xffffffffu;
+    auto wait = [&](int bar, uint32_t ph) -> bool {
+        return __all_sync(FULL, mbar_wait(BAR(bar), ph & 1, abort_flag, status, lim));
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (nt > 0 && elect_one()) {
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
+            mbar_expect_tx(BAR(QB_Q), 2 * BM * D * 2);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+                tma_load_4d(base + Q_OFF_Q + x * BOX_M, &tm_q, BAR(QB_Q), 64 * x, t0, hq, b);
+                tma_load_4d(base + Q_OFF_DO + x * BOX_M, &tm_do, BAR(QB_Q), 64 * x, t0, hq, b);
+            }
+        }
+        __syncwarp();
+        auto load = [&](const CUtensorMap* tm, const CUtensorMap* tm16, uint32_t bar, uint32_t dst, int j) {
+            const int s0 = tile_key(j), keys = tile_keys(j);
+            if (elect_one()) {
+                mbar_expect_tx(bar, (uint32_t)keys * D * 2);
+                if (keys < BN) {
+                    for (int r = 0; r < keys; r += 16)
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x) tma_load_4d(dst + x * BOX_N + r * 128, tm16, bar, 64 * x, s0 + r, hk, b);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) tma_load_4d(dst + x * BOX_N, tm, bar, 64 * x, s0, hk, b);
+                }
+            }
+            __syncwarp();
+        };
+        int nk = 0, nv = 0;
+        for (int j = 0; j < nt; ++j) {
+            if (j > 1 && !wait(QB_KEMPTY + (j & 1), (j >> 1) + 1)) break;
+            load(&tm_k, &tm_k16, BAR(QB_KFULL + (j & 1)), base + Q_OFF_K + (j & 1) * TILE_N, j);
+            nk = j + 1;
+            if (j > 0 && !wait(QB_VEMPTY, j - 1)) break;
+            load(&tm_v, &tm_v16, BAR(QB_VFULL), base + Q_OFF_V, j);
+            nv = j + 1;
+        }
+        if (nt > 0) wait_drain(BAR(QB_Q), 0);
+        for (int j = max(0, nk - 2); j < nk; ++j) wait_drain(BAR(QB_KFULL + (j & 1)), (j >> 1) & 1);
+        if (nv > 0) wait_drain(BAR(QB_VFULL), (nv - 1) & 1);
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        constexpr uint32_t idesc_g = idesc_bf16_f32(BM, D, true);
+        const uint64_t qdesc = smem_desc_sw128(base + Q_OFF_Q, 16, 1024), odesc = smem_desc_sw128(base + Q_OFF_DO, 16, 1024);
+        const uint64_t kdesc = smem_desc_sw128(base + Q_OFF_K, 16, 1024), vdesc = smem_desc_sw128(base + Q_OFF_V, 16, 1024);
+        const uint64_t kmdesc = smem_desc_sw128(base + Q_OFF_K, BOX_N, 1024);  // MN-major
+        auto scores = [&](int j) -> bool {  // S and dP, behind the product that reads dS from the columns of S
+            if (!wait(QB_KFULL + (j & 1), j >> 1) || !wait(QB_VFULL, j)) return false;
+            fence_after_sync();
+            const uint32_t idesc_s = idesc_bf16_f32(BM, tile_keys(j), false);
+            const uint64_t kd = desc_add(kdesc, (j & 1) * TILE_N);
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t m = (kk >> 2) * BOX_M + (kk & 3) * 32, o = (kk >> 2) * BOX_N + (kk & 3) * 32;
+                    mma_ss(tmem + TQ_S, desc_add(qdesc, m), desc_add(kd, o), idesc_s, kk > 0 ? 1u : 0u);
+                }
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t m = (kk >> 2) * BOX_M + (kk & 3) * 32, o = (kk >> 2) * BOX_N + (kk & 3) * 32;
+                    mma_ss(tmem + TQ_DP, desc_add(odesc, m), desc_add(vdesc, o), idesc_s, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(BAR(QB_SREADY));
+                mma_commit(BAR(QB_VEMPTY));
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = nt == 0 || (wait(QB_Q, 0) && scores(0));
+        for (int j = 0; ok && j < nt; ++j) {
+            ok = wait(QB_PREADY, j);
+            if (!ok) break;
+            fence_after_sync();
+            const uint64_t kd = desc_add(kmdesc, (j & 1) * TILE_N);
+            const int steps = tile_keys(j) / 16;
+            if (elect_one()) {
+                for (int kk = 0; kk < steps; ++kk)
+                    mma_ts(tmem + TQ_DQ, tmem + TQ_S + 32 * (kk >> 1) + 8 * (kk & 1), desc_add(kd, kk * 2048), idesc_g,
+                           j > 0 || kk > 0 ? 1u : 0u);
+                mma_commit(BAR(QB_KEMPTY + (j & 1)));
+            }
+            __syncwarp();
+            if (j + 1 < nt) ok = scores(j + 1);
+        }
+        if (elect_one()) mma_commit(BAR(QB_DRAIN));
+        __syncwarp();
+        wait_drain(BAR(QB_DRAIN), 0);
+    } else {
+        // ------------------------------------------------ weights, two threads per query
+        const int q4 = warp & 3, half = (warp - 2) >> 2;
+        const int r = q4 * 32 + lane;
+        const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+        const int t = t0 + r, c0 = 32 * half;
+        const size_t row = ((size_t)b * a.Hq + hq) * a.Tp + t;  // (rows are padded to whole tiles)
+        const float nl = a.nlse[row], nd = a.ndelta[row];
+        const f32x2 sl = mk2(a.scale_log2, a.scale_log2), nl2 = mk2(nl, nl), nd2 = mk2(nd, nd);
+        bool ok = true;
+        for (int j = 0; j < nt; ++j) {
+            const int s0 = tile_key(j), keys = tile_keys(j);
+            ok = wait(QB_SREADY, j);
+            if (!ok) break;
+            fence_after_sync();
+            if (a.lens && s0 + BN > len) {
+                // keys behind the end: cleared before they are summed over
+                const int x = (int)threadIdx.x - 64, kr = x & 63, box = x >> 6;
+                if (s0 + kr >= len && box < D / 64) {
+                    uint4* p = reinterpret_cast<uint4*>(gbase + Q_OFF_K + (j & 1) * TILE_N + box * BOX_N + kr * 128);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) p[e] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_async();
+                __syncwarp();
+            }
+            if (c0 < keys) {
+                const uint32_t ts = trow + TQ_S + c0, td = trow + TQ_DP + c0;
+                uint32_t u[32];
+                tmem_ld32(ts, u);
+                tmem_wait_ld();
+                // keys of this half that the row sees: lo <= c <= hi, or a sink c <= sh
+                const bool masked = s0 + BN - 1 > t0 || t0 + BM > len || s0 <= t0 + BM - 1 - a.window;
+                const int hi = t < len ? t - s0 - c0 : -1, lo = max(t - a.window + 1 - s0 - c0, 0);
+                const int sh = min(a.sinks - s0 - c0 - 1, hi);
+                const unsigned span = hi >= lo ? (unsigned)(hi - lo) : 0u;
+                const int off = hi >= lo ? lo : 64;
+                float p[32];
+#pragma unroll
+                for (int c = 0; c < 32; c += 2)
+                    un2(fma2(mk2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), sl, nl2), p[c], p[c + 1]);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) p[c] = ex2(p[c]);
+                tmem_ld32(td, u);
+                tmem_wait_ld();
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    float e0, e1;
+                    un2(mul2(add2(mk2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), nd2), mk2(p[c], p[c + 1])), e0, e1);
+                    if (masked) {
+                        if ((unsigned)(c - off) > span && c > sh) e0 = 0.f;
+                        if ((unsigned)(c + 1 - off) > span && c + 1 > sh) e1 = 0.f;
+                    }
+                    pk[c / 2] = pack_bf16(e0, e1);
+                }
+                tmem_st<16>(ts, pk);
+                tmem_wait_st();
+            }
+            fence_before_sync();
+            mbar_arrive(BAR(QB_PREADY));
+        }
+        if (ok) ok = wait(QB_DRAIN, 0);
+        ok = bar_and(ok && !*abort_flag, 1, kSoftmax);
+        fence_after_sync();
+        if (ok) {
+#pragma unroll 1
+            for (int x = 0; x < D / 64; ++x) {  // the queries are used up
+                const int col = (D / 2) * half + 32 * x;
+                stage32(trow + TQ_DQ + col, a.scale, nt > 0 && t < len, gbase + Q_OFF_Q, col, r);
+            }
+        }
+        fence_async();
+        bar_sync(1, kSoftmax);
+        if (warp == 2 && lane == 0 && ok) {
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) tma_store_4d(&tm_dq, base + Q_OFF_Q + x * BOX_M, 64 * x, t0, hq, b);
+            bulk_commit_group();
+            bulk_wait_group_read0();
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after_sync();
+        tmem_dealloc(tmem, 256);
+    }
+}
+
+// Shape of a call: padded rows, reach and stretches of the first key tile.
+struct Plan {
+    int window, sinks, nt, Tp, splits;
+    size_t rows, bytes;
+};
+Plan plan_of(const ssa_window_params_t& p) {
+    Plan x{};
+    x.window = p.window > 0 && p.window < p.T ? p.window : p.T;
+    x.sinks = x.window < p.T ? (p.sinks < p.T ? p.sinks : p.T) : 0;
+    x.nt = (p.T + BM - 1) / BM;
+    x.Tp = x.nt * BM;
+    const long long last = (p.T - 1) / BN, reach = ((long long)BM - 1 + x.window - 1) / BN;
+    if (x.sinks > 0 && last > reach) {
+        // a stretch of queries as long as a key tile's usual list, 32 tiles at least, 64 stretches at most
+        const long long usual = reach + 1 > 32 ? reach + 1 : 32, far = last - reach;
+        const long long n = (far + usual - 1) / usual;
+        x.splits = (int)(n < 64 ? n : 64);
+    }
+    x.rows = align_up((size_t)p.B * p.Hq * x.Tp * sizeof(float), 256);
+    x.bytes = 2 * x.rows;
+    if (x.splits) x.bytes += align_up((size_t)p.B * p.Hkv * (1 + x.splits) * 2 * BM * p.D * sizeof(float), 256);
+    return x;
+}
+
+template <int D>
+int run(const ssa_window_params_t& p, const View& q, const View& k, const View& v, const View& h, const float* lse,
+        const View& dh, const View& dq, const View& dk, const View& dv, BwdArgs a, cudaStream_t s) {
+    int st = opt_in_max_smem<window_dkdv_kernel<D>>("window_dkdv_kernel");
+    if (st == SSA_OK) st = opt_in_max_smem<window_dq_kernel<D>>("window_dq_kernel");
+    CUtensorMap q64, do64, k128, v128, mdk, mdv, q128, do128, k64, v64, k16, v16, mdq;
+    struct { CUtensorMap* m; const View* x; int H, rows; } maps[] = {
+        {&q64, &q, p.Hq, BN}, {&do64, &dh, p.Hq, BN}, {&k128, &k, p.Hkv, BM}, {&v128, &v, p.Hkv, BM},
+        {&mdk, &dk, p.Hkv, BM}, {&mdv, &dv, p.Hkv, BM}, {&q128, &q, p.Hq, BM}, {&do128, &dh, p.Hq, BM},
+        {&k64, &k, p.Hkv, BN}, {&v64, &v, p.Hkv, BN}, {&k16, &k, p.Hkv, 16}, {&v16, &v, p.Hkv, 16},
+        {&mdq, &dq, p.Hq, BM}};
+    for (const auto& m : maps)
+        if (st == SSA_OK) st = make_view_map(m.m, *m.x, D, p.T, m.H, p.B, m.rows);
+    if (st != SSA_OK) return st;
+    constexpr int rows = 256 / (D / 8);
+    window_rows_kernel<D><<<dim3((unsigned)(a.Tp / rows), (unsigned)p.Hq, (unsigned)p.B), 256, 0, s>>>(
+        h, dh, lse, const_cast<float*>(a.nlse), const_cast<float*>(a.ndelta), a);
+    const unsigned items = (unsigned)p.B * p.Hkv * (a.nt + a.splits);
+    window_dkdv_kernel<D><<<items, kThreads, K_SMEM, s>>>(q64, do64, k128, v128, mdk, mdv, a);
+    if (a.splits)
+        window_sink_kernel<D><<<dim3(2u * p.B * p.Hkv, (unsigned)(BM * D / 4 / 256)), 256, 0, s>>>(dk, dv, a);
+    window_dq_kernel<D><<<(unsigned)p.B * p.Hq * a.nt, kThreads, Q_SMEM, s>>>(q128, do128, k64, v64, k16, v16, mdq, a);
+    return check_launch("window backward (tensor cores)");
+}
+
+}  // namespace
+
+bool window_bwd_tc_supported(const ssa_window_params_t& p) {
+    return window_tc_supported(p) && (long long)p.B * p.Hq * ((p.T + BM - 1) / BM + 64) <= 0x7fffffffll;
+}
+
+size_t window_bwd_tc_workspace(const ssa_window_params_t& p) { return plan_of(p).bytes; }
+
+int launch_window_bwd_tc(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
+                         const int32_t* lens, const View& h, const float* lse, const View& dh, const View& dq,
+                         const View& dk, const View& dv, void* ws, cudaStream_t s) {
+    const Plan x = plan_of(p);
+    BwdArgs a{};
+    a.lens = lens;
+    a.nlse = static_cast<float*>(ws);
+    a.ndelta = reinterpret_cast<float*>(static_cast<char*>(ws) + x.rows);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * x.rows);
+    a.B = p.B, a.Hq = p.Hq, a.Hkv = p.Hkv, a.G = p.Hq / p.Hkv, a.T = p.T, a.Tp = x.Tp;
+    a.window = x.window, a.sinks = x.sinks, a.nt = x.nt, a.splits = x.splits;
+    a.scale = p.sm_scale, a.scale_log2 = p.sm_scale * kLog2e;
+    a.timeout_ns = wait_limit_ns();
+    return p.D == 64 ? run<64>(p, q, k, v, h, lse, dh, dq, dk, dv, a, s)
+                     : run<128>(p, q, k, v, h, lse, dh, dq, dk, dv, a, s);
+}
+
+int window_bwd_take_status() {
+    unsigned int v = 0, w = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_bwd_status, sizeof v);
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&w, g_bwd_range, sizeof w);
+    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
+    const unsigned int zero = 0;
+    if (v) {
+        cudaMemcpyToSymbol(g_bwd_status, &zero, sizeof zero);
+        return v & 1u ? fail(SSA_ERR_TIMEOUT, "window backward: a bounded mbarrier wait expired")
+                      : fail(SSA_ERR_CUDA, "window_dq_kernel: shared memory is not aligned");
+    }
+    if (w) {
+        cudaMemcpyToSymbol(g_bwd_range, &zero, sizeof zero);
+        return fail(SSA_ERR_INVALID_ARG, "window attention: a length was out of range");
+    }
+    return SSA_OK;
+}
+
+}  // namespace ssa
