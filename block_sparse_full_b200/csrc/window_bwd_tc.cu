@@ -26,13 +26,16 @@
 // tile i are, the two products into dK and dV of tile i while those of tile
 // i+1 are.  P^T and dS^T go back to TMEM as bf16 (over the scores) and are the A
 // operands, Q and dO tiles (used K-major for the scores) the MN-major B
-// operands.  Eight softmax warps, two threads per key with 32 queries each.
+// operands.  Sixteen softmax warps in two groups that take turns on the tiles, two
+// threads per key with 32 queries each (one group left the tensor cores
+// waiting: 651 us against XXX us at T = 4096, window 1024, 32/8 heads, batch 4).
 // A 128-key tile that holds sinks is seen by every later query; the queries
 // past the window's reach are split into stretches of about a CTA's usual
 // work, whose float32 parts are summed in order by window_sink_kernel.
 //
 // dQ: 256 TMEM columns (S 64, dP 64, dQ 128) and 112 KB, so two CTAs share the SM
-// and take turns on the tensor cores.
+// and take turns on the tensor cores.  dS goes over dP, so that the next S is
+// formed as soon as the softmax has read the last (573 us -> YYY us).
 //
 // Rows and keys behind a sequence's length may be NaN: weights are selected, not
 // multiplied, to zero, and such rows of a tile are cleared in shared memory
@@ -52,6 +55,7 @@ using namespace tc;
 constexpr int BM = 128;  // rows of a CTA's tile
 constexpr int BN = 64;   // rows of a tile that it walks
 constexpr int kThreads = 320, kSoftmax = 256;
+constexpr int kThreadsK = 576;  // dK/dV: two groups of softmax warps
 constexpr uint32_t BOX_M = BM * 128, BOX_N = BN * 128;  // boxes of 64 columns
 constexpr uint32_t TILE_M = 2 * BOX_M, TILE_N = 2 * BOX_N;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -160,7 +164,7 @@ static_assert(K_SMEM <= kMaxSmemPerCta, "shared memory");
 constexpr uint32_t TK_S = 0, TK_DP = 128, TK_DK = 256, TK_DV = 384;
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsK, 1)
 window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
@@ -311,7 +315,7 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         wait_drain(BAR(KB_DRAIN), 0);
     } else {
         // ------------------------------------------------ weights, two threads per key
-        const int q4 = warp & 3, half = (warp - 2) >> 2;
+        const int q4 = warp & 3, half = ((warp - 2) >> 2) & 1, group = (warp - 2) >> 3;
         const int r = q4 * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
         const int key = k0 + r, c0 = 32 * half;
@@ -320,14 +324,14 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int seen = key < a.sinks ? len - 1 : (int)min((long long)len - 1, (long long)key + a.window - 1);
         const f32x2 sl = mk2(sl2, sl2);
         bool ok = true;
-        for (int i = 0; i < n; ++i) {
+        for (int i = group; i < n; i += 2) {
             const int s = i % kStages, q0 = query_of(i);
             ok = wait(KB_SREADY + (i & 1), i >> 1) && wait(KB_FULL + s, i / kStages);
             if (!ok) break;
             fence_after_sync();
             if (a.lens && q0 + BN > len) {
                 // queries behind the end: cleared before they are summed over
-                const int x = (int)threadIdx.x - 64, row = x & 63, box = (x >> 6) & 1, which = x >> 7;
+                const int x = ((int)threadIdx.x - 64) & 255, row = x & 63, box = (x >> 6) & 1, which = x >> 7;
                 if (q0 + row >= len && box < D / 64) {
                     uint4* p = reinterpret_cast<uint4*>(gbase + K_OFF_ST + s * STAGE + which * TILE_N + box * BOX_N + row * 128);
 #pragma unroll
@@ -387,14 +391,14 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_arrive(BAR(KB_PREADY + (i & 1)));
         }
         if (ok) ok = wait(KB_DRAIN, 0);
-        ok = bar_and(ok && !*abort_flag, 1, kSoftmax);
+        ok = bar_and(ok && !*abort_flag, 1, 2 * kSoftmax);
         fence_after_sync();
         const bool parts = a.splits > 0 && J == 0;
         if (ok && parts) {
             float* slot = a.part + ((size_t)bh * (1 + a.splits) + (item < a.nt ? 0 : 1 + item - a.nt)) * 2 * BM * D;
 #pragma unroll 1
-            for (int x = 0; x < 2 * (D / 64); ++x) {  // this half's columns of dK, then of dV
-                const int w = x / (D / 64), col = (D / 2) * half + 32 * (x % (D / 64));
+            for (int x = 0; x < D / 64; ++x) {  // this half's columns of dK (group 0) or dV
+                const int w = group, col = (D / 2) * half + 32 * x;
                 uint32_t u[32];
                 tmem_ld32(trow + (w ? TK_DV : TK_DK) + col, u);
                 tmem_wait_ld();
@@ -408,14 +412,14 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         } else if (!parts) {
             if (ok) {
 #pragma unroll 1
-                for (int x = 0; x < D / 64; ++x) {  // K and V are used up
+                for (int x = 0; x < D / 64; ++x) {  // K and V are used up; a group each for dK and dV
                     const int col = (D / 2) * half + 32 * x;
-                    stage32(trow + TK_DK + col, a.scale, n > 0, gbase + K_OFF_K, col, r);
-                    stage32(trow + TK_DV + col, 1.f, n > 0, gbase + K_OFF_V, col, r);
+                    stage32(trow + (group ? TK_DV : TK_DK) + col, group ? 1.f : a.scale, n > 0,
+                            gbase + (group ? K_OFF_V : K_OFF_K), col, r);
                 }
             }
             fence_async();
-            bar_sync(1, kSoftmax);
+            bar_sync(1, 2 * kSoftmax);
             if (warp == 2 && lane == 0 && ok) {
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x) {
@@ -459,7 +463,7 @@ window_sink_kernel(const View dk, const View dv, const BwdArgs a) {
 
 constexpr uint32_t Q_OFF_Q = 0, Q_OFF_DO = TILE_M, Q_OFF_K = 2 * TILE_M, Q_OFF_V = Q_OFF_K + 2 * TILE_N;
 constexpr uint32_t Q_OFF_BAR = Q_OFF_V + TILE_N;
-enum : int { QB_Q, QB_KFULL, QB_KEMPTY = QB_KFULL + 2, QB_VFULL = QB_KEMPTY + 2, QB_VEMPTY, QB_SREADY, QB_PREADY, QB_DRAIN, QB_COUNT };
+enum : int { QB_Q, QB_KFULL, QB_KEMPTY = QB_KFULL + 2, QB_VFULL = QB_KEMPTY + 2, QB_VEMPTY, QB_SREADY, QB_SFREE, QB_PREADY, QB_DRAIN, QB_COUNT };
 constexpr uint32_t Q_OFF_MISC = Q_OFF_BAR + QB_COUNT * 8;
 constexpr uint32_t Q_SMEM = Q_OFF_MISC + 16;
 // two CTAs and their 1 KB of system memory each in the SM's 228 KB: no room to
@@ -501,7 +505,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     auto tile_keys = [&](int j) { return j < ns ? min(BN, (a.sinks - j * BN + 15) & ~15) : BN; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < QB_COUNT; ++i) mbar_init(BAR(i), i == QB_PREADY ? kSoftmax : 1);
+        for (int i = 0; i < QB_COUNT; ++i) mbar_init(BAR(i), i == QB_PREADY || i == QB_SFREE ? kSoftmax : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -564,30 +568,38 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint64_t qdesc = smem_desc_sw128(base + Q_OFF_Q, 16, 1024), odesc = smem_desc_sw128(base + Q_OFF_DO, 16, 1024);
         const uint64_t kdesc = smem_desc_sw128(base + Q_OFF_K, 16, 1024), vdesc = smem_desc_sw128(base + Q_OFF_V, 16, 1024);
         const uint64_t kmdesc = smem_desc_sw128(base + Q_OFF_K, BOX_N, 1024);  // MN-major
-        auto scores = [&](int j) -> bool {  // S and dP, behind the product that reads dS from the columns of S
-            if (!wait(QB_KFULL + (j & 1), j >> 1) || !wait(QB_VFULL, j)) return false;
+        auto product = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc) {  // 128 x keys over D
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t m = (kk >> 2) * BOX_M + (kk & 3) * 32, o = (kk >> 2) * BOX_N + (kk & 3) * 32;
+                mma_ss(d, desc_add(ad, m), desc_add(bd, o), idesc, kk > 0 ? 1u : 0u);
+            }
+        };
+        auto scores = [&](int j) -> bool {  // S = Q K_j^T
+            if (!wait(QB_KFULL + (j & 1), j >> 1)) return false;
             fence_after_sync();
-            const uint32_t idesc_s = idesc_bf16_f32(BM, tile_keys(j), false);
-            const uint64_t kd = desc_add(kdesc, (j & 1) * TILE_N);
+            if (elect_one())
+                product(tmem + TQ_S, qdesc, desc_add(kdesc, (j & 1) * TILE_N), idesc_bf16_f32(BM, tile_keys(j), false));
+            __syncwarp();
+            return true;
+        };
+        auto values = [&](int j) -> bool {  // dP = dO V_j^T, behind the product that reads dS from its columns
+            if (!wait(QB_VFULL, j)) return false;
+            fence_after_sync();
             if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t m = (kk >> 2) * BOX_M + (kk & 3) * 32, o = (kk >> 2) * BOX_N + (kk & 3) * 32;
-                    mma_ss(tmem + TQ_S, desc_add(qdesc, m), desc_add(kd, o), idesc_s, kk > 0 ? 1u : 0u);
-                }
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t m = (kk >> 2) * BOX_M + (kk & 3) * 32, o = (kk >> 2) * BOX_N + (kk & 3) * 32;
-                    mma_ss(tmem + TQ_DP, desc_add(odesc, m), desc_add(vdesc, o), idesc_s, kk > 0 ? 1u : 0u);
-                }
+                product(tmem + TQ_DP, odesc, vdesc, idesc_bf16_f32(BM, tile_keys(j), false));
                 mma_commit(BAR(QB_SREADY));
                 mma_commit(BAR(QB_VEMPTY));
             }
             __syncwarp();
             return true;
         };
-        bool ok = nt == 0 || (wait(QB_Q, 0) && scores(0));
+        bool ok = nt == 0 || (wait(QB_Q, 0) && scores(0) && values(0));
         for (int j = 0; ok && j < nt; ++j) {
+            if (j + 1 < nt) {  // the scores have been read: the next ones while dS is formed
+                ok = wait(QB_SFREE, j) && scores(j + 1);
+                if (!ok) break;
+            }
             ok = wait(QB_PREADY, j);
             if (!ok) break;
             fence_after_sync();
@@ -595,12 +607,12 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const int steps = tile_keys(j) / 16;
             if (elect_one()) {
                 for (int kk = 0; kk < steps; ++kk)
-                    mma_ts(tmem + TQ_DQ, tmem + TQ_S + 32 * (kk >> 1) + 8 * (kk & 1), desc_add(kd, kk * 2048), idesc_g,
+                    mma_ts(tmem + TQ_DQ, tmem + TQ_DP + 32 * (kk >> 1) + 8 * (kk & 1), desc_add(kd, kk * 2048), idesc_g,
                            j > 0 || kk > 0 ? 1u : 0u);
                 mma_commit(BAR(QB_KEMPTY + (j & 1)));
             }
             __syncwarp();
-            if (j + 1 < nt) ok = scores(j + 1);
+            if (j + 1 < nt) ok = values(j + 1);
         }
         if (elect_one()) mma_commit(BAR(QB_DRAIN));
         __syncwarp();
@@ -631,11 +643,15 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 fence_async();
                 __syncwarp();
             }
+            uint32_t u[32];
             if (c0 < keys) {
-                const uint32_t ts = trow + TQ_S + c0, td = trow + TQ_DP + c0;
-                uint32_t u[32];
-                tmem_ld32(ts, u);
+                tmem_ld32(trow + TQ_S + c0, u);
                 tmem_wait_ld();
+            }
+            fence_before_sync();
+            mbar_arrive(BAR(QB_SFREE));
+            if (c0 < keys) {
+                const uint32_t td = trow + TQ_DP + c0;
                 // keys of this half that the row sees: lo <= c <= hi, or a sink c <= sh
                 const bool masked = s0 + BN - 1 > t0 || t0 + BM > len || s0 <= t0 + BM - 1 - a.window;
                 const int hi = t < len ? t - s0 - c0 : -1, lo = max(t - a.window + 1 - s0 - c0, 0);
@@ -661,7 +677,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     }
                     pk[c / 2] = pack_bf16(e0, e1);
                 }
-                tmem_st<16>(ts, pk);
+                tmem_st<16>(td, pk);
                 tmem_wait_st();
             }
             fence_before_sync();
@@ -736,7 +752,7 @@ int run(const ssa_window_params_t& p, const View& q, const View& k, const View& 
     window_rows_kernel<D><<<dim3((unsigned)(a.Tp / rows), (unsigned)p.Hq, (unsigned)p.B), 256, 0, s>>>(
         h, dh, lse, const_cast<float*>(a.nlse), const_cast<float*>(a.ndelta), a);
     const unsigned items = (unsigned)p.B * p.Hkv * (a.nt + a.splits);
-    window_dkdv_kernel<D><<<items, kThreads, K_SMEM, s>>>(q64, do64, k128, v128, mdk, mdv, a);
+    window_dkdv_kernel<D><<<items, kThreadsK, K_SMEM, s>>>(q64, do64, k128, v128, mdk, mdv, a);
     if (a.splits)
         window_sink_kernel<D><<<dim3(2u * p.B * p.Hkv, (unsigned)(BM * D / 4 / 256)), 256, 0, s>>>(dk, dv, a);
     window_dq_kernel<D><<<(unsigned)p.B * p.Hq * a.nt, kThreads, Q_SMEM, s>>>(q128, do128, k64, v64, k16, v16, mdq, a);
