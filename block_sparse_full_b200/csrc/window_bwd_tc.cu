@@ -9,7 +9,7 @@
 //   window_rows_kernel   -lse log2 e and -delta of every row, padded to whole
 //                        tiles: one pass over dO and h, bound by reading them
 //   window_dkdv_kernel   a CTA per key tile of 128 and key/value head walks the
-//                        query tiles of 64 that see it, for each query head of
+//                        query tiles of 128 that see it, for each query head of
 //                        its group in turn: four products per tile
 //   window_dq_kernel     a CTA per query tile of 128 walks the key tiles of 64:
 //                        three products per tile
@@ -20,15 +20,19 @@
 // it again (at T = 4096, window 1024, 128 heads 2.4 GB, 0.37 ms, against two
 // products of 0.1 ms each).
 //
-// dK/dV: S^T = K Q^T and dP^T = V dO^T (M = 128 keys, N = 64 queries) land in two
-// TMEM buffers each (256 columns), dK and dV take the other 256 (D = 128), so
-// one CTA fills the SM: the scores of tile i+1 are formed while the weights of
-// tile i are, the two products into dK and dV of tile i while those of tile
-// i+1 are.  P^T and dS^T go back to TMEM as bf16 (over the scores) and are the A
+// dK/dV: S^T = K Q^T, dP^T = V dO^T (M = 128 keys, N = 128 queries), dK and dV take
+// all 512 TMEM columns (D = 128), so one CTA fills the SM and its four products
+// are ordered so that each runs beside a part of the softmax that does not
+// need it:
+//     tensor cores   dK_i-1   dP_i    | dV_i     S_i+1    | dK_i ...
+//     softmax        P_i = 2^(S_i ..) | dS_i = P_i (dP_i ..) | P_i+1 ...
+// P^T and dS^T go back to TMEM as bf16 (over the scores) and are the A
 // operands, Q and dO tiles (used K-major for the scores) the MN-major B
-// operands.  Sixteen softmax warps in two groups that take turns on the tiles, two
-// threads per key with 32 queries each (one group left the tensor cores
-// waiting: 651 us against XXX us at T = 4096, window 1024, 32/8 heads, batch 4).
+// operands.  Sixteen softmax warps, four threads per key with 32 queries each.
+// Tiles of 64 queries in two TMEM buffers instead overlap as well on paper,
+// but read K and V from shared memory twice as often, and shared memory then
+// is what bounds them: XXX us against YYY us at T = 4096, window 1024, 32/8
+// heads, batch 4.
 // A 128-key tile that holds sinks is seen by every later query; the queries
 // past the window's reach are split into stretches of about a CTA's usual
 // work, whose float32 parts are summed in order by window_sink_kernel.
@@ -55,7 +59,7 @@ using namespace tc;
 constexpr int BM = 128;  // rows of a CTA's tile
 constexpr int BN = 64;   // rows of a tile that it walks
 constexpr int kThreads = 320, kSoftmax = 256;
-constexpr int kThreadsK = 576;  // dK/dV: two groups of softmax warps
+constexpr int kThreadsK = 640, kSoftmaxK = 512;  // dK/dV: four warps of roles, sixteen softmax warps
 constexpr uint32_t BOX_M = BM * 128, BOX_N = BN * 128;  // boxes of 64 columns
 constexpr uint32_t TILE_M = 2 * BOX_M, TILE_N = 2 * BOX_N;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -152,12 +156,12 @@ window_rows_kernel(const View h, const View dh, const float* lse, float* nlse, f
 
 // ---------------------------------------------------------------- dK, dV
 
-constexpr int kStages = 3;
-constexpr uint32_t STAGE = 2 * TILE_N;  // Q, dO
-constexpr uint32_t K_OFF_K = 0, K_OFF_V = TILE_M, K_OFF_ST = 2 * TILE_M, K_OFF_ROW = K_OFF_ST + kStages * STAGE;
-constexpr uint32_t K_OFF_BAR = K_OFF_ROW + kStages * 2 * BN * 4;  // nlse, ndelta of a tile's 64 queries
-enum : int { KB_KV, KB_FULL, KB_EMPTY = KB_FULL + kStages, KB_SREADY = KB_EMPTY + kStages, KB_PREADY = KB_SREADY + 2,
-             KB_DRAIN = KB_PREADY + 2, KB_COUNT };
+// Two slots of 128 queries each for Q (with the row values) and dO.
+constexpr uint32_t K_OFF_K = 0, K_OFF_V = TILE_M, K_OFF_Q = 2 * TILE_M, K_OFF_DO = 4 * TILE_M;
+constexpr uint32_t K_OFF_ROW = 6 * TILE_M, ROWS = 2 * BM * 4;  // nlse, ndelta of a Q tile's queries
+constexpr uint32_t K_OFF_BAR = K_OFF_ROW + 2 * ROWS;
+enum : int { KB_KV, KB_QFULL, KB_QEMPTY = KB_QFULL + 2, KB_OFULL = KB_QEMPTY + 2, KB_OEMPTY = KB_OFULL + 2,
+             KB_SREADY = KB_OEMPTY + 2, KB_DPREADY, KB_PREADY, KB_DSREADY, KB_DRAIN, KB_COUNT };
 constexpr uint32_t K_OFF_MISC = K_OFF_BAR + KB_COUNT * 8;
 constexpr uint32_t K_SMEM = K_OFF_MISC + 16 + 1024;
 static_assert(K_SMEM <= kMaxSmemPerCta, "shared memory");
@@ -186,9 +190,9 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int J = item < a.nt ? item : 0;
     const int k0 = J * BM;
     const int len = seq_len(a, b);
-    const int last = (len - 1) / BN;  // last query tile (len 0: none, below)
-    const int reach = (int)min((long long)last, ((long long)k0 + BM - 1 + a.window - 1) / BN);
-    int q_first = k0 / BN, q_count, i0 = 0, i1;
+    const int last = (len - 1) / BM;  // last query tile (len 0: none, below)
+    const int reach = (int)min((long long)last, ((long long)k0 + BM - 1 + a.window - 1) / BM);
+    int q_first = J, q_count, i0 = 0, i1;
     if (item < a.nt) {
         q_count = k0 < len ? reach - q_first + 1 : 0;
         i1 = a.G * q_count;
@@ -202,10 +206,10 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     const int n = i1 - i0;
     auto head_of = [&](int i) { return hk * a.G + (i0 + i) / q_count; };
-    auto query_of = [&](int i) { return (q_first + (i0 + i) % q_count) * BN; };
+    auto query_of = [&](int i) { return (q_first + (i0 + i) % q_count) * BM; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < KB_COUNT; ++i) mbar_init(BAR(i), i >= KB_PREADY && i < KB_DRAIN ? kSoftmax : 1);
+        for (int i = 0; i < KB_COUNT; ++i) mbar_init(BAR(i), i == KB_PREADY || i == KB_DSREADY ? kSoftmaxK : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -222,11 +226,35 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         return __all_sync(FULL, mbar_wait(BAR(bar), ph & 1, abort_flag, status, lim));
     };
 
+    // Loads the tiles of one ring (with Q the row values too); the copies in flight
+    // land before the CTA ends, also where a wait gave up.
+    auto ring = [&](int full, int empty, const CUtensorMap* tm, uint32_t off, bool rows) {
+        int issued = 0;
+        for (int i = 0; i < n; ++i) {
+            const int s = i & 1;
+            if (i >= 2 && !wait(empty + s, (i >> 1) + 1)) break;
+            const int hq = head_of(i), q0 = query_of(i);
+            if (elect_one()) {
+                const uint32_t bar = BAR(full + s), dst = base + off + s * TILE_M;
+                mbar_expect_tx(bar, BM * D * 2 + (rows ? ROWS : 0));
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x) tma_load_4d(dst + x * BOX_M, tm, bar, 64 * x, q0, hq, b);
+                if (rows) {
+                    const size_t row = ((size_t)b * a.Hq + hq) * a.Tp + q0;
+                    bulk_load(base + K_OFF_ROW + s * ROWS, a.nlse + row, BM * 4, bar);
+                    bulk_load(base + K_OFF_ROW + s * ROWS + BM * 4, a.ndelta + row, BM * 4, bar);
+                }
+            }
+            __syncwarp();
+            issued = i + 1;
+        }
+        for (int i = max(0, issued - 2); i < issued; ++i) wait_drain(BAR(full + (i & 1)), (i >> 1) & 1);
+    };
+
     if (warp == 0) {
-        // ------------------------------------------------ TMA producer
+        // ------------------------------------------------ K, V and the ring of Q
         if (n > 0 && elect_one()) {
             prefetch_tmap(&tm_q);
-            prefetch_tmap(&tm_do);
             mbar_expect_tx(BAR(KB_KV), 2 * BM * D * 2);
 #pragma unroll
             for (int x = 0; x < D / 64; ++x) {
@@ -235,117 +263,110 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         }
         __syncwarp();
-        int issued = 0;
-        for (int i = 0; i < n; ++i) {
-            const int s = i % kStages;
-            if (i >= kStages && !wait(KB_EMPTY + s, i / kStages + 1)) break;
-            const int hq = head_of(i), q0 = query_of(i);
-            if (elect_one()) {
-                const uint32_t bar = BAR(KB_FULL + s), st = base + K_OFF_ST + s * STAGE;
-                mbar_expect_tx(bar, 2 * BN * D * 2 + 2 * BN * 4);
-#pragma unroll
-                for (int x = 0; x < D / 64; ++x) {
-                    tma_load_4d(st + x * BOX_N, &tm_q, bar, 64 * x, q0, hq, b);
-                    tma_load_4d(st + TILE_N + x * BOX_N, &tm_do, bar, 64 * x, q0, hq, b);
-                }
-                const size_t row = ((size_t)b * a.Hq + hq) * a.Tp + q0;
-                const uint32_t rows = base + K_OFF_ROW + s * 2 * BN * 4;
-                bulk_load(rows, a.nlse + row, BN * 4, bar);
-                bulk_load(rows + BN * 4, a.ndelta + row, BN * 4, bar);
-            }
-            __syncwarp();
-            issued = i + 1;
-        }
+        ring(KB_QFULL, KB_QEMPTY, &tm_q, K_OFF_Q, true);
         if (n > 0) wait_drain(BAR(KB_KV), 0);
-        for (int i = max(0, issued - kStages); i < issued; ++i) wait_drain(BAR(KB_FULL + i % kStages), (i / kStages) & 1);
+    } else if (warp == 2) {
+        // ------------------------------------------------ the ring of dO
+        ring(KB_OFULL, KB_OEMPTY, &tm_do, K_OFF_DO, false);
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false), idesc_g = idesc_bf16_f32(BM, D, true);
+        constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BM, false), idesc_g = idesc_bf16_f32(BM, D, true);
         const uint64_t kdesc = smem_desc_sw128(base + K_OFF_K, 16, 1024), vdesc = smem_desc_sw128(base + K_OFF_V, 16, 1024);
-        const uint64_t sdesc = smem_desc_sw128(base + K_OFF_ST, 16, 1024);      // Q and dO tiles, K-major
-        const uint64_t mdesc = smem_desc_sw128(base + K_OFF_ST, BOX_N, 1024);   // the same, MN-major
-        auto scores = [&](int i) -> bool {
-            const int s = i % kStages;
-            if (!wait(KB_FULL + s, i / kStages)) return false;
+        // Q and dO tiles, K-major for the scores and MN-major for the gradients
+        const uint64_t qdesc = smem_desc_sw128(base + K_OFF_Q, 16, 1024), odesc = smem_desc_sw128(base + K_OFF_DO, 16, 1024);
+        const uint64_t qmdesc = smem_desc_sw128(base + K_OFF_Q, BOX_M, 1024), omdesc = smem_desc_sw128(base + K_OFF_DO, BOX_M, 1024);
+        auto product = [&](uint32_t d, uint64_t ad, uint64_t bd) {  // 128 keys x 128 queries over D
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t o = (kk >> 2) * BOX_M + (kk & 3) * 32;
+                mma_ss(d, desc_add(ad, o), desc_add(bd, o), idesc_s, kk > 0 ? 1u : 0u);
+            }
+        };
+        auto gradient = [&](uint32_t d, uint32_t w, uint64_t bd, int i) {  // 128 keys x D over 128 queries
+#pragma unroll
+            for (int kk = 0; kk < BM / 16; ++kk)  // the quarters' weights lie 32 columns apart
+                mma_ts(d, w + 32 * (kk >> 1) + 8 * (kk & 1), desc_add(bd, kk * 2048), idesc_g, i > 0 || kk > 0 ? 1u : 0u);
+        };
+        auto scores = [&](int i) -> bool {  // S^T, behind the product that reads P from its columns
+            if (!wait(KB_QFULL + (i & 1), i >> 1)) return false;
             fence_after_sync();
-            const uint64_t qd = desc_add(sdesc, s * STAGE);
-            const uint32_t ts = tmem + TK_S + BN * (i & 1), td = tmem + TK_DP + BN * (i & 1);
             if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t m = (kk >> 2) * BOX_M + (kk & 3) * 32, o = (kk >> 2) * BOX_N + (kk & 3) * 32;
-                    mma_ss(ts, desc_add(kdesc, m), desc_add(qd, o), idesc_s, kk > 0 ? 1u : 0u);
-                }
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t m = (kk >> 2) * BOX_M + (kk & 3) * 32, o = (kk >> 2) * BOX_N + (kk & 3) * 32;
-                    mma_ss(td, desc_add(vdesc, m), desc_add(qd, TILE_N + o), idesc_s, kk > 0 ? 1u : 0u);
-                }
-                mma_commit(BAR(KB_SREADY + (i & 1)));
+                product(tmem + TK_S, kdesc, desc_add(qdesc, (i & 1) * TILE_M));
+                mma_commit(BAR(KB_SREADY));
             }
             __syncwarp();
             return true;
         };
-        bool ok = n == 0 || wait(KB_KV, 0);
-        for (int i = 0; ok && i < min(n, 2); ++i) ok = scores(i);
-        for (int i = 0; ok && i < n; ++i) {
-            ok = wait(KB_PREADY + (i & 1), i >> 1);
-            if (!ok) break;
+        auto values = [&](int i) -> bool {  // dP^T, behind the product that reads dS from its columns
+            if (!wait(KB_OFULL + (i & 1), i >> 1)) return false;
             fence_after_sync();
-            const int s = i % kStages;
-            const uint64_t qd = desc_add(mdesc, s * STAGE);
-            const uint32_t ts = tmem + TK_S + BN * (i & 1), td = tmem + TK_DP + BN * (i & 1);
             if (elect_one()) {
-                // 16 queries a step: the halves' weights lie 32 columns apart
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                    mma_ts(tmem + TK_DV, ts + 32 * (kk >> 1) + 8 * (kk & 1), desc_add(qd, TILE_N + kk * 2048), idesc_g,
-                           i > 0 || kk > 0 ? 1u : 0u);
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                    mma_ts(tmem + TK_DK, td + 32 * (kk >> 1) + 8 * (kk & 1), desc_add(qd, kk * 2048), idesc_g,
-                           i > 0 || kk > 0 ? 1u : 0u);
-                mma_commit(BAR(KB_EMPTY + s));
+                product(tmem + TK_DP, vdesc, desc_add(odesc, (i & 1) * TILE_M));
+                mma_commit(BAR(KB_DPREADY));
             }
             __syncwarp();
-            if (i + 2 < n) ok = scores(i + 2);
+            return true;
+        };
+        bool ok = n == 0 || (wait(KB_KV, 0) && scores(0) && values(0));
+        for (int i = 0; ok && i < n; ++i) {
+            ok = wait(KB_PREADY, i);
+            if (!ok) break;
+            fence_after_sync();
+            if (elect_one()) {
+                gradient(tmem + TK_DV, tmem + TK_S, desc_add(omdesc, (i & 1) * TILE_M), i);
+                mma_commit(BAR(KB_OEMPTY + (i & 1)));
+            }
+            __syncwarp();
+            if (i + 1 < n) ok = scores(i + 1);
+            ok = ok && wait(KB_DSREADY, i);
+            if (!ok) break;
+            fence_after_sync();
+            if (elect_one()) {
+                gradient(tmem + TK_DK, tmem + TK_DP, desc_add(qmdesc, (i & 1) * TILE_M), i);
+                mma_commit(BAR(KB_QEMPTY + (i & 1)));
+            }
+            __syncwarp();
+            if (i + 1 < n) ok = values(i + 1);
         }
         if (elect_one()) mma_commit(BAR(KB_DRAIN));
         __syncwarp();
         wait_drain(BAR(KB_DRAIN), 0);
-    } else {
-        // ------------------------------------------------ weights, two threads per key
-        const int q4 = warp & 3, half = ((warp - 2) >> 2) & 1, group = (warp - 2) >> 3;
+    } else if (warp >= 4) {
+        // ------------------------------------------------ weights, four threads per key
+        const int q4 = warp & 3, part = (warp - 4) >> 2;  // the warp's TMEM lanes; its quarter of the queries
         const int r = q4 * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
-        const int key = k0 + r, c0 = 32 * half;
+        const int key = k0 + r, c0 = 32 * part;
         const float sl2 = a.scale_log2;
         // the last query that sees the key
         const int seen = key < a.sinks ? len - 1 : (int)min((long long)len - 1, (long long)key + a.window - 1);
         const f32x2 sl = mk2(sl2, sl2);
         bool ok = true;
-        for (int i = group; i < n; i += 2) {
-            const int s = i % kStages, q0 = query_of(i);
-            ok = wait(KB_SREADY + (i & 1), i >> 1) && wait(KB_FULL + s, i / kStages);
+        for (int i = 0; i < n; ++i) {
+            const int q0 = query_of(i);
+            ok = wait(KB_SREADY, i) && wait(KB_QFULL + (i & 1), i >> 1);
             if (!ok) break;
             fence_after_sync();
-            if (a.lens && q0 + BN > len) {
+            if (a.lens && q0 + BM > len) {
                 // queries behind the end: cleared before they are summed over
-                const int x = ((int)threadIdx.x - 64) & 255, row = x & 63, box = (x >> 6) & 1, which = x >> 7;
+                ok = wait(KB_OFULL + (i & 1), i >> 1);
+                if (!ok) break;
+                const int x = (int)threadIdx.x - 128, row = x & 127, box = (x >> 7) & 1;
                 if (q0 + row >= len && box < D / 64) {
-                    uint4* p = reinterpret_cast<uint4*>(gbase + K_OFF_ST + s * STAGE + which * TILE_N + box * BOX_N + row * 128);
+                    uint8_t* tile = gbase + (x >> 8 ? K_OFF_DO : K_OFF_Q) + (i & 1) * TILE_M;
+                    uint4* p = reinterpret_cast<uint4*>(tile + box * BOX_M + row * 128);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) p[e] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_async();
                 __syncwarp();
             }
-            const uint32_t ts = trow + TK_S + BN * (i & 1) + c0, td = trow + TK_DP + BN * (i & 1) + c0;
+            const uint32_t ts = trow + TK_S + c0, td = trow + TK_DP + c0;
             uint32_t u[32];
             tmem_ld32(ts, u);
             tmem_wait_ld();
-            const float4* nl = reinterpret_cast<const float4*>(gbase + K_OFF_ROW + s * 2 * BN * 4) + c0 / 4;
-            const bool masked = q0 < k0 + BM - 1 || q0 + BN - 1 - k0 >= a.window || q0 + BN > len;
+            const float4* nl = reinterpret_cast<const float4*>(gbase + K_OFF_ROW + (i & 1) * ROWS) + c0 / 4;
+            const bool masked = q0 < k0 + BM - 1 || q0 + BM - 1 - k0 >= a.window || q0 + BM > len;
             const int lo = key - q0 - c0, hi = seen - q0 - c0;  // columns lo .. hi see the key
             float p[32];
 #pragma unroll
@@ -365,9 +386,15 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
             for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
             tmem_st<16>(ts, pk);
+            tmem_wait_st();
+            fence_before_sync();
+            mbar_arrive(BAR(KB_PREADY));
+            ok = wait(KB_DPREADY, i);
+            if (!ok) break;
+            fence_after_sync();
             tmem_ld32(td, u);
             tmem_wait_ld();
-            const float4* nd = nl + BN / 4;
+            const float4* nd = nl + BM / 4;
 #pragma unroll
             for (int c = 0; c < 32; c += 4) {
                 const float4 w = nd[c / 4];
@@ -388,17 +415,17 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tmem_st<16>(td, pk);
             tmem_wait_st();
             fence_before_sync();
-            mbar_arrive(BAR(KB_PREADY + (i & 1)));
+            mbar_arrive(BAR(KB_DSREADY));
         }
         if (ok) ok = wait(KB_DRAIN, 0);
-        ok = bar_and(ok && !*abort_flag, 1, 2 * kSoftmax);
+        ok = bar_and(ok && !*abort_flag, 1, kSoftmaxK);
         fence_after_sync();
         const bool parts = a.splits > 0 && J == 0;
         if (ok && parts) {
             float* slot = a.part + ((size_t)bh * (1 + a.splits) + (item < a.nt ? 0 : 1 + item - a.nt)) * 2 * BM * D;
 #pragma unroll 1
-            for (int x = 0; x < D / 64; ++x) {  // this half's columns of dK (group 0) or dV
-                const int w = group, col = (D / 2) * half + 32 * x;
+            for (int x = 0; x < D / 64; ++x) {  // two parts for dK, two for dV
+                const int w = part >> 1, col = (D / 2) * (part & 1) + 32 * x;
                 uint32_t u[32];
                 tmem_ld32(trow + (w ? TK_DV : TK_DK) + col, u);
                 tmem_wait_ld();
@@ -412,15 +439,15 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         } else if (!parts) {
             if (ok) {
 #pragma unroll 1
-                for (int x = 0; x < D / 64; ++x) {  // K and V are used up; a group each for dK and dV
-                    const int col = (D / 2) * half + 32 * x;
-                    stage32(trow + (group ? TK_DV : TK_DK) + col, group ? 1.f : a.scale, n > 0,
-                            gbase + (group ? K_OFF_V : K_OFF_K), col, r);
+                for (int x = 0; x < D / 64; ++x) {  // K and V are used up
+                    const int w = part >> 1, col = (D / 2) * (part & 1) + 32 * x;
+                    stage32(trow + (w ? TK_DV : TK_DK) + col, w ? 1.f : a.scale, n > 0, gbase + (w ? K_OFF_V : K_OFF_K),
+                            col, r);
                 }
             }
             fence_async();
-            bar_sync(1, 2 * kSoftmax);
-            if (warp == 2 && lane == 0 && ok) {
+            bar_sync(1, kSoftmaxK);
+            if (warp == 4 && lane == 0 && ok) {
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x) {
                     tma_store_4d(&tm_dk, base + K_OFF_K + x * BOX_M, 64 * x, k0, hk, b);
@@ -463,7 +490,7 @@ window_sink_kernel(const View dk, const View dv, const BwdArgs a) {
 
 constexpr uint32_t Q_OFF_Q = 0, Q_OFF_DO = TILE_M, Q_OFF_K = 2 * TILE_M, Q_OFF_V = Q_OFF_K + 2 * TILE_N;
 constexpr uint32_t Q_OFF_BAR = Q_OFF_V + TILE_N;
-enum : int { QB_Q, QB_KFULL, QB_KEMPTY = QB_KFULL + 2, QB_VFULL = QB_KEMPTY + 2, QB_VEMPTY, QB_SREADY, QB_SFREE, QB_PREADY, QB_DRAIN, QB_COUNT };
+enum : int { QB_Q, QB_KFULL, QB_KEMPTY = QB_KFULL + 2, QB_VFULL = QB_KEMPTY + 2, QB_VEMPTY, QB_SREADY, QB_DPREADY, QB_SFREE, QB_DSREADY, QB_DRAIN, QB_COUNT };
 constexpr uint32_t Q_OFF_MISC = Q_OFF_BAR + QB_COUNT * 8;
 constexpr uint32_t Q_SMEM = Q_OFF_MISC + 16;
 // two CTAs and their 1 KB of system memory each in the SM's 228 KB: no room to
@@ -505,7 +532,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     auto tile_keys = [&](int j) { return j < ns ? min(BN, (a.sinks - j * BN + 15) & ~15) : BN; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < QB_COUNT; ++i) mbar_init(BAR(i), i == QB_PREADY || i == QB_SFREE ? kSoftmax : 1);
+        for (int i = 0; i < QB_COUNT; ++i) mbar_init(BAR(i), i == QB_DSREADY || i == QB_SFREE ? kSoftmax : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -578,8 +605,10 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         auto scores = [&](int j) -> bool {  // S = Q K_j^T
             if (!wait(QB_KFULL + (j & 1), j >> 1)) return false;
             fence_after_sync();
-            if (elect_one())
+            if (elect_one()) {
                 product(tmem + TQ_S, qdesc, desc_add(kdesc, (j & 1) * TILE_N), idesc_bf16_f32(BM, tile_keys(j), false));
+                mma_commit(BAR(QB_SREADY));
+            }
             __syncwarp();
             return true;
         };
@@ -588,7 +617,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             fence_after_sync();
             if (elect_one()) {
                 product(tmem + TQ_DP, odesc, vdesc, idesc_bf16_f32(BM, tile_keys(j), false));
-                mma_commit(BAR(QB_SREADY));
+                mma_commit(BAR(QB_DPREADY));
                 mma_commit(BAR(QB_VEMPTY));
             }
             __syncwarp();
@@ -600,7 +629,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 ok = wait(QB_SFREE, j) && scores(j + 1);
                 if (!ok) break;
             }
-            ok = wait(QB_PREADY, j);
+            ok = wait(QB_DSREADY, j);
             if (!ok) break;
             fence_after_sync();
             const uint64_t kd = desc_add(kmdesc, (j & 1) * TILE_N);
@@ -664,6 +693,9 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     un2(fma2(mk2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), sl, nl2), p[c], p[c + 1]);
 #pragma unroll
                 for (int c = 0; c < 32; ++c) p[c] = ex2(p[c]);
+                ok = wait(QB_DPREADY, j);
+                if (!ok) break;
+                fence_after_sync();
                 tmem_ld32(td, u);
                 tmem_wait_ld();
                 uint32_t pk[16];
@@ -679,9 +711,14 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 tmem_st<16>(td, pk);
                 tmem_wait_st();
+            } else {
+                // nothing of the tile is here, but an arrival before the barrier's
+                // phase has begun would count for the tile before
+                ok = wait(QB_DPREADY, j);
+                if (!ok) break;
             }
             fence_before_sync();
-            mbar_arrive(BAR(QB_PREADY));
+            mbar_arrive(BAR(QB_DSREADY));
         }
         if (ok) ok = wait(QB_DRAIN, 0);
         ok = bar_and(ok && !*abort_flag, 1, kSoftmax);
@@ -721,10 +758,10 @@ Plan plan_of(const ssa_window_params_t& p) {
     x.sinks = x.window < p.T ? (p.sinks < p.T ? p.sinks : p.T) : 0;
     x.nt = (p.T + BM - 1) / BM;
     x.Tp = x.nt * BM;
-    const long long last = (p.T - 1) / BN, reach = ((long long)BM - 1 + x.window - 1) / BN;
+    const long long last = (p.T - 1) / BM, reach = ((long long)BM - 1 + x.window - 1) / BM;
     if (x.sinks > 0 && last > reach) {
-        // a stretch of queries as long as a key tile's usual list, 32 tiles at least, 64 stretches at most
-        const long long usual = reach + 1 > 32 ? reach + 1 : 32, far = last - reach;
+        // a stretch of queries as long as a key tile's usual list, 16 tiles at least, 64 stretches at most
+        const long long usual = reach + 1 > 16 ? reach + 1 : 16, far = last - reach;
         const long long n = (far + usual - 1) / usual;
         x.splits = (int)(n < 64 ? n : 64);
     }
@@ -739,9 +776,9 @@ int run(const ssa_window_params_t& p, const View& q, const View& k, const View& 
         const View& dh, const View& dq, const View& dk, const View& dv, BwdArgs a, cudaStream_t s) {
     int st = opt_in_max_smem<window_dkdv_kernel<D>>("window_dkdv_kernel");
     if (st == SSA_OK) st = opt_in_max_smem<window_dq_kernel<D>>("window_dq_kernel");
-    CUtensorMap q64, do64, k128, v128, mdk, mdv, q128, do128, k64, v64, k16, v16, mdq;
+    CUtensorMap k128, v128, mdk, mdv, q128, do128, k64, v64, k16, v16, mdq;
     struct { CUtensorMap* m; const View* x; int H, rows; } maps[] = {
-        {&q64, &q, p.Hq, BN}, {&do64, &dh, p.Hq, BN}, {&k128, &k, p.Hkv, BM}, {&v128, &v, p.Hkv, BM},
+        {&k128, &k, p.Hkv, BM}, {&v128, &v, p.Hkv, BM},
         {&mdk, &dk, p.Hkv, BM}, {&mdv, &dv, p.Hkv, BM}, {&q128, &q, p.Hq, BM}, {&do128, &dh, p.Hq, BM},
         {&k64, &k, p.Hkv, BN}, {&v64, &v, p.Hkv, BN}, {&k16, &k, p.Hkv, 16}, {&v16, &v, p.Hkv, 16},
         {&mdq, &dq, p.Hq, BM}};
@@ -752,7 +789,7 @@ int run(const ssa_window_params_t& p, const View& q, const View& k, const View& 
     window_rows_kernel<D><<<dim3((unsigned)(a.Tp / rows), (unsigned)p.Hq, (unsigned)p.B), 256, 0, s>>>(
         h, dh, lse, const_cast<float*>(a.nlse), const_cast<float*>(a.ndelta), a);
     const unsigned items = (unsigned)p.B * p.Hkv * (a.nt + a.splits);
-    window_dkdv_kernel<D><<<items, kThreadsK, K_SMEM, s>>>(q64, do64, k128, v128, mdk, mdv, a);
+    window_dkdv_kernel<D><<<items, kThreadsK, K_SMEM, s>>>(q128, do128, k128, v128, mdk, mdv, a);
     if (a.splits)
         window_sink_kernel<D><<<dim3(2u * p.B * p.Hkv, (unsigned)(BM * D / 4 / 256)), 256, 0, s>>>(dk, dv, a);
     window_dq_kernel<D><<<(unsigned)p.B * p.Hq * a.nt, kThreads, Q_SMEM, s>>>(q128, do128, k64, v64, k16, v16, mdq, a);

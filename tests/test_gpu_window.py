@@ -71,6 +71,8 @@ SHAPES = [
     (1, 2, 1, 1030, 128, 1, 4),
     (1, 1, 1, 1300, 128, 1000, 128),
     (1, 2, 1, 515, 64, 4096, 4),
+    (2, 4, 2, 900, 128, 130, 80),  # the sinks' second tile is a 16-row step
+    (1, 2, 1, 2500, 64, 40, 97),
 ]
 
 
