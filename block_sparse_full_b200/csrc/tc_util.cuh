@@ -381,6 +381,13 @@ __device__ __forceinline__ void stage_row_cols(uint32_t trow_col, float mul, uin
     }
 }
 
+// Bits lo .. hi of a word (either end may lie outside it; none if hi < lo).
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+    uint32_t m = lo <= 0 ? 0xffffffffu : lo > 31 ? 0u : 0xffffffffu << lo;
+    m &= hi >= 31 ? 0xffffffffu : hi < 0 ? 0u : 0xffffffffu >> (31 - hi);
+    return m;
+}
+
 // ---------------------------------------------------------------- packed f32x2
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 mk2(float a, float b) {

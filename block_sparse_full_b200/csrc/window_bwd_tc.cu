@@ -366,23 +366,29 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tmem_ld32(ts, u);
             tmem_wait_ld();
             const float4* nl = reinterpret_cast<const float4*>(gbase + K_OFF_ROW + (i & 1) * ROWS) + c0 / 4;
+            // the queries of this quarter that see the key
             const bool masked = q0 < k0 + BM - 1 || q0 + BM - 1 - k0 >= a.window || q0 + BM > len;
-            const int lo = key - q0 - c0, hi = seen - q0 - c0;  // columns lo .. hi see the key
+            const uint32_t bits = masked ? bit_range(key - q0 - c0, seen - q0 - c0) : 0xffffffffu;
             float p[32];
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-                const float4 w = nl[c / 4];
-                un2(fma2(mk2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), sl, mk2(w.x, w.y)), p[c], p[c + 1]);
-                un2(fma2(mk2(__uint_as_float(u[c + 2]), __uint_as_float(u[c + 3])), sl, mk2(w.z, w.w)), p[c + 2], p[c + 3]);
-            }
-#pragma unroll
-            for (int c = 0; c < 32; ++c) p[c] = ex2(p[c]);
-            if (masked) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (c < lo || c > hi) p[c] = 0.f;
-            }
             uint32_t pk[16];
+            if (__any_sync(FULL, bits != 0)) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                    const float4 w = nl[c / 4];
+                    un2(fma2(mk2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), sl, mk2(w.x, w.y)), p[c], p[c + 1]);
+                    un2(fma2(mk2(__uint_as_float(u[c + 2]), __uint_as_float(u[c + 3])), sl, mk2(w.z, w.w)), p[c + 2], p[c + 3]);
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) p[c] = ex2(p[c]);
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!(bits >> c & 1u)) p[c] = 0.f;
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) p[c] = 0.f;
+            }
 #pragma unroll
             for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
             tmem_st<16>(ts, pk);
@@ -395,6 +401,7 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tmem_ld32(td, u);
             tmem_wait_ld();
             const float4* nd = nl + BM / 4;
+            const bool tail = a.lens && (q0 + BM > len || k0 + BM > len);
 #pragma unroll
             for (int c = 0; c < 32; c += 4) {
                 const float4 w = nd[c / 4];
@@ -403,11 +410,11 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 float e0, e1, e2, e3;
                 un2(mul2(d0, mk2(p[c], p[c + 1])), e0, e1);
                 un2(mul2(d1, mk2(p[c + 2], p[c + 3])), e2, e3);
-                if (masked) {  // selected: dP of what nobody sees may be NaN
-                    if (c < lo || c > hi) e0 = 0.f;
-                    if (c + 1 < lo || c + 1 > hi) e1 = 0.f;
-                    if (c + 2 < lo || c + 2 > hi) e2 = 0.f;
-                    if (c + 3 < lo || c + 3 > hi) e3 = 0.f;
+                if (tail) {  // selected: dP of rows behind the end may be NaN (elsewhere a masked P of 0 does it)
+                    if (!(bits >> c & 1u)) e0 = 0.f;
+                    if (!(bits >> (c + 1) & 1u)) e1 = 0.f;
+                    if (!(bits >> (c + 2) & 1u)) e2 = 0.f;
+                    if (!(bits >> (c + 3) & 1u)) e3 = 0.f;
                 }
                 pk[c / 2] = pack_bf16(e0, e1);
                 pk[c / 2 + 1] = pack_bf16(e2, e3);
@@ -681,12 +688,13 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_arrive(BAR(QB_SFREE));
             if (c0 < keys) {
                 const uint32_t td = trow + TQ_DP + c0;
-                // keys of this half that the row sees: lo <= c <= hi, or a sink c <= sh
+                // keys of this half that the row sees: the window's, or a sink
                 const bool masked = s0 + BN - 1 > t0 || t0 + BM > len || s0 <= t0 + BM - 1 - a.window;
-                const int hi = t < len ? t - s0 - c0 : -1, lo = max(t - a.window + 1 - s0 - c0, 0);
-                const int sh = min(a.sinks - s0 - c0 - 1, hi);
-                const unsigned span = hi >= lo ? (unsigned)(hi - lo) : 0u;
-                const int off = hi >= lo ? lo : 64;
+                uint32_t bits = 0xffffffffu;
+                if (masked) {
+                    const int hi = t < len ? t - s0 - c0 : -1;
+                    bits = bit_range(t - a.window + 1 - s0 - c0, hi) | bit_range(0, min(a.sinks - s0 - c0 - 1, hi));
+                }
                 float p[32];
 #pragma unroll
                 for (int c = 0; c < 32; c += 2)
@@ -704,8 +712,8 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     float e0, e1;
                     un2(mul2(add2(mk2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), nd2), mk2(p[c], p[c + 1])), e0, e1);
                     if (masked) {
-                        if ((unsigned)(c - off) > span && c > sh) e0 = 0.f;
-                        if ((unsigned)(c + 1 - off) > span && c + 1 > sh) e1 = 0.f;
+                        if (!(bits >> c & 1u)) e0 = 0.f;
+                        if (!(bits >> (c + 1) & 1u)) e1 = 0.f;
                     }
                     pk[c / 2] = pack_bf16(e0, e1);
                 }

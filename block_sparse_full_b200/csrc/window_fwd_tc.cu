@@ -377,26 +377,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                     for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(u0[c]), s[32 + c] = __uint_as_float(u1[c]);
                 }
-                // keys of this tile that the row sees: lo <= c <= hi, or a sink c <= sh
-                if constexpr (kPrefix) {
-                    if (end < BN) {
+                // keys of this tile that the row sees: the window's, or a sink
+                if (kPrefix ? end < BN : s0 + BN - 1 > t0 || end < BN || s0 <= t0 + BM - 1 - a.window) {
 #pragma unroll
-                        for (int c = 0; c < BN; ++c)
-                            if (c >= end) s[c] = -INFINITY;
-                    }
-                } else if (s0 + BN - 1 > t0 || end < BN || s0 <= t0 + BM - 1 - a.window) {
-                    const int hi = min(t, len - 1) - s0, lo = max(t - a.window + 1 - s0, 0);
-                    const unsigned span = hi >= lo ? (unsigned)(hi - lo) : 0u;
-                    const int off = hi >= lo ? lo : BN;  // an empty range lies past the tile
-                    const int sh = min(a.sinks - s0 - 1, hi);
-                    if (a.sinks <= s0) {
+                    for (int c0 = 0; c0 < BN; c0 += 32) {
+                        uint32_t bits;
+                        if constexpr (kPrefix) {
+                            bits = bit_range(0, end - 1 - c0);
+                        } else {
+                            const int hi = min(t, len - 1) - s0 - c0;
+                            bits = bit_range(t - a.window + 1 - s0 - c0, hi) | bit_range(0, min(a.sinks - s0 - c0 - 1, hi));
+                        }
 #pragma unroll
-                        for (int c = 0; c < BN; ++c)
-                            if ((unsigned)(c - off) > span) s[c] = -INFINITY;
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < BN; ++c)
-                            if ((unsigned)(c - off) > span && c > sh) s[c] = -INFINITY;
+                        for (int c = 0; c < 32; ++c)
+                            if (!(bits >> c & 1u)) s[c0 + c] = -INFINITY;
                     }
                 }
                 float mx4[4];
