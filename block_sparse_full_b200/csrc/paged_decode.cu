@@ -159,6 +159,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// Programmatic launches: the kernels of a call may overlap where they do not
+// depend on one another.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // A place in the list of units.
 struct Cursor {
     int b, hr, t;
@@ -434,9 +439,13 @@ decode_kernel(const DecodeArgs a, const Pass p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int HR = a.Hkv * p.RT;
 
+    launch_dependents();  // every CTA is on its SM: the next kernel's may come in beside them
     const long long total = tiles_before(p, p.nseq, TK) * HR;
     const int C = used_ctas(total, p.C);
-    if ((int)blockIdx.x >= C) return;
+    if ((int)blockIdx.x >= C) {
+        wait_for_previous();
+        return;
+    }
     const long long ubeg = stretch(total, C, blockIdx.x), uend = stretch(total, C, blockIdx.x + 1);
 
     // the place of unit ubeg: the sequence by a warp-wide scan
@@ -459,7 +468,10 @@ decode_kernel(const DecodeArgs a, const Pass p) {
                 before += __shfl_sync(0xffffffffu, inc - n, __ffs(in) - 1);
             } else {
                 before += __shfl_sync(0xffffffffu, inc, 31);
-                if (b0 + 32 >= p.nseq) return;  // cannot be: ubeg < total
+                if (b0 + 32 >= p.nseq) {  // cannot be: ubeg < total
+                    wait_for_previous();
+                    return;
+                }
             }
         }
         ld.b = found;
@@ -604,6 +616,9 @@ decode_kernel(const DecodeArgs a, const Pass p) {
         advance(cu);
     }
     cp_wait<0>();
+    // The pass over a shared prefix may still be running beside this one; the join
+    // waits for this kernel only, so this kernel ends after it.
+    wait_for_previous();
 }
 
 // Where the partials of a row lie: n slots, one from every CTA c0 .. c0 + n - 1,
@@ -629,20 +644,29 @@ struct PrefixTc {
     int splits, ntq, nb;
 };
 
-// Joins the partials of the rows (one warp each) of one sequence and head.
-// pre: the pass over the shared prefix (nseq = 0: none), or ptc.
+// Joins the partials of the rows of one sequence and head.  pre: the pass over
+// the shared prefix (nseq = 0: none), or ptc.  Few rows leave several of the eight
+// warps to each: they take its partials in turn and are joined in order.
+constexpr int kJoinWarps = 8;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(32 * kJoinWarps)
 join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int TK = Tile<T>::keys, E = D / 32;  // outputs per lane
     constexpr size_t kSlot = (size_t)kRows * (D + 2);
-    const int b = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 31;
+    __shared__ float2 ml_of[kJoinWarps];
+    __shared__ float o_of[kJoinWarps][D];
+    const int b = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int HR = a.Hkv * p.RT;
+    const int per = a.G >= 5 ? 1 : a.G >= 3 ? 2 : a.G == 2 ? 4 : 8;  // warps of a row
+    const int sub = warp % per;
+    // the lengths were there before the passes began: the lists are laid out while they still run
     const Seen s = seen_tiles(p, seq_len(p, b), TK);
     const long long before = tiles_before(p, b, TK);
     const long long total = tiles_before(p, p.nseq, TK) * HR;
-    for (int g = threadIdx.x >> 5; g < a.G; g += blockDim.x >> 5) {
+    for (int g0 = 0; g0 < a.G; g0 += kJoinWarps / per) {
+        const int g = min(g0 + warp / per, a.G - 1);
+        const bool row = g0 + warp / per < a.G;
         // own partials: a first one, then every `step` floats; then the prefix's likewise
         const float *own0 = nullptr, *own1 = nullptr, *pre0 = nullptr, *pre1 = nullptr;
         int n_own = 0, n_pre = 0, pr = 0, prows = kRows;
@@ -656,10 +680,10 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc
             own1 = p.part + x.rest * kSlot;
         }
         if (pre.nseq > 0) {
-            const int row = b * a.G + g, hr = h * pre.RT + row / kRows;
+            const int prow = b * a.G + g, hr = h * pre.RT + prow / kRows;
             const Seen ps = seen_tiles(pre, pre.fixed_len, TK);
             const long long ptotal = (long long)ps.nt * a.Hkv * pre.RT;
-            pr = row % kRows;
+            pr = prow % kRows;
             const Parts x = parts_of(pre, ptotal, (long long)hr * ps.nt, (long long)(hr + 1) * ps.nt, 2 * (size_t)pre.C + hr);
             n_pre = x.n;
             pre0 = pre.part + x.first * kSlot;
@@ -670,45 +694,70 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc
             n_pre = ptc.splits;
             pstep = (size_t)128 * (D + 2);
             pre0 = pre1 = ptc.part + (size_t)(h * ptc.ntq + b / ptc.nb) * ptc.splits * pstep;
-        } else if (n_own == 1) {
-            continue;  // written by the pass itself
         }
-        const int np = n_own + n_pre;
+        const bool written = n_pre == 0 && n_own == 1;  // by the pass itself
+        const int np = row && !written ? n_own + n_pre : 0;
         auto part = [&](int i) -> const float* {
             if (i < n_own) return i == 0 ? own0 : own1 + i * (2 * kSlot);
             i -= n_own;
             return i == 0 ? pre0 : pre1 + i * pstep;
         };
-        auto sums = [&](int i) -> float2 {  // (maximum, sum)
-            const float* x = part(i) + (i < n_own ? kRows * D + 2 * r : prows * D + 2 * pr);
-            return *reinterpret_cast<const float2*>(x);
-        };
-        float M = -INFINITY;
-        for (int i = lane; i < np; i += 32) M = fmaxf(M, sums(i).x);
-        M = warp_max(M);
-        float L = 0.f, acc[E];
+        wait_for_previous();
+        // this warp's partials sub, sub + per, ..: 32 at a time, a lane holding one's (maximum, sum)
+        float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        for (int i0 = 0; i0 < np; i0 += 32) {
-            float w = 0.f;
-            if (i0 + lane < np) {
-                const float2 ml = sums(i0 + lane);
-                w = ml.x == -INFINITY ? 0.f : ex2f(ml.x - M);
-                L += w * ml.y;
+        const int mine = (np - sub + per - 1) / per;
+        for (int i0 = 0; i0 < mine; i0 += 32) {
+            const int m = min(32, mine - i0);
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (lane < m) {
+                const int i = sub + (i0 + lane) * per;
+                ml = *reinterpret_cast<const float2*>(part(i) + (i < n_own ? kRows * D + 2 * r : prows * D + 2 * pr));
             }
-            const int m = min(32, np - i0);
+            const float up = fmaxf(M, warp_max(ml.x));
+            if (up == -INFINITY) continue;  // nothing was seen
+            const float al = ex2f(M - up), w = ex2f(ml.x - up);
+            M = up;
+            L = L * al + warp_sum(w * ml.y);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= al;
 #pragma unroll 8
-            for (int i = 0; i < m; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                const float* src = part(i0 + i) + (i0 + i < n_own ? r : pr) * D + E * lane;
+            for (int k = 0; k < m; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+                const int i = sub + (i0 + k) * per;
+                const float* src = part(i) + (i < n_own ? r : pr) * D + E * lane;
                 float x[E];
                 if constexpr (E == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
                 else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, x[e], acc[e]);
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, x[e], acc[e]);
             }
         }
-        L = warp_sum(L);
+        if (per > 1) {
+            __syncthreads();
+            if (lane == 0) ml_of[warp] = make_float2(M, L);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o_of[warp][E * lane + e] = acc[e];
+            __syncthreads();
+            if (sub == 0) {
+                float up = M;
+                for (int k = 1; k < per; ++k) up = fmaxf(up, ml_of[warp + k].x);
+                const float al = M == -INFINITY ? 0.f : ex2f(M - up);
+                L *= al;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] *= al;
+                for (int k = 1; k < per; ++k) {
+                    const float2 ml = ml_of[warp + k];
+                    const float w = ml.x == -INFINITY ? 0.f : ex2f(ml.x - up);
+                    L = fmaf(w, ml.y, L);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, o_of[warp + k][E * lane + e], acc[e]);
+                }
+                M = up;
+            }
+        }
+        if (!row || written || sub != 0) continue;
         const float inv = L > 0.f ? 1.f / L : 0.f;
         T* dst = static_cast<T*>(a.h.data) + (size_t)b * a.h.sb + (size_t)(h * a.G + g) * a.h.sh + E * lane;
         if constexpr (sizeof(T) == 2) {
@@ -726,38 +775,51 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc
 
 constexpr int kCtas = 296;  // two CTAs on each of 148 SMs
 
-template <typename T, int D, int RG>
-int launch_pass(const DecodeArgs& a, const Pass& p, cudaStream_t s) {
-    const int st = opt_in_max_smem<decode_kernel<T, D, RG>>("decode_kernel");
-    if (st != SSA_OK) return st;
-    decode_kernel<T, D, RG><<<p.C, kThreads, decode_smem<T, D>(), s>>>(a, p);
-    return check_launch("decode_kernel");
-}
-template <typename T, int D>
-int run_pass(const DecodeArgs& a, const Pass& p, cudaStream_t s) {
-    if constexpr (sizeof(T) == 4)  // few rows: fewer registers and products per key
-        if (p.R <= 4) return launch_pass<T, D, 4>(a, p, s);
-    return launch_pass<T, D, kRows>(a, p, s);
-}
-
-template <typename T, int D>
-int run(const DecodeArgs& a, const Pass& own, const Pass& pre, const PrefixTc& ptc, cudaStream_t s) {
-    int st = SSA_OK;
-    if (pre.nseq) st = run_pass<T, D>(a, pre, s);
-    if (st == SSA_OK) st = run_pass<T, D>(a, own, s);
-    if (st != SSA_OK) return st;
+// Launch that may begin while the kernel before it in the stream still runs.
+template <typename... Params, typename... Args>
+int launch_beside(const char* what, void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                  const Args&... args) {
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)a.Hkv, (unsigned)a.B);
-    c.blockDim = dim3((unsigned)(32 * (a.G < 4 ? a.G : 4)));
+    c.gridDim = grid;
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
     c.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     c.attrs = &at;
     c.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&c, join_kernel<T, D>, a, own, pre, ptc);
-    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "join_kernel: %s", cudaGetErrorString(e));
-    return check_launch("join_kernel");
+    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
+    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return check_launch(what);
+}
+
+template <typename T, int D, int RG>
+int launch_pass(const DecodeArgs& a, const Pass& p, bool beside, cudaStream_t s) {
+    const int st = opt_in_max_smem<decode_kernel<T, D, RG>>("decode_kernel");
+    if (st != SSA_OK) return st;
+    if (beside)
+        return launch_beside("decode_kernel", decode_kernel<T, D, RG>, dim3((unsigned)p.C), kThreads, decode_smem<T, D>(),
+                             s, a, p);
+    decode_kernel<T, D, RG><<<p.C, kThreads, decode_smem<T, D>(), s>>>(a, p);
+    return check_launch("decode_kernel");
+}
+template <typename T, int D>
+int run_pass(const DecodeArgs& a, const Pass& p, bool beside, cudaStream_t s) {
+    if constexpr (sizeof(T) == 4)  // few rows: fewer registers and products per key
+        if (p.R <= 4) return launch_pass<T, D, 4>(a, p, beside, s);
+    return launch_pass<T, D, kRows>(a, p, beside, s);
+}
+
+template <typename T, int D>
+int run(const DecodeArgs& a, const Pass& own, const Pass& pre, const PrefixTc& ptc, cudaStream_t s) {
+    int st = SSA_OK;
+    if (pre.nseq) st = run_pass<T, D>(a, pre, false, s);
+    // the sequences' own pages do not wait for the prefix (the kernel ends after it, though)
+    if (st == SSA_OK) st = run_pass<T, D>(a, own, pre.nseq || ptc.splits, s);
+    if (st != SSA_OK) return st;
+    return launch_beside("join_kernel", join_kernel<T, D>, dim3((unsigned)a.Hkv, (unsigned)a.B), 32 * kJoinWarps, 0, s, a,
+                         own, pre, ptc);
 }
 
 int tile_keys(const ssa_cache_params_t& p) { return p.dtype == SSA_BF16 ? 64 : 32; }

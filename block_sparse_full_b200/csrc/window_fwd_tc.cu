@@ -166,6 +166,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
+    if constexpr (kPrefix) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = *reinterpret_cast<uint32_t*>(gbase + OFF_MISC);
     const unsigned FULL = 0xffffffffu;
 

@@ -22,6 +22,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_uint, c_void_p
 
 import torch
@@ -535,82 +536,91 @@ _I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
 _TORCH_DT = {SSA_F32: torch.float32, SSA_BF16: torch.bfloat16}
 
 
-def _view(t, name, shape, dtype, device):
-    """ssa_view_t of a tensor [B,H,T,D], or [B,H,D] / [T,H,D] (``shape`` says which it must be)."""
+# These helpers run on every call of a decode loop, so they are kept lean: a
+# view is handed over as the packed bytes of an ssa_view_t.
+_pack_view = struct.Struct("@Pqqq").pack
+
+
+def _strides(t, name, shape, dtype, device):
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype or t.device != device:
+    if t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
     st = t.stride()
-    if st[-1] != 1 and t.shape[-1] != 1:
+    if st[-1] != 1:
         raise ValueError(f"{name}: the last axis must be contiguous (stride {st[-1]})")
     return st
 
 
 def _view4(t, name, shape, dtype, device):
-    st = _view(t, name, shape, dtype, device)
-    return ssa_view_t(t.data_ptr(), st[0], st[1], st[2])
+    """[B,H,T,D]"""
+    st = _strides(t, name, shape, dtype, device)
+    return _pack_view(t.data_ptr(), st[0], st[1], st[2])
 
 
 def _view_bh(t, name, shape, dtype, device):
-    st = _view(t, name, shape, dtype, device)
-    return ssa_view_t(t.data_ptr(), st[0], st[1], 0)
+    """[B,H,D]"""
+    st = _strides(t, name, shape, dtype, device)
+    return _pack_view(t.data_ptr(), st[0], st[1], 0)
 
 
 def _view_th(t, name, shape, dtype, device):
-    st = _view(t, name, shape, dtype, device)
-    return ssa_view_t(t.data_ptr(), 0, st[1], st[0])
+    """[T,H,D]"""
+    st = _strides(t, name, shape, dtype, device)
+    return _pack_view(t.data_ptr(), 0, st[1], st[0])
 
 
 def _plain(t, name, shape, dtype, device):
     """Pointer of a contiguous tensor of this shape and type (None passes)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _pages(p, t, name, device):
-    shape = (p.n_pages, p.Hkv, p.page, p.D)
     st = t.stride()
-    if (t.shape != shape or t.dtype != _TORCH_DT[p.dtype] or t.device != device
+    if (t.shape != (p.n_pages, p.Hkv, p.page, p.D) or t.dtype is not _TORCH_DT[p.dtype] or t.device != device
             or st[1:] != (p.page * p.D, p.D, 1) or (st[0] != p.page_stride and p.n_pages > 1)):
-        raise ValueError(f"{name} must be {_TORCH_DT[p.dtype]} pages {shape} on {device}, each page contiguous and "
-                         f"{p.page_stride} elements after the one before, got {t.dtype} {tuple(t.shape)} with "
-                         f"strides {st} on {t.device}")
+        raise ValueError(f"{name} must be {_TORCH_DT[p.dtype]} pages {(p.n_pages, p.Hkv, p.page, p.D)} on {device}, "
+                         f"each page contiguous and {p.page_stride} elements after the one before, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {st} on {t.device}")
     return t.data_ptr()
 
 
 def _cuda(t, name):
-    if not t.is_cuda:
+    dev = t.device
+    if dev.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return dev
 
 
-class _on:
-    """Makes the tensors' device the current one for a call, if it is not."""
-
-    def __init__(self, device):
-        self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _launch(where, fn, device, *args):
+    """fn(*args, stream) on the device's current stream, with that device current."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if status != SSA_OK:
+        check(status, where)
 
 
-def _scratch(nbytes, ws, where, device):
-    if nbytes == ctypes.c_size_t(-1).value:
+_INVALID = ctypes.c_size_t(-1).value
+
+
+def _scratch(nbytes, where, device):
+    if nbytes == _INVALID:
         raise SsaError(where, SSA_ERR_INVALID_ARG, ssa_last_error())
-    if ws is None:
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    if ws.device != device:
-        raise ValueError(f"ws must be on {device}")
+    return torch.empty(nbytes or 1, dtype=torch.uint8, device=device)
+
+
+def _given(ws, device):
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
     return ws
 
 
@@ -627,11 +637,9 @@ def window_fwd(params, q, k, v, lens=None, out=None):
     qs, ks = (p.B, p.Hq, p.T, p.D), (p.B, p.Hkv, p.T, p.D)
     if out is None:
         out = {"h": torch.empty_like(q), "lse": torch.empty(qs[:3], dtype=_F32, device=dev)}
-    with _on(dev):
-        check(ssa_window_fwd(p, _view4(q, "q", qs, dt, dev), _view4(k, "k", ks, dt, dev),
-                             _view4(v, "v", ks, dt, dev), _plain(lens, "lens", (p.B,), _I32, dev),
-                             _view4(out["h"], "h", qs, dt, dev), _plain(out["lse"], "lse", qs[:3], _F32, dev),
-                             _stream(dev)), "ssa_window_fwd")
+    _launch("ssa_window_fwd", _lib.ssa_window_fwd, dev, ctypes.byref(p), _view4(q, "q", qs, dt, dev),
+            _view4(k, "k", ks, dt, dev), _view4(v, "v", ks, dt, dev), _plain(lens, "lens", (p.B,), _I32, dev),
+            _view4(out["h"], "h", qs, dt, dev), _plain(out["lse"], "lse", qs[:3], _F32, dev))
     return out
 
 
@@ -641,14 +649,12 @@ def window_bwd(params, q, k, v, fwd, dh, lens=None, ws=None, out=None):
     dt = _TORCH_DT[p.dtype]
     qs, ks = (p.B, p.Hq, p.T, p.D), (p.B, p.Hkv, p.T, p.D)
     dq, dk, dv = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)) if out is None else out
-    ws = _scratch(ssa_window_workspace_size(p), ws, "ssa_window_workspace_size", dev)
-    with _on(dev):
-        check(ssa_window_bwd(p, _view4(q, "q", qs, dt, dev), _view4(k, "k", ks, dt, dev),
-                             _view4(v, "v", ks, dt, dev), _plain(lens, "lens", (p.B,), _I32, dev),
-                             _view4(fwd["h"], "h", qs, dt, dev), _plain(fwd["lse"], "lse", qs[:3], _F32, dev),
-                             _view4(dh, "dh", qs, dt, dev), _view4(dq, "dq", qs, dt, dev),
-                             _view4(dk, "dk", ks, dt, dev), _view4(dv, "dv", ks, dt, dev), _ptr(ws), ws.numel(),
-                             _stream(dev)), "ssa_window_bwd")
+    ws = _scratch(ssa_window_workspace_size(p), "ssa_window_workspace_size", dev) if ws is None else _given(ws, dev)
+    _launch("ssa_window_bwd", _lib.ssa_window_bwd, dev, ctypes.byref(p), _view4(q, "q", qs, dt, dev),
+            _view4(k, "k", ks, dt, dev), _view4(v, "v", ks, dt, dev), _plain(lens, "lens", (p.B,), _I32, dev),
+            _view4(fwd["h"], "h", qs, dt, dev), _plain(fwd["lse"], "lse", qs[:3], _F32, dev),
+            _view4(dh, "dh", qs, dt, dev), _view4(dq, "dq", qs, dt, dev), _view4(dk, "dk", ks, dt, dev),
+            _view4(dv, "dv", ks, dt, dev), ws.data_ptr(), ws.nbytes)
     return dq, dk, dv
 
 
@@ -672,23 +678,20 @@ def cache_append(params, k_pages, v_pages, table, lens, k, v, q=None, inv_freq=N
     if q is not None and q_out is None:
         q_out = torch.empty_like(q)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    with _on(dev):
-        check(ssa_cache_append(
-            p, N, _view_th(k, "k", ks, dt, dev), _view_th(v, "v", ks, dt, dev),
-            None if q is None else _view_th(q, "q", qs, dt, dev), _pages(p, k_pages, "k_pages", dev),
-            _pages(p, v_pages, "v_pages", dev), _plain(table, "table", (p.B, p.max_pages), _I32, dev),
-            _plain(lens, "lens", (p.B,), _I32, dev), _plain(new_lens, "new_lens", (p.B,), _I32, dev),
-            _plain(q_start, "q_start", (p.B + 1,), _I32, dev),
-            _plain(inv_freq, "inv_freq", (rot // 2,), _F64, dev), rot, int(bool(interleaved)), pos_offset,
+    _launch("ssa_cache_append", _lib.ssa_cache_append, dev, ctypes.byref(p), N, _view_th(k, "k", ks, dt, dev),
+            _view_th(v, "v", ks, dt, dev), None if q is None else _view_th(q, "q", qs, dt, dev),
+            _pages(p, k_pages, "k_pages", dev), _pages(p, v_pages, "v_pages", dev),
+            _plain(table, "table", (p.B, p.max_pages), _I32, dev), _plain(lens, "lens", (p.B,), _I32, dev),
+            _plain(new_lens, "new_lens", (p.B,), _I32, dev), _plain(q_start, "q_start", (p.B + 1,), _I32, dev),
+            _plain(inv_freq, "inv_freq", (rot // 2,), _F64, dev), rot, 1 if interleaved else 0, pos_offset,
             None if q is None else _view_th(q_out, "q_out", qs, dt, dev),
-            None if k_out is None else _view_th(k_out, "k_out", ks, dt, dev), _stream(dev)), "ssa_cache_append")
+            None if k_out is None else _view_th(k_out, "k_out", ks, dt, dev))
     return {"q": q_out, "lens": new_lens}
 
 
-def _decode_out(p, out, dev, dt):
+def _decode_out(p, q, out, dev):
     if out is None:
-        out = {"h": torch.empty((p.B, p.Hq, p.D), dtype=dt, device=dev),
-               "lse": torch.empty((p.B, p.Hq), dtype=_F32, device=dev)}
+        out = {"h": torch.empty_like(q), "lse": torch.empty((p.B, p.Hq), dtype=_F32, device=dev)}
     return out
 
 
@@ -697,15 +700,13 @@ def paged_decode(params, q, k_pages, v_pages, table, lens, ws=None, out=None):
     -> dict(h [B,Hq,D], lse [B,Hq] float32).  ``lens`` count the token itself."""
     p, dev = params, _cuda(q, "q")
     dt, hs = _TORCH_DT[p.dtype], (p.B, p.Hq, p.D)
-    out = _decode_out(p, out, dev, dt)
-    ws = _scratch(ssa_cache_workspace_size(p, 0), ws, "ssa_cache_workspace_size", dev)
-    with _on(dev):
-        check(ssa_paged_decode(p, _view_bh(q, "q", hs, dt, dev), _pages(p, k_pages, "k_pages", dev),
-                               _pages(p, v_pages, "v_pages", dev),
-                               _plain(table, "table", (p.B, p.max_pages), _I32, dev),
-                               _plain(lens, "lens", (p.B,), _I32, dev), _view_bh(out["h"], "h", hs, dt, dev),
-                               _plain(out["lse"], "lse", hs[:2], _F32, dev), _ptr(ws), ws.numel(),
-                               _stream(dev)), "ssa_paged_decode")
+    out = _decode_out(p, q, out, dev)
+    ws = _scratch(ssa_cache_workspace_size(p, 0), "ssa_cache_workspace_size", dev) if ws is None else _given(ws, dev)
+    _launch("ssa_paged_decode", _lib.ssa_paged_decode, dev, ctypes.byref(p), _view_bh(q, "q", hs, dt, dev),
+            _pages(p, k_pages, "k_pages", dev), _pages(p, v_pages, "v_pages", dev),
+            _plain(table, "table", (p.B, p.max_pages), _I32, dev), _plain(lens, "lens", (p.B,), _I32, dev),
+            _view_bh(out["h"], "h", hs, dt, dev), _plain(out["lse"], "lse", hs[:2], _F32, dev), ws.data_ptr(),
+            ws.nbytes)
     return out
 
 
@@ -714,17 +715,15 @@ def prefix_decode(params, q, k_pages, v_pages, prefix_pages, prefix_len, table, 
     ``prefix_len`` tokens of ``prefix_pages`` and the ``lens`` tokens of its own pages."""
     p, dev = params, _cuda(q, "q")
     dt, hs = _TORCH_DT[p.dtype], (p.B, p.Hq, p.D)
-    out = _decode_out(p, out, dev, dt)
-    ws = _scratch(ssa_cache_workspace_size(p, prefix_len), ws, "ssa_cache_workspace_size", dev)
+    out = _decode_out(p, q, out, dev)
+    ws = _scratch(ssa_cache_workspace_size(p, prefix_len), "ssa_cache_workspace_size", dev) if ws is None else _given(ws, dev)
     n = -(-prefix_len // p.page)
-    with _on(dev):
-        check(ssa_prefix_decode(p, _view_bh(q, "q", hs, dt, dev), _pages(p, k_pages, "k_pages", dev),
-                                _pages(p, v_pages, "v_pages", dev),
-                                _plain(prefix_pages, "prefix_pages", (n,), _I32, dev) if n else None, prefix_len,
-                                _plain(table, "table", (p.B, p.max_pages), _I32, dev),
-                                _plain(lens, "lens", (p.B,), _I32, dev), _view_bh(out["h"], "h", hs, dt, dev),
-                                _plain(out["lse"], "lse", hs[:2], _F32, dev), _ptr(ws), ws.numel(),
-                                _stream(dev)), "ssa_prefix_decode")
+    _launch("ssa_prefix_decode", _lib.ssa_prefix_decode, dev, ctypes.byref(p), _view_bh(q, "q", hs, dt, dev),
+            _pages(p, k_pages, "k_pages", dev), _pages(p, v_pages, "v_pages", dev),
+            _plain(prefix_pages, "prefix_pages", (n,), _I32, dev) if n else None, prefix_len,
+            _plain(table, "table", (p.B, p.max_pages), _I32, dev), _plain(lens, "lens", (p.B,), _I32, dev),
+            _view_bh(out["h"], "h", hs, dt, dev), _plain(out["lse"], "lse", hs[:2], _F32, dev), ws.data_ptr(),
+            ws.nbytes)
     return out
 
 
@@ -749,7 +748,7 @@ class PagedCache:
         self.prefix_pages = B * width + torch.arange(shared, dtype=_I32, device=device)
         self.inv_freq, self.interleaved = inv_freq, interleaved
         n = ssa_cache_workspace_size(self.params, prefix_len)
-        self.ws = _scratch(n, None, "ssa_cache_workspace_size", self.k_pages.device)
+        self.ws = _scratch(n, "ssa_cache_workspace_size", self.k_pages.device)
 
     def append(self, k, v, q=None, q_start=None, q_out=None, k_out=None):
         """Appends new tokens (see ``cache_append``) -> the rotated queries."""
