@@ -11,7 +11,9 @@
 // The call only moves data: a token's rows are read and written once.  One CTA
 // per token: its rotary angles are computed once, by one thread per pair, and
 // shared by all heads through shared memory, while every thread's first
-// 16-byte vectors are already on their way.  Vectors of 16 bytes need
+// 16-byte vectors are already on their way.  (Four tokens to a CTA, and two or
+// four accesses in flight per thread, cost more in resident threads than they
+// gave: 86 to 143 us for 16384 tokens.)  Vectors of 16 bytes need
 // rot_dim / 2 (pairs a half apart) or rot_dim (neighbours) to be whole
 // vectors; other rotary sizes take the element-wise instance.
 #include "device_util.cuh"
@@ -19,8 +21,6 @@
 
 namespace ssa {
 namespace {
-
-constexpr int kThreads = 256;
 
 __device__ unsigned int g_append_status;
 
@@ -61,7 +61,7 @@ __device__ __forceinline__ void stv(T* p, const Vec<T, VEC>& v) {
 }
 
 // VEC: elements per access of the turned rows (16 bytes, or 1 / 2).
-template <typename T, int VEC, bool kInter>
+template <typename T, int VEC, bool kInter, int kThreads>
 __global__ void __launch_bounds__(kThreads)
 append_kernel(const AppendArgs a) {
     constexpr int VMAX = 16 / (int)sizeof(T);
@@ -78,15 +78,20 @@ append_kernel(const AppendArgs a) {
         const int n = a.N / a.B;
         b = i / n;
         first = (long long)b * n;
-    } else if (i >= a.q_start[0] && i < a.q_start[a.B]) {
-        int lo = 0, hi = a.B;  // q_start[lo] <= i < q_start[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.q_start[mid] <= i) lo = mid;
-            else hi = mid;
+    } else {
+        // the last sequence that starts at i or before, 32 of them at a time (every
+        // warp for itself; a search by halves would wait for a load at each step)
+        const int lane = threadIdx.x & 31;
+        for (int b0 = 0; b0 <= a.B; b0 += 32) {
+            const int s = b0 + lane <= a.B ? a.q_start[b0 + lane] : 0x7fffffff;
+            const unsigned le = __ballot_sync(0xffffffffu, s <= i);
+            if (le) {
+                b = b0 + 31 - __clz(le);
+                first = __shfl_sync(0xffffffffu, s, 31 - __clz(le));
+            }
+            if (le != 0xffffffffu) break;
         }
-        b = lo;
-        first = a.q_start[lo];
+        if (b == a.B) b = -1;  // behind the last one
     }
     long long slot = -1;
     size_t row = 0;  // element offset of head 0's row in the pools
@@ -204,17 +209,24 @@ __global__ void lens_kernel(const AppendArgs a) {
     for (int b = threadIdx.x; b < a.B; b += blockDim.x) a.new_lens[b] = grown(a, b, a.lens[b]);
 }
 
-template <typename T>
+template <typename T, int kThreads>
 void launch(const AppendArgs& a, bool inter, unsigned grid, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
     if (inter) {
-        if (2 * a.half % V == 0) append_kernel<T, V, true><<<grid, kThreads, 0, s>>>(a);
-        else append_kernel<T, 2, true><<<grid, kThreads, 0, s>>>(a);
+        if (2 * a.half % V == 0) append_kernel<T, V, true, kThreads><<<grid, kThreads, 0, s>>>(a);
+        else append_kernel<T, 2, true, kThreads><<<grid, kThreads, 0, s>>>(a);
     } else {
-        if (a.half % V == 0) append_kernel<T, V, false><<<grid, kThreads, 0, s>>>(a);
-        else append_kernel<T, 1, false><<<grid, kThreads, 0, s>>>(a);
+        if (a.half % V == 0) append_kernel<T, V, false, kThreads><<<grid, kThreads, 0, s>>>(a);
+        else append_kernel<T, 1, false, kThreads><<<grid, kThreads, 0, s>>>(a);
     }
 }
+
+// Tokens up to which a CTA has 256 threads and not 128: few tokens leave SMs
+// idle, and the wider CTA is done sooner (8 tokens of 16/4 heads of 128, bf16: 3.3 us
+// against 3.7); many are held up by the barrier behind the look-ups, which
+// couples fewer warps in a small CTA (1000 tokens of 32/8 heads 9.0 against 7.2 us,
+// 16384 tokens 91 against 74 us, 81 % of the measured copy bandwidth).
+constexpr int kFewTokens = 512;
 
 }  // namespace
 
@@ -238,8 +250,11 @@ int launch_cache_append(const ssa_cache_params_t& p, int n, const View& k, const
     const bool extra = new_lens && !a.step && new_lens != lens;
     const unsigned grid = (unsigned)n + (extra ? 1u : 0u);
     if (grid) {
-        if (p.dtype == SSA_BF16) launch<__nv_bfloat16>(a, interleaved != 0, grid, s);
-        else launch<float>(a, interleaved != 0, grid, s);
+        const bool inter = interleaved != 0, few = n <= kFewTokens;
+        if (p.dtype == SSA_BF16)
+            few ? launch<__nv_bfloat16, 256>(a, inter, grid, s) : launch<__nv_bfloat16, 128>(a, inter, grid, s);
+        else
+            few ? launch<float, 256>(a, inter, grid, s) : launch<float, 128>(a, inter, grid, s);
         const int st = check_launch("append_kernel");
         if (st != SSA_OK) return st;
     }
