@@ -10,9 +10,13 @@
 // tiles, 256 threads of 4 x 4 scores and 4 x D/16 outputs each, operands in
 // shared memory with rows of D + 4 floats (16 lanes read 16 rows without bank
 // conflicts).  Only the tiles that the window and the sinks reach are
-// visited.  The gradients take two kernels, one CTA per key tile for dk and dv
-// (summing over the query heads of its group in order) and one per query tile
-// for dq, so that every sum has one owner and a fixed order.
+// visited.  The gradients take two kernels, one per query tile for dq and one
+// over key tiles for dk and dv: a tile's list of (query head of the group, query
+// tile) is one CTA's, or, where there are too few key tiles to fill the SMs and
+// for tiles that hold sinks (every later query sees them), is cut into
+// stretches whose parts window_parts_kernel sums in order.  (Two sequences of
+// 777 tokens, 4/2 heads of 64, window 128, 4 sinks: 92 us for both directions,
+// 332 us with one CTA to a key tile.)
 #include "device_util.cuh"
 #include "ssa_internal.h"
 
@@ -32,8 +36,16 @@ struct WinArgs {
     float* delta;
     const int32_t* lens;
     int B, Hq, Hkv, G, T, window, sinks;
+    int nsink, cuts, sink_cuts;  // key tiles with sinks; stretches of a tile's list without and with them
+    float* part;                 // [B * Hkv][slots][dk, dv][64][D]
     float sm_scale;
 };
+
+// Slots of a head: a tile with one stretch has none.
+__host__ __device__ __forceinline__ int first_slot(const WinArgs& a, int tile) {
+    const int s = a.sink_cuts > 1 ? a.sink_cuts : 0, c = a.cuts > 1 ? a.cuts : 0;
+    return tile < a.nsink ? tile * s : a.nsink * s + (tile - a.nsink) * c;
+}
 
 __device__ __forceinline__ int seq_len(const WinArgs& a, int b) {
     if (!a.lens) return a.T;
@@ -337,7 +349,11 @@ window_dkdv_simt_kernel(const WinArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr size_t N = tile_floats<D>();
     float *Q = sm, *dO = Q + N, *K = dO + N, *V = K + N, *P = V + N, *dS = P + BT * PP;
-    const int s0 = blockIdx.x * BT, hk = blockIdx.y, b = blockIdx.z;
+    // item -> (tile, stretch): the tiles with sinks first
+    const int hk = blockIdx.y, b = blockIdx.z, nsc = a.nsink * a.sink_cuts;
+    const bool sink = (int)blockIdx.x < nsc;
+    const int cuts = sink ? a.sink_cuts : a.cuts, x0 = sink ? (int)blockIdx.x : (int)blockIdx.x - nsc;
+    const int tile = (sink ? 0 : a.nsink) + x0 / cuts, cut = x0 % cuts, s0 = tile * BT;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int len = seq_len(a, b);
     float4 ok[4][D / 64], ov[4][D / 64];
@@ -353,26 +369,39 @@ window_dkdv_simt_kernel(const WinArgs a) {
         f.store(V);
         // the last query that sees a key of the tile (a sink: the last of all)
         const int tl = s0 < a.sinks ? len - 1 : (int)min((long long)len - 1, (long long)s0 + BT - 1 + a.window - 1);
-        for (int g = 0; g < a.G; ++g) {
-            const int hq = hk * a.G + g;
+        const int per = tl / BT - tile + 1;  // query tiles of a head
+        const long long all = (long long)a.G * per;
+        const int i1 = (int)(all * (cut + 1) / cuts);
+        for (int i = (int)(all * cut / cuts); i < i1; ++i) {
+            const int hq = hk * a.G + i / per, t0 = s0 + i % per * BT;
             const float* lse = a.lse + ((size_t)b * a.Hq + hq) * a.T;
             const float* delta = a.delta + ((size_t)b * a.Hq + hq) * a.T;
-            for (int t0 = s0; t0 <= tl; t0 += BT) {
-                __syncthreads();
-                f.load(a.q, b, hq, t0, len);
-                f.store(Q);
-                f.load(a.dh, b, hq, t0, len);
-                f.store(dO);
-                __syncthreads();
-                float s[4][4], dp[4][4];
-                scores<D>(Q, K, ty, tx, s);
-                scores<D>(dO, V, ty, tx, dp);
-                weights(a, lse, delta, t0, s0, len, ty, tx, s, dp, P, dS);
-                __syncthreads();
-                scatter<D>(P, dO, ty, tx, ov);
-                scatter<D>(dS, Q, ty, tx, ok);
-            }
+            __syncthreads();
+            f.load(a.q, b, hq, t0, len);
+            f.store(Q);
+            f.load(a.dh, b, hq, t0, len);
+            f.store(dO);
+            __syncthreads();
+            float s[4][4], dp[4][4];
+            scores<D>(Q, K, ty, tx, s);
+            scores<D>(dO, V, ty, tx, dp);
+            weights(a, lse, delta, t0, s0, len, ty, tx, s, dp, P, dS);
+            __syncthreads();
+            scatter<D>(P, dO, ty, tx, ov);
+            scatter<D>(dS, Q, ty, tx, ok);
         }
+    }
+    if (cuts > 1) {
+        const int nt = (a.T + BT - 1) / BT;
+        float* slot = a.part + ((size_t)(b * a.Hkv + hk) * first_slot(a, nt) + first_slot(a, tile) + cut) * 2 * BT * D;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                st4(slot + (4 * ty + i) * D + 4 * tx + 64 * c, ok[i][c]);
+                st4(slot + (BT + 4 * ty + i) * D + 4 * tx + 64 * c, ov[i][c]);
+            }
+        return;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -386,6 +415,27 @@ window_dkdv_simt_kernel(const WinArgs a) {
     }
 }
 
+// dk and dv of the tiles whose lists are in stretches: their parts in order
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+window_parts_kernel(const WinArgs a) {
+    constexpr int kBlocks = 2 * BT * D / 4 / kThreads;  // of a tile
+    const int tile = blockIdx.x / kBlocks, hk = blockIdx.y, b = blockIdx.z, nt = (a.T + BT - 1) / BT;
+    const int cuts = tile < a.nsink ? a.sink_cuts : a.cuts;
+    if (cuts == 1) return;
+    const float* src = a.part + ((size_t)(b * a.Hkv + hk) * first_slot(a, nt) + first_slot(a, tile)) * 2 * BT * D;
+    const int x = (int)(blockIdx.x % kBlocks) * kThreads + threadIdx.x;
+    const int w = x / (BT * D / 4), r = x / (D / 4) % BT, c = 4 * (x % (D / 4));
+    if (tile * BT + r >= a.T) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i < cuts; ++i) {
+        const float4 v = ld4(src + (size_t)i * 2 * BT * D + 4 * x);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    st4(at<T>(w ? a.dv : a.dk, b, hk, tile * BT + r) + c, s);
+}
+
 WinArgs args(const ssa_window_params_t& p, const View& q, const View& k, const View& v, const int32_t* lens,
              const View& h, float* lse) {
     WinArgs a{};
@@ -394,7 +444,22 @@ WinArgs args(const ssa_window_params_t& p, const View& q, const View& k, const V
     a.window = p.window > 0 && p.window < p.T ? p.window : p.T;  // a window of T tokens leaves none behind
     a.sinks = a.window < p.T ? (p.sinks < p.T ? p.sinks : p.T) : 0;
     a.sm_scale = p.sm_scale;
+    // stretches: about three CTAs for each of 148 SMs; those of a tile with sinks about as long as the others
+    const int nt = (p.T + BT - 1) / BT;
+    const long long tiles = (long long)p.B * p.Hkv * nt, per = ((long long)BT - 1 + a.window - 1) / BT + 1;
+    const long long list = a.G * (per < nt ? per : nt);
+    long long cuts = (444 + tiles - 1) / tiles;
+    cuts = cuts < list ? cuts : list;
+    a.cuts = (int)cuts;
+    a.nsink = (a.sinks + BT - 1) / BT;
+    const long long longest = (long long)a.G * nt, usual = (list + cuts - 1) / cuts;
+    const long long sc = (longest + usual - 1) / usual;
+    a.sink_cuts = a.nsink ? (int)(sc < 64 ? sc : 64) : 1;
     return a;
+}
+
+size_t part_bytes(const WinArgs& a, int D) {
+    return (size_t)a.B * a.Hkv * first_slot(a, (a.T + BT - 1) / BT) * 2 * BT * D * sizeof(float);
 }
 
 template <typename T, int D>
@@ -417,7 +482,11 @@ int bwd(const WinArgs& a, cudaStream_t s) {
     if (st != SSA_OK) return st;
     const unsigned nt = (unsigned)((a.T + BT - 1) / BT);
     window_delta_kernel<T, D><<<dim3((unsigned)((a.T + 7) / 8), (unsigned)a.Hq, (unsigned)a.B), kThreads, 0, s>>>(a);
-    window_dkdv_simt_kernel<T, D><<<dim3(nt, (unsigned)a.Hkv, (unsigned)a.B), kThreads, smem_k, s>>>(a);
+    const unsigned items = (unsigned)(a.nsink * a.sink_cuts + ((int)nt - a.nsink) * a.cuts);
+    window_dkdv_simt_kernel<T, D><<<dim3(items, (unsigned)a.Hkv, (unsigned)a.B), kThreads, smem_k, s>>>(a);
+    if (a.cuts > 1 || a.sink_cuts > 1)
+        window_parts_kernel<T, D><<<dim3((a.cuts > 1 ? nt : (unsigned)a.nsink) * (2 * BT * D / 4 / kThreads), (unsigned)a.Hkv,
+                                          (unsigned)a.B), kThreads, 0, s>>>(a);
     window_dq_simt_kernel<T, D><<<dim3(nt, (unsigned)a.Hq, (unsigned)a.B), kThreads, smem_q, s>>>(a);
     return check_launch("window backward (CUDA cores)");
 }
@@ -432,7 +501,8 @@ int launch_window_fwd_simt(const ssa_window_params_t& p, const View& q, const Vi
 }
 
 size_t window_bwd_simt_workspace(const ssa_window_params_t& p) {
-    return align_up((size_t)p.B * p.Hq * p.T * sizeof(float), 256);  // delta
+    return align_up((size_t)p.B * p.Hq * p.T * sizeof(float), 256) +  // delta
+           align_up(part_bytes(args(p, View{}, View{}, View{}, nullptr, View{}, nullptr), p.D), 256);
 }
 
 int launch_window_bwd_simt(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
@@ -440,6 +510,7 @@ int launch_window_bwd_simt(const ssa_window_params_t& p, const View& q, const Vi
                            const View& dq, const View& dk, const View& dv, void* ws, cudaStream_t s) {
     WinArgs a = args(p, q, k, v, lens, h, const_cast<float*>(lse));
     a.dh = dh, a.dq = dq, a.dk = dk, a.dv = dv, a.delta = static_cast<float*>(ws);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up((size_t)p.B * p.Hq * p.T * sizeof(float), 256));
     if (p.dtype == SSA_BF16) return p.D == 64 ? bwd<__nv_bfloat16, 64>(a, s) : bwd<__nv_bfloat16, 128>(a, s);
     return p.D == 64 ? bwd<float, 64>(a, s) : bwd<float, 128>(a, s);
 }
