@@ -1,8 +1,10 @@
-"""Build step for libssa.so (the C-ABI library) with nvcc for sm_100a.
+"""Build step for libssa.so (the C-ABI library) with nvcc for sm_100a, and for
+_marshal.so (argument marshalling for Python, against torch's headers) with g++.
 
 Compiles every ``csrc/*.cu`` to an object under ``_build/`` (in parallel) and
-links them into ``block_sparse_full_b200/libssa.so``.  Objects are rebuilt only
-when their source or a header is newer.  Run as ``python -m
+links them into ``block_sparse_full_b200/libssa.so``; ``csrc/marshal.cpp``
+becomes ``block_sparse_full_b200/_marshal.so``.  They are rebuilt only when a
+source or a header is newer.  Run as ``python -m
 block_sparse_full_b200.build``.
 """
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssa.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -55,6 +59,26 @@ def _compile(src: str, obj: str, extra, verbose: bool):
     return r.stderr
 
 
+def _build_marshal(verbose: bool, force: bool):
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not force and not _stale(MARSHAL, [src, os.path.join(INCLUDE, "ssa.h")]):
+        return
+    import torch  # only its location and ABI
+
+    t = os.path.dirname(torch.__file__)
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(t, "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), src, "-o", MARSHAL,
+           LIB, "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for marshal.cpp:\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -74,13 +98,14 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
             if ptxas_info and log:
                 print(f"== {os.path.basename(futs[f])}\n{log}", flush=True)
     if jobs or _stale(LIB, objs):
-        cmd = [nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart_static", "-ldl", "-lrt",
+        cmd = [nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=libssa.so", "-o", LIB, *objs, "-lcudart_static", "-ldl", "-lrt",
                "-lpthread"]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _build_marshal(verbose, force)
     return LIB
 
 

@@ -1,6 +1,7 @@
 """Thin Python binding of libssa (the C ABI in include/ssa.h).
 
-Two layers, both argument marshalling only:
+Two layers, both argument marshalling only (the second one, for the calls of a
+decode loop, in ``csrc/marshal.cpp``):
 
 * ``ssa_*`` functions with the C names and signatures; pointers and the
   stream are plain integers.
@@ -22,7 +23,6 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-import struct
 from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_uint, c_void_p
 
 import torch
@@ -147,6 +147,7 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+from . import _marshal  # noqa: E402  (tensor checks and calls of the paged cache and window attention; needs libssa)
 
 
 def lib() -> ctypes.CDLL:
@@ -532,96 +533,7 @@ def cache_params_for(q, k_pages, table, window=0, sinks=0, sm_scale=None) -> ssa
                         k_pages.stride(0))
 
 
-_I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
-_TORCH_DT = {SSA_F32: torch.float32, SSA_BF16: torch.bfloat16}
-
-
-# These helpers run on every call of a decode loop, so they are kept lean: a
-# view is handed over as the packed bytes of an ssa_view_t.
-_pack_view = struct.Struct("@Pqqq").pack
-
-
-def _strides(t, name, shape, dtype, device):
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous (stride {st[-1]})")
-    return st
-
-
-def _view4(t, name, shape, dtype, device):
-    """[B,H,T,D]"""
-    st = _strides(t, name, shape, dtype, device)
-    return _pack_view(t.data_ptr(), st[0], st[1], st[2])
-
-
-def _view_bh(t, name, shape, dtype, device):
-    """[B,H,D]"""
-    st = _strides(t, name, shape, dtype, device)
-    return _pack_view(t.data_ptr(), st[0], st[1], 0)
-
-
-def _view_th(t, name, shape, dtype, device):
-    """[T,H,D]"""
-    st = _strides(t, name, shape, dtype, device)
-    return _pack_view(t.data_ptr(), 0, st[1], st[0])
-
-
-def _plain(t, name, shape, dtype, device):
-    """Pointer of a contiguous tensor of this shape and type (None passes)."""
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _pages(p, t, name, device):
-    st = t.stride()
-    if (t.shape != (p.n_pages, p.Hkv, p.page, p.D) or t.dtype is not _TORCH_DT[p.dtype] or t.device != device
-            or st[1:] != (p.page * p.D, p.D, 1) or (st[0] != p.page_stride and p.n_pages > 1)):
-        raise ValueError(f"{name} must be {_TORCH_DT[p.dtype]} pages {(p.n_pages, p.Hkv, p.page, p.D)} on {device}, "
-                         f"each page contiguous and {p.page_stride} elements after the one before, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {st} on {t.device}")
-    return t.data_ptr()
-
-
-def _cuda(t, name):
-    dev = t.device
-    if dev.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
-
-
-def _launch(where, fn, device, *args):
-    """fn(*args, stream) on the device's current stream, with that device current."""
-    i = device.index
-    if i == torch.cuda.current_device():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
-    if status != SSA_OK:
-        check(status, where)
-
-
-_INVALID = ctypes.c_size_t(-1).value
-
-
-def _scratch(nbytes, where, device):
-    if nbytes == _INVALID:
-        raise SsaError(where, SSA_ERR_INVALID_ARG, ssa_last_error())
-    return torch.empty(nbytes or 1, dtype=torch.uint8, device=device)
-
-
-def _given(ws, device):
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous tensor on {device}")
-    return ws
+_NO_PAIR = (None, None)
 
 
 def window_fwd(params, q, k, v, lens=None, out=None):
@@ -632,30 +544,18 @@ def window_fwd(params, q, k, v, lens=None, out=None):
     behind a length get h = 0 and lse = -inf.  h is laid out like q where q
     fills its memory, else contiguous.
     """
-    p, dev = params, _cuda(q, "q")
-    dt = _TORCH_DT[p.dtype]
-    qs, ks = (p.B, p.Hq, p.T, p.D), (p.B, p.Hkv, p.T, p.D)
-    if out is None:
-        out = {"h": torch.empty_like(q), "lse": torch.empty(qs[:3], dtype=_F32, device=dev)}
-    _launch("ssa_window_fwd", _lib.ssa_window_fwd, dev, ctypes.byref(p), _view4(q, "q", qs, dt, dev),
-            _view4(k, "k", ks, dt, dev), _view4(v, "v", ks, dt, dev), _plain(lens, "lens", (p.B,), _I32, dev),
-            _view4(out["h"], "h", qs, dt, dev), _plain(out["lse"], "lse", qs[:3], _F32, dev))
-    return out
+    r = _marshal.window_fwd(params, q, k, v, lens, *(_NO_PAIR if out is None else (out["h"], out["lse"])))
+    if r.__class__ is int:
+        check(r, "ssa_window_fwd")
+    return {"h": r[0], "lse": r[1]} if out is None else out
 
 
 def window_bwd(params, q, k, v, fwd, dh, lens=None, ws=None, out=None):
     """Gradients (dq, dk, dv) of <dh, h>, from the inputs and the result of ``window_fwd``."""
-    p, dev = params, _cuda(q, "q")
-    dt = _TORCH_DT[p.dtype]
-    qs, ks = (p.B, p.Hq, p.T, p.D), (p.B, p.Hkv, p.T, p.D)
-    dq, dk, dv = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)) if out is None else out
-    ws = _scratch(ssa_window_workspace_size(p), "ssa_window_workspace_size", dev) if ws is None else _given(ws, dev)
-    _launch("ssa_window_bwd", _lib.ssa_window_bwd, dev, ctypes.byref(p), _view4(q, "q", qs, dt, dev),
-            _view4(k, "k", ks, dt, dev), _view4(v, "v", ks, dt, dev), _plain(lens, "lens", (p.B,), _I32, dev),
-            _view4(fwd["h"], "h", qs, dt, dev), _plain(fwd["lse"], "lse", qs[:3], _F32, dev),
-            _view4(dh, "dh", qs, dt, dev), _view4(dq, "dq", qs, dt, dev), _view4(dk, "dk", ks, dt, dev),
-            _view4(dv, "dv", ks, dt, dev), ws.data_ptr(), ws.nbytes)
-    return dq, dk, dv
+    r = _marshal.window_bwd(params, q, k, v, lens, fwd["h"], fwd["lse"], dh, ws, *(out or (None, None, None)))
+    if r.__class__ is int:
+        check(r, "ssa_window_bwd")
+    return r
 
 
 def cache_append(params, k_pages, v_pages, table, lens, k, v, q=None, inv_freq=None, interleaved=False,
@@ -670,61 +570,33 @@ def cache_append(params, k_pages, v_pages, table, lens, k, v, q=None, inv_freq=N
     be ``lens`` (advanced in place), ``q_out`` may be q, ``k_out`` (k itself or
     another tensor) also receives the rotated keys.
     """
-    p, dev = params, _cuda(k, "k")
-    dt, N = _TORCH_DT[p.dtype], k.shape[0]
-    ks, qs = (N, p.Hkv, p.D), (N, p.Hq, p.D)
-    if new_lens is None:
-        new_lens = torch.empty_like(lens)
-    if q is not None and q_out is None:
-        q_out = torch.empty_like(q)
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _launch("ssa_cache_append", _lib.ssa_cache_append, dev, ctypes.byref(p), N, _view_th(k, "k", ks, dt, dev),
-            _view_th(v, "v", ks, dt, dev), None if q is None else _view_th(q, "q", qs, dt, dev),
-            _pages(p, k_pages, "k_pages", dev), _pages(p, v_pages, "v_pages", dev),
-            _plain(table, "table", (p.B, p.max_pages), _I32, dev), _plain(lens, "lens", (p.B,), _I32, dev),
-            _plain(new_lens, "new_lens", (p.B,), _I32, dev), _plain(q_start, "q_start", (p.B + 1,), _I32, dev),
-            _plain(inv_freq, "inv_freq", (rot // 2,), _F64, dev), rot, 1 if interleaved else 0, pos_offset,
-            None if q is None else _view_th(q_out, "q_out", qs, dt, dev),
-            None if k_out is None else _view_th(k_out, "k_out", ks, dt, dev))
-    return {"q": q_out, "lens": new_lens}
-
-
-def _decode_out(p, q, out, dev):
-    if out is None:
-        out = {"h": torch.empty_like(q), "lse": torch.empty((p.B, p.Hq), dtype=_F32, device=dev)}
-    return out
+    r = _marshal.cache_append(params, k_pages, v_pages, table, lens, k, v, q, inv_freq, interleaved, q_start, pos_offset,
+                              new_lens, q_out, k_out)
+    if r.__class__ is int:
+        check(r, "ssa_cache_append")
+    return {"q": r[0], "lens": r[1]}
 
 
 def paged_decode(params, q, k_pages, v_pages, table, lens, ws=None, out=None):
     """Attention of one token per sequence, q [B,Hq,D], over the paged cache
     -> dict(h [B,Hq,D], lse [B,Hq] float32).  ``lens`` count the token itself."""
-    p, dev = params, _cuda(q, "q")
-    dt, hs = _TORCH_DT[p.dtype], (p.B, p.Hq, p.D)
-    out = _decode_out(p, q, out, dev)
-    ws = _scratch(ssa_cache_workspace_size(p, 0), "ssa_cache_workspace_size", dev) if ws is None else _given(ws, dev)
-    _launch("ssa_paged_decode", _lib.ssa_paged_decode, dev, ctypes.byref(p), _view_bh(q, "q", hs, dt, dev),
-            _pages(p, k_pages, "k_pages", dev), _pages(p, v_pages, "v_pages", dev),
-            _plain(table, "table", (p.B, p.max_pages), _I32, dev), _plain(lens, "lens", (p.B,), _I32, dev),
-            _view_bh(out["h"], "h", hs, dt, dev), _plain(out["lse"], "lse", hs[:2], _F32, dev), ws.data_ptr(),
-            ws.nbytes)
-    return out
+    r = _marshal.decode(params, q, k_pages, v_pages, None, -1, table, lens, ws,
+                        *(_NO_PAIR if out is None else (out["h"], out["lse"])))
+    if r.__class__ is int:
+        check(r, "ssa_paged_decode")
+    return {"h": r[0], "lse": r[1]} if out is None else out
 
 
 def prefix_decode(params, q, k_pages, v_pages, prefix_pages, prefix_len, table, lens, ws=None, out=None):
     """``paged_decode`` for a batch behind one shared prefix: every query sees the first
     ``prefix_len`` tokens of ``prefix_pages`` and the ``lens`` tokens of its own pages."""
-    p, dev = params, _cuda(q, "q")
-    dt, hs = _TORCH_DT[p.dtype], (p.B, p.Hq, p.D)
-    out = _decode_out(p, q, out, dev)
-    ws = _scratch(ssa_cache_workspace_size(p, prefix_len), "ssa_cache_workspace_size", dev) if ws is None else _given(ws, dev)
-    n = -(-prefix_len // p.page)
-    _launch("ssa_prefix_decode", _lib.ssa_prefix_decode, dev, ctypes.byref(p), _view_bh(q, "q", hs, dt, dev),
-            _pages(p, k_pages, "k_pages", dev), _pages(p, v_pages, "v_pages", dev),
-            _plain(prefix_pages, "prefix_pages", (n,), _I32, dev) if n else None, prefix_len,
-            _plain(table, "table", (p.B, p.max_pages), _I32, dev), _plain(lens, "lens", (p.B,), _I32, dev),
-            _view_bh(out["h"], "h", hs, dt, dev), _plain(out["lse"], "lse", hs[:2], _F32, dev), ws.data_ptr(),
-            ws.nbytes)
-    return out
+    if prefix_len < 0:
+        raise ValueError(f"prefix_len must not be negative, got {prefix_len}")
+    r = _marshal.decode(params, q, k_pages, v_pages, prefix_pages, prefix_len, table, lens, ws,
+                        *(_NO_PAIR if out is None else (out["h"], out["lse"])))
+    if r.__class__ is int:
+        check(r, "ssa_prefix_decode")
+    return {"h": r[0], "lse": r[1]} if out is None else out
 
 
 class PagedCache:
@@ -742,13 +614,15 @@ class PagedCache:
         shape = (B * width + shared, Hkv, page, D)
         self.k_pages = torch.zeros(shape, dtype=dtype, device=device)
         self.v_pages = torch.zeros_like(self.k_pages)
-        self.table = torch.arange(B * width, dtype=_I32, device=device).view(B, width)
-        self.lens = torch.zeros(B, dtype=_I32, device=device)
+        self.table = torch.arange(B * width, dtype=torch.int32, device=device).view(B, width)
+        self.lens = torch.zeros(B, dtype=torch.int32, device=device)
         self.prefix_len = prefix_len
-        self.prefix_pages = B * width + torch.arange(shared, dtype=_I32, device=device)
+        self.prefix_pages = B * width + torch.arange(shared, dtype=torch.int32, device=device)
         self.inv_freq, self.interleaved = inv_freq, interleaved
         n = ssa_cache_workspace_size(self.params, prefix_len)
-        self.ws = _scratch(n, "ssa_cache_workspace_size", self.k_pages.device)
+        if n == ctypes.c_size_t(-1).value:
+            raise SsaError("ssa_cache_workspace_size", SSA_ERR_INVALID_ARG, ssa_last_error())
+        self.ws = torch.empty(n, dtype=torch.uint8, device=device)
 
     def append(self, k, v, q=None, q_start=None, q_out=None, k_out=None):
         """Appends new tokens (see ``cache_append``) -> the rotated queries."""
@@ -762,7 +636,7 @@ class PagedCache:
         p, dev = self.params, self.k_pages.device
         one = cache_params(1, p.Hq, p.Hkv, p.D, p.page, p.n_pages, max(1, self.prefix_pages.numel()), p.dtype)
         cache_append(one, self.k_pages, self.v_pages, self.prefix_pages.view(1, -1),
-                     torch.zeros(1, dtype=_I32, device=dev), k, v, None, self.inv_freq, self.interleaved,
+                     torch.zeros(1, dtype=torch.int32, device=dev), k, v, None, self.inv_freq, self.interleaved,
                      k_out=k_out)
 
     def attend(self, q, out=None):

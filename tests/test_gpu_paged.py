@@ -422,3 +422,54 @@ def test_decode_is_repeatable_and_shares_no_state():
     torch.cuda.synchronize()
     for b in got:
         assert torch.equal(a["h"], b["h"]) and torch.equal(a["lse"], b["lse"])
+
+
+def test_tensors_are_checked():
+    B, Hq, Hkv, D, page = 2, 4, 2, 64, 16
+    pool = torch.zeros(4, Hkv, page, D, dtype=torch.bfloat16, device=DEV)
+    table = torch.zeros(B, 2, dtype=torch.int32, device=DEV)
+    lens = torch.ones(B, dtype=torch.int32, device=DEV)
+    q = torch.zeros(B, Hq, D, dtype=torch.bfloat16, device=DEV)
+    k = q[:, :Hkv]
+    p = ssa.cache_params_for(q, pool, table)
+
+    def bad(what, fn, *args, **kw):
+        with pytest.raises(ValueError, match=what):
+            fn(p, *args, **kw)
+
+    dec = ssa.paged_decode
+    bad("q must have shape", dec, q[:1], pool, pool, table, lens)
+    bad("q must be", dec, q.float(), pool, pool, table, lens)
+    bad("last axis", dec, q.transpose(1, 2).contiguous().transpose(1, 2), pool, pool, table, lens)
+    bad("k_pages", dec, q, pool.float(), pool, table, lens)
+    bad("v_pages: each page", dec, q, pool, pool.transpose(1, 2).contiguous().transpose(1, 2), table, lens)
+    bad("table must have", dec, q, pool, pool, table[:, :1], lens)
+    bad("table must be", dec, q, pool, pool, table.long(), lens)
+    bad("table must be contiguous", dec, q, pool, pool, table.t().contiguous().t(), lens)
+    bad("lens must be", dec, q, pool, pool, table, lens.cpu())
+    bad("ws must be", dec, q, pool, pool, table, lens, ws=torch.empty(1 << 20, dtype=torch.uint8))
+    bad("prefix_pages", ssa.prefix_decode, q, pool, pool, table, 17, table, lens)
+    bad("prefix_len", ssa.prefix_decode, q, pool, pool, table, -1, table, lens)
+    app = ssa.cache_append
+    bad("v must have", app, pool, pool, table, lens, k, q)
+    bad("q_out without", app, pool, pool, table, lens, k, k, q_out=q)
+    bad("inv_freq has more", app, pool, pool, table, lens, k, k, inv_freq=torch.ones(33, dtype=torch.float64, device=DEV))
+    bad("inv_freq must be", app, pool, pool, table, lens, k, k, inv_freq=torch.ones(8, device=DEV))
+    bad("q_start must have", app, pool, pool, table, lens, k, k, q_start=lens)
+    bad("pos_offset", app, pool, pool, table, lens, k, k, pos_offset=-1)
+    with pytest.raises(ssa.SsaError, match="new_lens overlaps"):
+        big = torch.zeros(3, dtype=torch.int32, device=DEV)
+        app(p, pool, pool, table, big[:2], k, k, new_lens=big[1:])
+    with pytest.raises(ssa.SsaError, match="workspace"):
+        dec(p, q, pool, pool, table, lens, ws=torch.empty(256, dtype=torch.uint8, device=DEV))
+    w = ssa.window_params(1, 2, 1, 8, 64, 4, 0, torch.bfloat16)
+    x, y = (torch.zeros(1, H, 8, 64, dtype=torch.bfloat16, device=DEV) for H in (2, 1))
+    with pytest.raises(ValueError, match="k must have"):
+        ssa.window_fwd(w, x, x, y)
+    with pytest.raises(ssa.SsaError, match="batch stride|token stride"):
+        ssa.window_fwd(w, x, y[:, :, :1].expand(1, 1, 8, 64), y)
+    f = ssa.window_fwd(w, x, y, y)
+    with pytest.raises(ValueError, match="dh must have"):
+        ssa.window_bwd(w, x, y, y, f, y)
+    with pytest.raises(ValueError, match="lse must be"):
+        ssa.window_bwd(w, x, y, y, {**f, "lse": f["lse"].double()}, x)

@@ -153,14 +153,7 @@ def test_tensor_helpers_check_shape_type_and_device():
         ssa.paged_decode(c, t, t, t, t, t)
     with pytest.raises(ValueError, match="CUDA"):
         ssa.cache_append(c, t, t, t, t, t, t)
-    dev = torch.device("cpu")
-    with pytest.raises(ValueError, match="shape"):
-        ssa._view4(t, "q", (1, 2, 9, 64), t.dtype, dev)
-    with pytest.raises(ValueError, match="bfloat16"):
-        ssa._view4(t, "q", t.shape, torch.bfloat16, dev)
-    with pytest.raises(ValueError, match="last axis"):
-        ssa._view4(t.transpose(2, 3), "q", (1, 2, 64, 8), t.dtype, dev)
-    with pytest.raises(ValueError, match="contiguous"):
-        ssa._plain(t.transpose(1, 2), "x", (1, 8, 2, 64), t.dtype, dev)
-    with pytest.raises(ValueError, match="pages"):
-        ssa._pages(c, torch.zeros(8, 2, 64, 64, dtype=torch.bfloat16), "k_pages", dev)
+    with pytest.raises(TypeError, match="tensor"):
+        ssa.window_fwd(p, None, t, t)
+    with pytest.raises(TypeError, match="structure"):
+        ssa.window_fwd(c, t, t, t)
