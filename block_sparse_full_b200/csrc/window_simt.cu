@@ -17,6 +17,8 @@
 // stretches whose parts window_parts_kernel sums in order.  (Two sequences of
 // 777 tokens, 4/2 heads of 64, window 128, 4 sinks: 92 us for both directions,
 // 332 us with one CTA to a key tile.)
+#include <cooperative_groups.h>
+
 #include "device_util.cuh"
 #include "ssa_internal.h"
 
@@ -179,87 +181,193 @@ struct KeyTiles {
 template <int D>
 constexpr size_t tile_floats() { return (size_t)BT * (D + 4); }
 
+// Forward: groups of D threads walk the key tiles in turn, each with its own
+// buffers, running maximum, sum and output, and are joined at the end in group
+// order.  A thread holds 8 rows x 64 / (D / 8) keys of the scores and 8 x 8 outputs.
+// Key and value tiles are on their way while the other is in use.  Where the
+// query tiles do not fill the SMs a cluster of CTAs shares one, tile by tile,
+// and reads the others' shares through distributed shared memory (1000 tokens, 2
+// heads of 64, window 256: 32 us with one CTA to a query tile, 18 with four).
+template <int D>
+struct Fwd {
+    static constexpr int kGroup = D, kGroups = D == 64 ? 4 : 2;  // threads of a group; groups
+    static constexpr int TX = D / 8, KT = BT / TX;               // key columns of threads; keys of a thread
+    static constexpr size_t kFloats = 2 * (size_t)BT * (D + 4) + BT * PP;  // K, V, P of a group
+    static constexpr size_t smem = (BT * (D + 4) + kGroups * kFloats) * sizeof(float);
+};
+
+// Rows t0 .. of one head -> shared memory, by the n threads of a group; rows from
+// len on are zero.  float32 is copied asynchronously, bf16 converted on the way.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2)
+__device__ __forceinline__ void stage(float* dst, const View& v, int b, int h, int t0, int len, int tid, int n) {
+    constexpr int kAll = BT * D / 4;
+    if constexpr (sizeof(T) == 4) {
+        for (int e = tid; e < kAll; e += n) {
+            const int r = e / (D / 4), c = 4 * (e % (D / 4));
+            const bool in = t0 + r < len;
+            const T* src = at<const T>(v, b, h, in ? t0 + r : 0) + c;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             static_cast<uint32_t>(__cvta_generic_to_shared(dst + r * (D + 4) + c))),
+                         "l"(src), "r"(in ? 16 : 0)
+                         : "memory");
+        }
+    } else {
+#pragma unroll 8
+        for (int e = tid; e < kAll; e += n) {
+            const int r = e / (D / 4), c = 4 * (e % (D / 4));
+            *reinterpret_cast<float4*>(dst + r * (D + 4) + c) =
+                t0 + r < len ? ld4(at<const T>(v, b, h, t0 + r) + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(Fwd<D>::kGroup* Fwd<D>::kGroups, 1)
 window_fwd_simt_kernel(const WinArgs a) {
+    using F = Fwd<D>;
+    constexpr int TX = F::TX, KT = F::KT, G = F::kGroups;
     extern __shared__ __align__(16) float sm[];
-    float *Q = sm, *KV = Q + tile_floats<D>(), *P = KV + tile_floats<D>();
-    const int t0 = blockIdx.x * BT, hq = blockIdx.y, b = blockIdx.z, hk = hq / a.G;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int group = threadIdx.x / F::kGroup, tid = threadIdx.x % F::kGroup;
+    float *Q = sm, *K = Q + BT * (D + 4) + group * F::kFloats, *V = K + BT * (D + 4), *P = V + BT * (D + 4);
+    auto sync = [group] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(F::kGroup) : "memory"); };
+    auto wait1 = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };
+    const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int cs = cluster.num_blocks(), rank = cluster.block_rank();
+    const int t0 = blockIdx.x / cs * BT, hq = blockIdx.y, b = blockIdx.z, hk = hq / a.G;
+    const int first = rank + cs * group, step = cs * G;  // this group's key tiles: CTAs first
+    const int tx = tid % TX, ty = tid / TX;  // rows ty + 8 i, keys tx + TX j
     const int len = seq_len(a, b);
-    float4 o[4][D / 64];
-    float m[4], l[4];
+    float4 o[8][2];
+    float m[8], l[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         m[i] = -INFINITY, l[i] = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     if (t0 < len) {
         const float sl2 = a.sm_scale * kLog2e;
         const KeyTiles kt(a, t0, min(t0 + BT, len) - 1);
-        Fetch<T, D> f;
-        f.load(a.q, b, hq, t0, len);
-        f.store(Q);
-        f.load(a.k, b, hk, kt.tile(0) * BT, len);
-        for (int j = 0; j < kt.n; ++j) {
+        stage<T, D>(Q, a.q, b, hq, t0, len, threadIdx.x, F::kGroup * G);
+        if (first < kt.n) {
+            stage<T, D>(K, a.k, b, hk, kt.tile(first) * BT, len, tid, F::kGroup);
+            stage<T, D>(V, a.v, b, hk, kt.tile(first) * BT, len, tid, F::kGroup);
+        }
+        // the queries are the oldest copies of every thread: there once the keys are
+        if (first < kt.n) wait1();
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        for (int j = first; j < kt.n; j += step) {
             const int s0 = kt.tile(j) * BT;
-            __syncthreads();  // the values of the tile before are used up
-            f.store(KV);
-            f.load(a.v, b, hk, s0, len);
-            __syncthreads();
-            float s[4][4];
-            scores<D>(Q, KV, ty, tx, s);
-            __syncthreads();
-            f.store(KV);
-            if (j + 1 < kt.n) f.load(a.k, b, hk, kt.tile(j + 1) * BT, len);
+            wait1();
+            sync();  // the keys are there
+            float s[8][KT];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = t0 + 4 * ty + i;
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int x = 0; x < KT; ++x) s[i][x] = 0.f;
+#pragma unroll 2
+            for (int d = 0; d < D; d += 4) {
+                float4 q[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[i] = ld4(Q + (ty + 8 * i) * (D + 4) + d);
+#pragma unroll
+                for (int x = 0; x < KT; ++x) {
+                    const float4 k = ld4(K + (tx + TX * x) * (D + 4) + d);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[i][x] = dot4(q[i], k, s[i][x]);
+                }
+            }
+            sync();  // the keys are used up
+            if (j + step < kt.n) stage<T, D>(K, a.k, b, hk, kt.tile(j + step) * BT, len, tid, F::kGroup);
+            else asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int t = t0 + ty + 8 * i;
                 float mx = -INFINITY;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    s[i][x] = sees(a, t, s0 + tx + 16 * x) ? s[i][x] * sl2 : -INFINITY;
+                for (int x = 0; x < KT; ++x) {
+                    s[i][x] = sees(a, t, s0 + tx + TX * x) ? s[i][x] * sl2 : -INFINITY;
                     mx = fmaxf(mx, s[i][x]);
                 }
 #pragma unroll
-                for (int sh = 1; sh < 16; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                for (int sh = 1; sh < TX; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
                 const float mn = fmaxf(m[i], mx), mz = mn == -INFINITY ? 0.f : mn;
                 const float al = exp2f(m[i] - mz);
                 m[i] = mn;
                 l[i] *= al;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    o[i][c].x *= al, o[i][c].y *= al, o[i][c].z *= al, o[i][c].w *= al;
-                }
+                for (int c = 0; c < 2; ++c) o[i][c].x *= al, o[i][c].y *= al, o[i][c].z *= al, o[i][c].w *= al;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                for (int x = 0; x < KT; ++x) {
                     const float p = exp2f(s[i][x] - mz);
                     l[i] += p;
-                    P[(4 * ty + i) * PP + tx + 16 * x] = p;
+                    P[(ty + 8 * i) * PP + tx + TX * x] = p;
                 }
             }
-            __syncthreads();
-            gather<D>(P, KV, ty, tx, o);
+            wait1();
+            sync();  // weights and values are there
+#pragma unroll 2
+            for (int n = 0; n < BT; n += 4) {
+                float4 w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = ld4(P + (ty + 8 * i) * PP + n);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float4 v = ld4(V + (n + k) * (D + 4) + 4 * tx + 4 * TX * c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) axpy((&w[i].x)[k], v, o[i][c]);
+                    }
+            }
+            sync();  // and used up
+            if (j + step < kt.n) stage<T, D>(V, a.v, b, hk, kt.tile(j + step) * BT, len, tid, F::kGroup);
+            else asm volatile("cp.async.commit_group;" ::: "memory");
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = t0 + 4 * ty + i;
-        float L = l[i];
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int sh = 1; sh < 16; sh <<= 1) L += __shfl_xor_sync(0xffffffffu, L, sh);
+        for (int sh = 1; sh < TX; sh <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], sh);
+    // every group's share goes over its own tiles
+    sync();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) *reinterpret_cast<float4*>(K + (ty + 8 * i) * (D + 4) + 4 * tx + 4 * TX * c) = o[i][c];
+        if (tx == 0) P[2 * (ty + 8 * i)] = m[i], P[2 * (ty + 8 * i) + 1] = l[i];
+    }
+    if (cs > 1) cluster.sync();
+    else __syncthreads();
+    // and the threads of all CTAs join them, four outputs each
+    constexpr int kAll = F::kGroup * G;
+    for (int e = rank * kAll + threadIdx.x; e < BT * D / 4; e += cs * kAll) {
+        const int r = e / (D / 4), c = 4 * (e % (D / 4)), t = t0 + r;
         if (t >= a.T) continue;
-        const bool row = t < len;
-        const float inv = row ? 1.f / L : 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            const float4 x = o[i][c];
-            st4(at<T>(a.h, b, hq, t) + 4 * tx + 64 * c,
-                row ? make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
+        float mx = -INFINITY, L = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < len) {
+            for (int g = 0; g < G; ++g)
+                for (int k = 0; k < cs; ++k) {
+                    const float* own = sm + BT * (D + 4) + g * F::kFloats;
+                    const float* base = k == rank ? own : cluster.map_shared_rank(own, k);
+                    const float2 ml = *reinterpret_cast<const float2*>(base + 2 * BT * (D + 4) + 2 * r);
+                    if (ml.x == -INFINITY) continue;
+                    const float mn = fmaxf(mx, ml.x), w0 = exp2f(mx - mn), w1 = exp2f(ml.x - mn);
+                    mx = mn;
+                    L = fmaf(L, w0, w1 * ml.y);
+                    x.x *= w0, x.y *= w0, x.z *= w0, x.w *= w0;
+                    axpy(w1, ld4(base + r * (D + 4) + c), x);
+                }
+            const float inv = 1.f / L;
+            x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
         }
-        if (tx == 0) a.lse[((size_t)b * a.Hq + hq) * a.T + t] = row ? (m[i] + log2f(L)) * kLn2 : -INFINITY;
+        st4(at<T>(a.h, b, hq, t) + c, x);
+        if (c == 0) a.lse[((size_t)b * a.Hq + hq) * a.T + t] = t < len ? (mx + log2f(L)) * kLn2 : -INFINITY;
     }
+    if (cs > 1) cluster.sync();  // the shares stay until every CTA has read them
 }
 
 // delta_t = dh_t . h_t, one warp per row
@@ -464,11 +572,27 @@ size_t part_bytes(const WinArgs& a, int D) {
 
 template <typename T, int D>
 int fwd(const WinArgs& a, cudaStream_t s) {
-    constexpr size_t smem = (2 * tile_floats<D>() + BT * PP) * sizeof(float);
+    static_assert(Fwd<D>::smem <= kMaxSmemPerCta, "shared memory");
     const int st = opt_in_max_smem<window_fwd_simt_kernel<T, D>>("window_fwd_simt_kernel");
     if (st != SSA_OK) return st;
-    const dim3 grid((unsigned)((a.T + BT - 1) / BT), (unsigned)a.Hq, (unsigned)a.B);
-    window_fwd_simt_kernel<T, D><<<grid, kThreads, smem, s>>>(a);
+    // CTAs of a query tile: while each has an SM and a key tile
+    const long long tiles = (a.T + BT - 1) / BT, ctas = tiles * a.Hq * a.B;
+    const long long keys = (a.window + BT - 1) / BT + 1 + (a.sinks + BT - 1) / BT;
+    int cs = 1;
+    while (cs < 8 && 2 * cs * ctas <= 148 && 2 * cs <= keys && 2 * cs <= tiles) cs *= 2;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(tiles * cs), (unsigned)a.Hq, (unsigned)a.B);
+    c.blockDim = dim3(Fwd<D>::kGroup * Fwd<D>::kGroups);
+    c.dynamicSmemBytes = Fwd<D>::smem;
+    c.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)cs;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&c, window_fwd_simt_kernel<T, D>, a);
+    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "window_fwd_simt_kernel: %s", cudaGetErrorString(e));
     return check_launch("window_fwd_simt_kernel");
 }
 
