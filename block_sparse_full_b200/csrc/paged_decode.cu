@@ -182,7 +182,10 @@ struct Rows<__nv_bfloat16, D, RG> {
     float o[D / 8][4];
     float m[2], l[2];  // rows lane / 4 and lane / 4 + 8; l is this thread's share
 
-    __device__ __forceinline__ void begin(const DecodeArgs& a, const Pass& p, int b, int h, int r0, float*) {
+    // the queries of a unit's rows (not needed by maxima() and add(): the loads of
+    // the next rows run while the last ones are joined)
+    static constexpr bool kEarly = true;
+    __device__ __forceinline__ void queries(const DecodeArgs& a, const Pass& p, int b, int h, int r0, float*) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -197,9 +200,11 @@ struct Rows<__nv_bfloat16, D, RG> {
                 for (int x = 0; x < 2; ++x)
                     q[k][i + 2 * x] =
                         src ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8 * x + 2 * (lane & 3)) : 0u;
-            m[i] = -INFINITY;
-            l[i] = 0.f;
         }
+    }
+    __device__ __forceinline__ void reset() {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
 #pragma unroll
@@ -280,6 +285,7 @@ struct Rows<__nv_bfloat16, D, RG> {
         const int lane = threadIdx.x & 31;
         if ((lane & 3) == 0) dst[lane >> 2] = m[0], dst[(lane >> 2) + 8] = m[1];
     }
+    // this warp's share of the rows, scaled to the common maximum: stored, or added to what is there
     __device__ __forceinline__ void add(float* sum, float* lsum, const float* top, bool first, int nr) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -310,7 +316,8 @@ struct Rows<float, D, RG> {
     float m[RG], l[RG];
     static constexpr int kCol = D / 4;  // lanes that hold the columns (32, or 16 twice)
 
-    __device__ __forceinline__ void begin(const DecodeArgs& a, const Pass& p, int b, int h, int r0, float* qs) {
+    static constexpr bool kEarly = false;
+    __device__ __forceinline__ void queries(const DecodeArgs& a, const Pass& p, int b, int h, int r0, float* qs) {
         __syncthreads();  // the unit before has done with qs
         for (int x = threadIdx.x; x < RG * D / 4; x += kThreads) {
             const int r = r0 + x / (D / 4), c = 4 * (x % (D / 4));
@@ -322,6 +329,8 @@ struct Rows<float, D, RG> {
             *reinterpret_cast<float4*>(qs + (x / (D / 4)) * D + c) = v;
         }
         __syncthreads();
+    }
+    __device__ __forceinline__ void reset() {
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
             m[g] = -INFINITY, l[g] = 0.f;
@@ -390,6 +399,7 @@ struct Rows<float, D, RG> {
 #pragma unroll
             for (int g = 0; g < RG; ++g) dst[g] = m[g];
     }
+    // this warp's share of the rows, scaled to the common maximum: stored, or added to what is there
     __device__ __forceinline__ void add(float* sum, float* lsum, const float* top, bool first, int nr) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -542,7 +552,8 @@ decode_kernel(const DecodeArgs a, const Pass p) {
     bool fresh = true;
     for (long long u = ubeg; u < uend; ++u) {
         if (fresh) {
-            rows.begin(a, p, cu.b, cu.hr / p.RT, (cu.hr % p.RT) * kRows, qs);
+            if (!decltype(rows)::kEarly || u == ubeg) rows.queries(a, p, cu.b, cu.hr / p.RT, (cu.hr % p.RT) * kRows, qs);
+            rows.reset();
             seg0 = u;
             fresh = false;
         }
@@ -565,6 +576,9 @@ decode_kernel(const DecodeArgs a, const Pass p) {
         const bool last = cu.t + 1 == cu.s.nt;
         if (last || u + 1 == uend) {
             // join the warps' shares, in warp order
+            Cursor nx = cu;
+            advance(nx);
+            if (decltype(rows)::kEarly && u + 1 < uend) rows.queries(a, p, nx.b, nx.hr / p.RT, (nx.hr % p.RT) * kRows, qs);
             const int r0 = (cu.hr % p.RT) * kRows, nr = min(kRows, p.R - r0);
             rows.maxima(maxs + warp * kRows);
             __syncthreads();
@@ -575,18 +589,38 @@ decode_kernel(const DecodeArgs a, const Pass p) {
                 top[threadIdx.x] = t;
             }
             __syncthreads();
-#pragma unroll 1
-            for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) rows.add(sum, lsum, top, w == 0, nr);
+            // up to four rows: every warp has room for its own share, else one after the other
+            const bool apart = nr <= kRows / kWarps;
+            if (apart) {
+                rows.add(sum + warp * 4 * D, lsum + warp * 4, top, true, nr);
                 __syncthreads();
+            } else {
+#pragma unroll 1
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w == warp) rows.add(sum, lsum, top, w == 0, nr);
+                    __syncthreads();
+                }
             }
+            auto out4 = [&](int x) -> float4 {  // 4 outputs of a row, x = their place in [row][D / 4]
+                float4 v = reinterpret_cast<const float4*>(sum)[x];
+                if (apart)
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) {
+                        const float4 y = reinterpret_cast<const float4*>(sum + w * 4 * D)[x];
+                        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+                    }
+                return v;
+            };
+            auto sum_of = [&](int r) -> float {
+                return apart ? (lsum[r] + lsum[4 + r]) + (lsum[8 + r] + lsum[12 + r]) : lsum[r];
+            };
             const bool whole = last && u - seg0 + 1 == cu.s.nt;
             const int hd = cu.hr / p.RT;
             if (whole && p.direct) {
                 for (int x = threadIdx.x; x < nr * D / 4; x += kThreads) {
                     const int r = x / (D / 4), c = 4 * (x % (D / 4));
-                    const float4 v = *reinterpret_cast<const float4*>(sum + r * D + c);
-                    const float inv = 1.f / lsum[r];
+                    const float4 v = out4(x);
+                    const float inv = 1.f / sum_of(r);
                     T* dst = static_cast<T*>(a.h.data) + (size_t)(cu.b + (r0 + r) / a.G) * a.h.sb +
                              (size_t)(hd * a.G + (r0 + r) % a.G) * a.h.sh + c;
                     if constexpr (sizeof(T) == 2) {
@@ -598,22 +632,24 @@ decode_kernel(const DecodeArgs a, const Pass p) {
                 if ((int)threadIdx.x < nr) {
                     const int r = r0 + threadIdx.x;
                     a.lse[(size_t)(cu.b + r / a.G) * a.Hq + hd * a.G + r % a.G] =
-                        (top[threadIdx.x] + log2f(lsum[threadIdx.x])) * kLn2;
+                        (top[threadIdx.x] + log2f(sum_of(threadIdx.x))) * kLn2;
                 }
             } else {
                 const size_t slot = whole ? 2 * (size_t)p.C + (size_t)cu.b * HR + cu.hr
                                           : 2 * (size_t)blockIdx.x + (seg0 > ubeg ? 1 : 0);
                 float* dst = p.part + slot * kRows * (D + 2);
                 for (int x = threadIdx.x; x < nr * D / 4; x += kThreads)
-                    reinterpret_cast<float4*>(dst)[x] = reinterpret_cast<const float4*>(sum)[x];
+                    reinterpret_cast<float4*>(dst)[x] = out4(x);
                 if ((int)threadIdx.x < nr)
                     *reinterpret_cast<float2*>(dst + kRows * D + 2 * threadIdx.x) =
-                        make_float2(top[threadIdx.x], lsum[threadIdx.x]);
+                        make_float2(top[threadIdx.x], sum_of(threadIdx.x));
             }
             fresh = true;
             __syncthreads();  // sum, top and lsum are free again
+            cu = nx;
+        } else {
+            advance(cu);
         }
-        advance(cu);
     }
     cp_wait<0>();
     // The pass over a shared prefix may still be running beside this one; the join
