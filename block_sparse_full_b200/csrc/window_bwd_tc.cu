@@ -29,17 +29,19 @@
 // P^T and dS^T go back to TMEM as bf16 (over the scores) and are the A
 // operands, Q and dO tiles (used K-major for the scores) the MN-major B
 // operands.  Sixteen softmax warps, four threads per key with 32 queries each.
-// Tiles of 64 queries in two TMEM buffers instead overlap as well on paper,
-// but read K and V from shared memory twice as often, and shared memory then
-// is what bounds them: XXX us against YYY us at T = 4096, window 1024, 32/8
-// heads, batch 4.
+// Bound by the chain S -> P -> dV, next S: the tensor cores are busy 45 % of the
+// time (610 us at T = 4096, window 1024, 32/8 heads, batch 4).  Tiles of 64 queries
+// in two TMEM buffers, two groups of warps in turn, overlap more but read K and V
+// from shared memory twice as often (612 us); P^T in shared memory, which frees S
+// earlier, adds 64 KB of such traffic to a tile and was 12 % slower.
 // A 128-key tile that holds sinks is seen by every later query; the queries
 // past the window's reach are split into stretches of about a CTA's usual
 // work, whose float32 parts are summed in order by window_sink_kernel.
 //
 // dQ: 256 TMEM columns (S 64, dP 64, dQ 128) and 112 KB, so two CTAs share the SM
 // and take turns on the tensor cores.  dS goes over dP, so that the next S is
-// formed as soon as the softmax has read the last (573 us -> YYY us).
+// formed as soon as the softmax has read the last, and the exponentials do not
+// wait for dP (573 us -> 436 us at the same shape).
 //
 // Rows and keys behind a sequence's length may be NaN: weights are selected, not
 // multiplied, to zero, and such rows of a tile are cleared in shared memory

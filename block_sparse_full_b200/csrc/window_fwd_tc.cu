@@ -7,13 +7,14 @@
 // over the key tiles j of 64 that some row of the tile sees.
 //
 // CTA = one query tile of one head, 192 threads, two CTAs on an SM:
-//   warp 0      TMA producer: Q once, then K_j and V_j into rings of two
+//   warp 0      TMA producer: Q once, then K_j into a ring of three and V_j into
+//               one of two
 //   warp 1      TMEM owner and MMA issuer (one thread)
 //   warps 2..5  softmax, a thread per row: it reads its 64 scores from TMEM
 //               into registers, forms P there and writes it back as bf16 over
 //               the scores.
 // TMEM: 256 of the 512 columns: S/P in two buffers of 64, O in [128, 128 + D);
-// shared memory: 96 KB.  The scores of tile j+1 are formed while the weights
+// shared memory: 112 KB.  The scores of tile j+1 are formed while the weights
 // of tile j are, and the product with V_j while those of tile j+1 are, so a
 // CTA's softmax does not wait for its products; the second CTA of the SM fills
 // the softmax's own latencies, the first loads and the last stores.  Tiles are
@@ -58,19 +59,23 @@ constexpr int kThreads = 192;
 constexpr uint32_t Q_BOX = BM * 128;  // [128 rows x 64 columns] bf16 box
 constexpr uint32_t KV_BOX = BN * 128; // [64 rows x 64 columns]
 constexpr uint32_t KV_BYTES = 2 * KV_BOX;
-constexpr uint32_t OFF_Q = 0, OFF_K = 2 * Q_BOX, OFF_V = OFF_K + 2 * KV_BYTES, OFF_BAR = OFF_V + 2 * KV_BYTES;
-enum : int {  // two of each but the first and the last: tile j uses number j % 2
-    B_QFULL, B_KFULL, B_KEMPTY = B_KFULL + 2, B_VFULL = B_KEMPTY + 2, B_VEMPTY = B_VFULL + 2, B_SREADY = B_VEMPTY + 2,
+constexpr int kK = 3;  // slots of K; V, the scores and their barriers have two
+constexpr uint32_t OFF_Q = 0, OFF_K = 2 * Q_BOX, OFF_V = OFF_K + kK * KV_BYTES, OFF_BAR = OFF_V + 2 * KV_BYTES;
+enum : int {  // one of Q, kK of K, two of the others: tile j uses number j % 2
+    B_QFULL, B_KFULL, B_KEMPTY = B_KFULL + kK, B_VFULL = B_KEMPTY + kK, B_VEMPTY = B_VFULL + 2, B_SREADY = B_VEMPTY + 2,
     B_PREADY = B_SREADY + 2, B_DRAIN = B_PREADY + 2, B_COUNT
 };
 constexpr uint32_t OFF_MISC = OFF_BAR + B_COUNT * 8;  // [0] tmem base, [1] abort flag
-constexpr uint32_t SMEM_BYTES = OFF_MISC + 16 + 1024;  // slack for 1024-byte alignment
+// two CTAs and their 1 KB of system memory each in the SM's 228 KB: no room to
+// round the base up, it is 1024-byte aligned by declaration (and checked)
+constexpr uint32_t SMEM_BYTES = OFF_MISC + 16;
+static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
 constexpr int kPrefixCtas = 296, kPrefixTiles = 2;  // CTAs of a pass over a prefix, at least so many key tiles each
 constexpr uint32_t TM_S = 0, TM_O = 128, kTmemCols = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.693147180559945309f;
 
-__device__ unsigned int g_attn_tc_status;   // bit 0: a wait expired
+__device__ unsigned int g_attn_tc_status;   // bit 0: a wait expired, bit 1: misaligned shared memory
 __device__ unsigned int g_attn_tc_range;    // a length (1) or page number (2) was out of range
 
 struct AttnArgs {
@@ -102,10 +107,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k16,
                const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ CUtensorMap tm_h,
                const AttnArgs a) {
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t* gbase = smem_raw + (base - raw);
+    extern __shared__ __align__(1024) uint8_t smem_tiles[];
+    uint8_t* gbase = smem_tiles;
+    const uint32_t base = smem_u32(smem_tiles);
+    if (base & 1023u) {  // not reached: the tiles' swizzle needs the alignment
+        if (threadIdx.x == 0) atomicOr(&g_attn_tc_status, 2u);
+        return;
+    }
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + OFF_MISC + 4);
     unsigned int* status = &g_attn_tc_status;
     const uint64_t lim = a.timeout_ns;
@@ -184,22 +192,27 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
         }
         __syncwarp();
+        // the pages of tile j, one to a lane
+        auto page_of = [&](int j) -> int {
+            int pg = 0;
+            if constexpr (kPrefix) {
+                const int s0 = tile_key(j), step = min(BN, a.page);
+                if (j < nt && lane < BN / step && s0 + lane * step < len) pg = a.pages[(s0 + lane * step) / a.page];
+            }
+            return pg;
+        };
         // one K or V tile: whole boxes, the sinks' 16-row steps, or a box per page
-        auto load = [&](bool is_k, int j) {
+        auto load = [&](bool is_k, int j, int pg) {
             const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-            const uint32_t bar = BAR((is_k ? B_KFULL : B_VFULL) + (j & 1));
-            const uint32_t dst = base + (is_k ? OFF_K : OFF_V) + (j & 1) * KV_BYTES;
+            const uint32_t bar = BAR(is_k ? B_KFULL + j % kK : B_VFULL + (j & 1));
+            const uint32_t dst = base + (is_k ? OFF_K + j % kK * KV_BYTES : OFF_V + (j & 1) * KV_BYTES);
             const int s0 = tile_key(j), keys = tile_keys(j);
             if constexpr (kPrefix) {
                 const int step = min(BN, a.page);  // rows of a box
                 const int np = min(BN / step, (len - s0 + step - 1) / step);
-                int pg = 0;
-                if (lane < np) {
-                    pg = a.pages[(s0 + lane * step) / a.page];
-                    if (pg < 0 || pg >= a.n_pages) {
-                        atomicOr(&g_attn_tc_range, 2u);
-                        pg = 0;
-                    }
+                if (lane < np && (pg < 0 || pg >= a.n_pages)) {
+                    atomicOr(&g_attn_tc_range, 2u);
+                    pg = 0;
                 }
                 if (lane == 0) mbar_expect_tx(bar, (uint32_t)(np * step) * D * 2);
                 __syncwarp();
@@ -222,19 +235,34 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             __syncwarp();
         };
-        int nk = 0, nv = 0;
+        // K runs kK tiles ahead of V: behind V_j in line, K_j+1 would be asked for only
+        // one tile before its scores are due
+        int nk = 0, nv = 0, pg[kK + 1];
+#pragma unroll
+        for (int i = 0; i <= kK; ++i) pg[i] = page_of(i);
+#pragma unroll
+        for (int i = 0; i < kK; ++i)
+            if (i < nt) {
+                load(true, i, pg[i]);
+                nk = i + 1;
+            }
         for (int j = 0; j < nt; ++j) {
-            const uint32_t ph = ((j >> 1) + 1) & 1;
-            if (j > 1 && !__all_sync(FULL, mbar_wait(BAR(B_KEMPTY + (j & 1)), ph, abort_flag, status, lim))) break;
-            load(true, j);
-            nk = j + 1;
-            if (j > 1 && !__all_sync(FULL, mbar_wait(BAR(B_VEMPTY + (j & 1)), ph, abort_flag, status, lim))) break;
-            load(false, j);
+            if (j > 1 && !__all_sync(FULL, mbar_wait(BAR(B_VEMPTY + (j & 1)), ((j >> 1) + 1) & 1, abort_flag, status, lim))) break;
+            load(false, j, pg[0]);
             nv = j + 1;
+            const int jk = j + kK;
+            if (jk < nt) {
+                if (!__all_sync(FULL, mbar_wait(BAR(B_KEMPTY + jk % kK), (jk / kK + 1) & 1, abort_flag, status, lim))) break;
+                load(true, jk, pg[kK]);
+                nk = jk + 1;
+            }
+#pragma unroll
+            for (int i = 0; i < kK; ++i) pg[i] = pg[i + 1];
+            pg[kK] = page_of(jk + 1);  // (not looked at before it is used: nothing waits for it here)
         }
         // copies in flight land before the CTA ends, also where a wait gave up
         if (nt > 0) wait_drain(BAR(B_QFULL), 0);
-        for (int j = max(0, nk - 2); j < nk; ++j) wait_drain(BAR(B_KFULL + (j & 1)), (j >> 1) & 1);
+        for (int j = max(0, nk - kK); j < nk; ++j) wait_drain(BAR(B_KFULL + j % kK), (j / kK) & 1);
         for (int j = max(0, nv - 2); j < nv; ++j) wait_drain(BAR(B_VFULL + (j & 1)), (j >> 1) & 1);
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
@@ -246,17 +274,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             return __all_sync(FULL, mbar_wait(BAR(bar + (j & 1)), (j >> 1) & 1, abort_flag, status, lim));
         };
         auto scores = [&](int j) -> bool {  // S = Q K_j^T, behind the product that reads P from the same columns
-            if (!wait(B_KFULL, j)) return false;
+            if (!__all_sync(FULL, mbar_wait(BAR(B_KFULL + j % kK), (j / kK) & 1, abort_flag, status, lim))) return false;
             fence_after_sync();
             const uint32_t idesc_qk = idesc_bf16_f32(BM, tile_keys(j), false);
-            const uint64_t kd = desc_add(kdesc, (j & 1) * KV_BYTES);
+            const uint64_t kd = desc_add(kdesc, j % kK * KV_BYTES);
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_ss(tmem + TM_S + BN * (j & 1), desc_add(qdesc, (kk >> 2) * Q_BOX + (kk & 3) * 32),
                            desc_add(kd, (kk >> 2) * KV_BOX + (kk & 3) * 32), idesc_qk, kk > 0 ? 1u : 0u);
                 mma_commit(BAR(B_SREADY + (j & 1)));
-                mma_commit(BAR(B_KEMPTY + (j & 1)));
+                mma_commit(BAR(B_KEMPTY + j % kK));
             }
             __syncwarp();
             return true;
@@ -615,7 +643,8 @@ int attn_tc_take_status() {
     const unsigned int zero = 0;
     if (v) {
         cudaMemcpyToSymbol(g_attn_tc_status, &zero, sizeof zero);
-        return fail(SSA_ERR_TIMEOUT, "attn_tc_kernel: a bounded mbarrier wait expired");
+        return v & 1u ? fail(SSA_ERR_TIMEOUT, "attn_tc_kernel: a bounded mbarrier wait expired")
+                      : fail(SSA_ERR_CUDA, "attn_tc_kernel: shared memory is not aligned");
     }
     if (w) {
         cudaMemcpyToSymbol(g_attn_tc_range, &zero, sizeof zero);
