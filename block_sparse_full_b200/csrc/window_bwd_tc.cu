@@ -8,11 +8,12 @@
 // Four launches (five with sinks that the window leaves behind):
 //   window_rows_kernel   -lse log2 e and -delta of every row, padded to whole
 //                        tiles: one pass over dO and h, bound by reading them
+//   window_dq_kernel     a CTA per query tile of 128 walks the key tiles of 64:
+//                        three products per tile (up to 128 keys to a row it walks
+//                        them twice, first for delta)
 //   window_dkdv_kernel   a CTA per key tile of 128 and key/value head walks the
 //                        query tiles of 128 that see it, for each query head of
 //                        its group in turn: four products per tile
-//   window_dq_kernel     a CTA per query tile of 128 walks the key tiles of 64:
-//                        three products per tile
 //   window_sink_kernel   sums the parts of the first key tile (below)
 // S and dP are formed in both kernels: seven products instead of five, but every sum
 // has one owner and a fixed order, without atomics, and without a dS of T x
@@ -74,6 +75,7 @@ struct BwdArgs {
     const float* nlse;    // [B, Hq, Tp]: -lse log2 e
     const float* ndelta;  // [B, Hq, Tp]: -delta
     float* part;          // [B, Hkv, 1 + splits][dK, dV][128][D], with sinks out of reach
+    bool sweep;           // dQ walks the keys twice, first for delta
     int B, Hq, Hkv, G, T, Tp, window, sinks, nt;  // nt: tiles of 128
     int splits;           // stretches of queries past the reach of key tile 0
     float scale, scale_log2;
@@ -135,7 +137,7 @@ window_rows_kernel(const View h, const View dh, const float* lse, float* nlse, f
     if (t >= a.Tp) return;  // (Tp is a multiple of the rows of a block: whole blocks)
     const bool row = t < seq_len(a, b);
     float s = 0.f;
-    if (row) {
+    if (row && !a.sweep) {
         const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(h.data) + (size_t)b * h.sb +
                                                         (size_t)hq * h.sh + (size_t)t * h.st + c);
         const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(dh.data) + (size_t)b * dh.sb +
@@ -501,13 +503,16 @@ constexpr uint32_t Q_OFF_Q = 0, Q_OFF_DO = TILE_M, Q_OFF_K = 2 * TILE_M, Q_OFF_V
 constexpr uint32_t Q_OFF_BAR = Q_OFF_V + TILE_N;
 enum : int { QB_Q, QB_KFULL, QB_KEMPTY = QB_KFULL + 2, QB_VFULL = QB_KEMPTY + 2, QB_VEMPTY, QB_SREADY, QB_DPREADY, QB_SFREE, QB_DSREADY, QB_DRAIN, QB_COUNT };
 constexpr uint32_t Q_OFF_MISC = Q_OFF_BAR + QB_COUNT * 8;
-constexpr uint32_t Q_SMEM = Q_OFF_MISC + 16;
+constexpr uint32_t Q_OFF_SUM = Q_OFF_MISC + 16;  // [row] float
+constexpr uint32_t Q_SMEM = Q_OFF_SUM + BM * 4;
 // two CTAs and their 1 KB of system memory each in the SM's 228 KB: no room to
 // round the base up, it is 1024-byte aligned by declaration (and checked)
 static_assert(2 * (Q_SMEM + 1024) <= 233472, "two CTAs per SM");
 constexpr uint32_t TQ_S = 0, TQ_DP = 64, TQ_DQ = 128;
 
-template <int D>
+// kSweep: the key tiles are walked twice, first for delta_t = sum_s P_ts dP_ts
+// (which also replaces the one from h, for the dK/dV kernel after this one).
+template <int D, bool kSweep>
 __global__ void __launch_bounds__(kThreads, 2)
 window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -537,8 +542,17 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ns = min((a.sinks + BN - 1) / BN, w0);
         nt = ns + (min(t0 + BM, len) - 1) / BN + 1 - w0;
     }
-    auto tile_key = [&](int j) { return (j < ns ? j : w0 + j - ns) * BN; };
-    auto tile_keys = [&](int j) { return j < ns ? min(BN, (a.sinks - j * BN + 15) & ~15) : BN; };
+    const int once = nt;  // tiles of a sweep
+    if constexpr (kSweep) nt *= 2;
+    auto tile_of = [&](int j) { return kSweep && j >= once ? j - once : j; };
+    auto tile_key = [&](int j) {
+        const int x = tile_of(j);
+        return (x < ns ? x : w0 + x - ns) * BN;
+    };
+    auto tile_keys = [&](int j) {
+        const int x = tile_of(j);
+        return x < ns ? min(BN, (a.sinks - x * BN + 15) & ~15) : BN;
+    };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < QB_COUNT; ++i) mbar_init(BAR(i), i == QB_DSREADY || i == QB_SFREE ? kSoftmax : 1);
@@ -643,10 +657,11 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             fence_after_sync();
             const uint64_t kd = desc_add(kmdesc, (j & 1) * TILE_N);
             const int steps = tile_keys(j) / 16;
+            const int j0 = kSweep ? once : 0;  // the tile whose product comes first
             if (elect_one()) {
-                for (int kk = 0; kk < steps; ++kk)
+                for (int kk = 0; kk < steps && j >= j0; ++kk)
                     mma_ts(tmem + TQ_DQ, tmem + TQ_DP + 32 * (kk >> 1) + 8 * (kk & 1), desc_add(kd, kk * 2048), idesc_g,
-                           j > 0 || kk > 0 ? 1u : 0u);
+                           j > j0 || kk > 0 ? 1u : 0u);
                 mma_commit(BAR(QB_KEMPTY + (j & 1)));
             }
             __syncwarp();
@@ -662,10 +677,25 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
         const int t = t0 + r, c0 = 32 * half;
         const size_t row = ((size_t)b * a.Hq + hq) * a.Tp + t;  // (rows are padded to whole tiles)
-        const float nl = a.nlse[row], nd = a.ndelta[row];
-        const f32x2 sl = mk2(a.scale_log2, a.scale_log2), nl2 = mk2(nl, nl), nd2 = mk2(nd, nd);
-        bool ok = true;
+        const float nl = a.nlse[row], nd = kSweep ? 0.f : a.ndelta[row];
+        const f32x2 sl = mk2(a.scale_log2, a.scale_log2), nl2 = mk2(nl, nl);
+        f32x2 nd2 = mk2(nd, nd);
+        float delta = 0.f;  // kSweep: sum of P dP over this half of the first sweep
+        float* sums = reinterpret_cast<float*>(gbase + Q_OFF_SUM);
+        bool ok = true, voted = false;
         for (int j = 0; j < nt; ++j) {
+            if (kSweep && j == once) {  // the halves of delta, in order; the second sweep takes it, and dK/dV
+                if (half == 1) sums[r] = delta;
+                if (!bar_and(true, 1, kSoftmax)) {  // a warp has given up: this was the vote below
+                    ok = false, voted = true;
+                    break;
+                }
+                if (half == 0) sums[r] += delta;
+                bar_sync(1, kSoftmax);
+                const float d = -sums[r];
+                nd2 = mk2(d, d);
+                if (half == 0) const_cast<float*>(a.ndelta)[row] = d;
+            }
             const int s0 = tile_key(j), keys = tile_keys(j);
             ok = wait(QB_SREADY, j);
             if (!ok) break;
@@ -717,10 +747,13 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         if (!(bits >> c & 1u)) e0 = 0.f;
                         if (!(bits >> (c + 1) & 1u)) e1 = 0.f;
                     }
+                    if (kSweep && j < once) delta += e0 + e1;
                     pk[c / 2] = pack_bf16(e0, e1);
                 }
-                tmem_st<16>(td, pk);
-                tmem_wait_st();
+                if (!kSweep || j >= once) {
+                    tmem_st<16>(td, pk);
+                    tmem_wait_st();
+                }
             } else {
                 // nothing of the tile is here, but an arrival before the barrier's
                 // phase has begun would count for the tile before
@@ -731,7 +764,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_arrive(BAR(QB_DSREADY));
         }
         if (ok) ok = wait(QB_DRAIN, 0);
-        ok = bar_and(ok && !*abort_flag, 1, kSoftmax);
+        if (!voted) ok = bar_and(ok && !*abort_flag, 1, kSoftmax);
         fence_after_sync();
         if (ok) {
 #pragma unroll 1
@@ -756,6 +789,13 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tmem_dealloc(tmem, 256);
     }
 }
+
+// Up to so many keys to a row delta comes from a sweep of its own in dQ, not from
+// dh . h: h was rounded to bf16, and with few keys it is so large that the error
+// counts beside the rounding of dS (relative error of dq and dk against 64 bits
+// at T = 206, window 30, 0.0026 from h and 0.0024 from the sweep; with 1024 keys 0.0024
+// from h).  The sweep adds two products of three to a tile.
+constexpr int kSweepKeys = 128;
 
 // Shape of a call: padded rows, reach and stretches of the first key tile.
 struct Plan {
@@ -785,7 +825,8 @@ template <int D>
 int run(const ssa_window_params_t& p, const View& q, const View& k, const View& v, const View& h, const float* lse,
         const View& dh, const View& dq, const View& dk, const View& dv, BwdArgs a, cudaStream_t s) {
     int st = opt_in_max_smem<window_dkdv_kernel<D>>("window_dkdv_kernel");
-    if (st == SSA_OK) st = opt_in_max_smem<window_dq_kernel<D>>("window_dq_kernel");
+    if (st == SSA_OK) st = opt_in_max_smem<window_dq_kernel<D, false>>("window_dq_kernel");
+    if (st == SSA_OK) st = opt_in_max_smem<window_dq_kernel<D, true>>("window_dq_kernel");
     CUtensorMap k128, v128, mdk, mdv, q128, do128, k64, v64, k16, v16, mdq;
     struct { CUtensorMap* m; const View* x; int H, rows; } maps[] = {
         {&k128, &k, p.Hkv, BM}, {&v128, &v, p.Hkv, BM},
@@ -798,11 +839,13 @@ int run(const ssa_window_params_t& p, const View& q, const View& k, const View& 
     constexpr int rows = 256 / (D / 8);
     window_rows_kernel<D><<<dim3((unsigned)(a.Tp / rows), (unsigned)p.Hq, (unsigned)p.B), 256, 0, s>>>(
         h, dh, lse, const_cast<float*>(a.nlse), const_cast<float*>(a.ndelta), a);
+    const unsigned tiles = (unsigned)p.B * p.Hq * a.nt;
+    if (a.sweep) window_dq_kernel<D, true><<<tiles, kThreads, Q_SMEM, s>>>(q128, do128, k64, v64, k16, v16, mdq, a);
+    else window_dq_kernel<D, false><<<tiles, kThreads, Q_SMEM, s>>>(q128, do128, k64, v64, k16, v16, mdq, a);
     const unsigned items = (unsigned)p.B * p.Hkv * (a.nt + a.splits);
     window_dkdv_kernel<D><<<items, kThreadsK, K_SMEM, s>>>(q128, do128, k128, v128, mdk, mdv, a);
     if (a.splits)
         window_sink_kernel<D><<<dim3(2u * p.B * p.Hkv, (unsigned)(BM * D / 4 / 256)), 256, 0, s>>>(dk, dv, a);
-    window_dq_kernel<D><<<(unsigned)p.B * p.Hq * a.nt, kThreads, Q_SMEM, s>>>(q128, do128, k64, v64, k16, v16, mdq, a);
     return check_launch("window backward (tensor cores)");
 }
 
@@ -825,6 +868,7 @@ int launch_window_bwd_tc(const ssa_window_params_t& p, const View& q, const View
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * x.rows);
     a.B = p.B, a.Hq = p.Hq, a.Hkv = p.Hkv, a.G = p.Hq / p.Hkv, a.T = p.T, a.Tp = x.Tp;
     a.window = x.window, a.sinks = x.sinks, a.nt = x.nt, a.splits = x.splits;
+    a.sweep = x.window <= kSweepKeys;
     a.scale = p.sm_scale, a.scale_log2 = p.sm_scale * kLog2e;
     a.timeout_ns = wait_limit_ns();
     return p.D == 64 ? run<64>(p, q, k, v, h, lse, dh, dq, dk, dv, a, s)

@@ -16,7 +16,9 @@
 // for tiles that hold sinks (every later query sees them), is cut into
 // stretches whose parts window_parts_kernel sums in order.  (Two sequences of
 // 777 tokens, 4/2 heads of 64, window 128, 4 sinks: 92 us for both directions,
-// 332 us with one CTA to a key tile.)
+// 332 us with one CTA to a key tile.)  Clusters of CTAs share a query tile of dq
+// as they do in the forward (976 tokens, 4/2 heads of 128, all keys: 258 us for
+// both directions, 365 us without).
 #include <cooperative_groups.h>
 
 #include "device_util.cuh"
@@ -409,7 +411,10 @@ window_dq_simt_kernel(const WinArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr size_t N = tile_floats<D>();
     float *Q = sm, *dO = Q + N, *K = dO + N, *V = K + N, *dS = V + N;
-    const int t0 = blockIdx.x * BT, hq = blockIdx.y, b = blockIdx.z, hk = hq / a.G;
+    // (a cluster shares a query tile as in the forward)
+    const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int cs = cluster.num_blocks(), rank = cluster.block_rank();
+    const int t0 = blockIdx.x / cs * BT, hq = blockIdx.y, b = blockIdx.z, hk = hq / a.G;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int len = seq_len(a, b);
     const float* lse = a.lse + ((size_t)b * a.Hq + hq) * a.T;
@@ -426,7 +431,7 @@ window_dq_simt_kernel(const WinArgs a) {
         f.store(Q);
         f.load(a.dh, b, hq, t0, len);
         f.store(dO);
-        for (int j = 0; j < kt.n; ++j) {
+        for (int j = rank; j < kt.n; j += cs) {
             const int s0 = kt.tile(j) * BT;
             __syncthreads();
             f.load(a.k, b, hk, s0, len);
@@ -441,6 +446,26 @@ window_dq_simt_kernel(const WinArgs a) {
             __syncthreads();
             gather<D>(dS, K, ty, tx, o);
         }
+    }
+    if (cs > 1) {  // sums in the order of the ranks, the rows of a tile spread over the CTAs
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) *reinterpret_cast<float4*>(Q + (4 * ty + i) * (D + 4) + 4 * tx + 64 * c) = o[i][c];
+        cluster.sync();
+        for (int e = rank * kThreads + threadIdx.x; e < BT * D / 4; e += cs * kThreads) {
+            const int r = e / (D / 4), c = 4 * (e % (D / 4));
+            if (t0 + r >= a.T) continue;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < cs; ++k) {
+                const float4 y = ld4(cluster.map_shared_rank(Q, k) + r * (D + 4) + c);
+                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+            }
+            st4(at<T>(a.dq, b, hq, t0 + r) + c, x);
+        }
+        cluster.sync();  // the shares stay until every CTA has read them
+        return;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -570,20 +595,24 @@ size_t part_bytes(const WinArgs& a, int D) {
     return (size_t)a.B * a.Hkv * first_slot(a, (a.T + BT - 1) / BT) * 2 * BT * D * sizeof(float);
 }
 
-template <typename T, int D>
-int fwd(const WinArgs& a, cudaStream_t s) {
-    static_assert(Fwd<D>::smem <= kMaxSmemPerCta, "shared memory");
-    const int st = opt_in_max_smem<window_fwd_simt_kernel<T, D>>("window_fwd_simt_kernel");
-    if (st != SSA_OK) return st;
-    // CTAs of a query tile: while each has an SM and a key tile
+// CTAs that share a query tile: as long as each has an SM (windows, whose tiles
+// are alike; with all keys the late tiles are the longest and three CTAs to an SM
+// even out) and a key tile.
+int cluster_of(const WinArgs& a) {
     const long long tiles = (a.T + BT - 1) / BT, ctas = tiles * a.Hq * a.B;
     const long long keys = (a.window + BT - 1) / BT + 1 + (a.sinks + BT - 1) / BT;
+    const long long most = 2 * (long long)a.window > a.T ? 444 : 148;
     int cs = 1;
-    while (cs < 8 && 2 * cs * ctas <= 148 && 2 * cs <= keys && 2 * cs <= tiles) cs *= 2;
+    while (cs < 8 && 2 * cs * ctas <= most && 2 * cs <= keys && 2 * cs <= tiles) cs *= 2;
+    return cs;
+}
+template <typename K>
+int launch_clusters(const char* what, K* kernel, const WinArgs& a, int threads, size_t smem, cudaStream_t s) {
+    const int cs = cluster_of(a);
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)(tiles * cs), (unsigned)a.Hq, (unsigned)a.B);
-    c.blockDim = dim3(Fwd<D>::kGroup * Fwd<D>::kGroups);
-    c.dynamicSmemBytes = Fwd<D>::smem;
+    c.gridDim = dim3((unsigned)((a.T + BT - 1) / BT * cs), (unsigned)a.Hq, (unsigned)a.B);
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
     c.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -591,9 +620,18 @@ int fwd(const WinArgs& a, cudaStream_t s) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     c.attrs = &at;
     c.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&c, window_fwd_simt_kernel<T, D>, a);
-    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "window_fwd_simt_kernel: %s", cudaGetErrorString(e));
-    return check_launch("window_fwd_simt_kernel");
+    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, a);
+    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return check_launch(what);
+}
+
+template <typename T, int D>
+int fwd(const WinArgs& a, cudaStream_t s) {
+    static_assert(Fwd<D>::smem <= kMaxSmemPerCta, "shared memory");
+    const int st = opt_in_max_smem<window_fwd_simt_kernel<T, D>>("window_fwd_simt_kernel");
+    if (st != SSA_OK) return st;
+    return launch_clusters("window_fwd_simt_kernel", window_fwd_simt_kernel<T, D>, a, Fwd<D>::kGroup * Fwd<D>::kGroups,
+                           Fwd<D>::smem, s);
 }
 
 template <typename T, int D>
@@ -611,8 +649,9 @@ int bwd(const WinArgs& a, cudaStream_t s) {
     if (a.cuts > 1 || a.sink_cuts > 1)
         window_parts_kernel<T, D><<<dim3((a.cuts > 1 ? nt : (unsigned)a.nsink) * (2 * BT * D / 4 / kThreads), (unsigned)a.Hkv,
                                           (unsigned)a.B), kThreads, 0, s>>>(a);
-    window_dq_simt_kernel<T, D><<<dim3(nt, (unsigned)a.Hq, (unsigned)a.B), kThreads, smem_q, s>>>(a);
-    return check_launch("window backward (CUDA cores)");
+    st = check_launch("window backward (CUDA cores)");
+    if (st != SSA_OK) return st;
+    return launch_clusters("window_dq_simt_kernel", window_dq_simt_kernel<T, D>, a, kThreads, smem_q, s);
 }
 
 }  // namespace
