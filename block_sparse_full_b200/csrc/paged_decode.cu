@@ -884,7 +884,8 @@ long long seen_most(const ssa_cache_params_t& p) {
 
 size_t paged_decode_workspace(const ssa_cache_params_t& p, int prefix_len) {
     const int G = p.Hq / p.Hkv, RT = row_tiles(G), tk = tile_keys(p);
-    size_t n = pass_bytes(pass_ctas(p.B, p.Hkv, RT, seen_most(p), tk), (long long)p.B * p.Hkv * RT, p.D);
+    // (without a prefix a row tile that one CTA holds is written to the output)
+    size_t n = pass_bytes(pass_ctas(p.B, p.Hkv, RT, seen_most(p), tk), prefix_len > 0 ? (long long)p.B * p.Hkv * RT : 0, p.D);
     if (prefix_len > 0 && prefix_tc_supported(p)) {
         n += align_up(prefix_tc_plan(p, prefix_len).bytes, 256);
     } else if (prefix_len > 0) {

@@ -25,24 +25,34 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 constexpr size_t kMaxSmemPerCta = 232448;
 
 // Lets kernel K take dynamic shared memory up to the per-CTA maximum less its
-// static shared memory (once per process; launches above the default 48 KB
-// of dynamic plus static shared memory fail without it).  Call it before any
-// stream capture.  Returns an SSA status; *dyn_limit receives the limit.
+// static shared memory (once per process and device; launches above the default
+// 48 KB of dynamic plus static shared memory fail without it).  Call it before
+// any stream capture.  Returns an SSA status; *dyn_limit receives the limit.
 template <auto K>
 int opt_in_max_smem(const char* what, size_t* dyn_limit = nullptr) {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    static size_t limit = 0;
-    std::call_once(once, [] {
+    constexpr int kDevices = 64;
+    struct State {
+        std::once_flag once;
+        cudaError_t err = cudaSuccess;
+        size_t limit = 0;
+    };
+    static State states[kDevices];
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    if (dev >= kDevices) return fail(SSA_ERR_UNSUPPORTED, "%s: device %d of more than %d", what, dev, kDevices);
+    State& s = states[dev];
+    std::call_once(s.once, [&s] {
         cudaFuncAttributes fa;
-        err = cudaFuncGetAttributes(&fa, K);
-        if (err == cudaSuccess) {
-            limit = kMaxSmemPerCta - fa.sharedSizeBytes;
-            err = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
+        s.err = cudaFuncGetAttributes(&fa, K);
+        if (s.err == cudaSuccess) {
+            s.limit = kMaxSmemPerCta - fa.sharedSizeBytes;
+            s.err = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.limit);
         }
     });
-    if (dyn_limit) *dyn_limit = limit;
-    if (err != cudaSuccess) return fail(SSA_ERR_CUDA, "%s: shared memory attribute: %s", what, cudaGetErrorString(err));
+    if (dyn_limit) *dyn_limit = s.limit;
+    if (s.err != cudaSuccess)
+        return fail(SSA_ERR_CUDA, "%s: shared memory attribute: %s", what, cudaGetErrorString(s.err));
     return SSA_OK;
 }
 

@@ -9,7 +9,7 @@
 //   window_rows_kernel   -lse log2 e and -delta of every row, padded to whole
 //                        tiles: one pass over dO and h, bound by reading them
 //   window_dq_kernel     a CTA per query tile of 128 walks the key tiles of 64:
-//                        three products per tile (up to 128 keys to a row it walks
+//                        three products per tile (where rows see few keys it walks
 //                        them twice, first for delta)
 //   window_dkdv_kernel   a CTA per key tile of 128 and key/value head walks the
 //                        query tiles of 128 that see it, for each query head of
@@ -74,13 +74,19 @@ struct BwdArgs {
     const int32_t* lens;
     const float* nlse;    // [B, Hq, Tp]: -lse log2 e
     const float* ndelta;  // [B, Hq, Tp]: -delta
-    float* part;          // [B, Hkv, 1 + splits][dK, dV][128][D], with sinks out of reach
-    bool sweep;           // dQ walks the keys twice, first for delta
+    float* part;          // per head, with sinks out of reach: [dK, dV][128][D], then splits x [dK, dV][sinks][D]
+    bool sweep;           // every query tile of dQ sweeps the keys for delta first
     int B, Hq, Hkv, G, T, Tp, window, sinks, nt;  // nt: tiles of 128
     int splits;           // stretches of queries past the reach of key tile 0
     float scale, scale_log2;
     unsigned long long timeout_ns;
 };
+
+// Floats before part i (0: the queries in reach) of head bh.
+__host__ __device__ __forceinline__ size_t part_offset(const BwdArgs& a, int bh, int i, int D) {
+    const size_t head = 2 * (size_t)D * (BM + (size_t)a.splits * a.sinks);
+    return bh * head + (i > 0 ? 2 * (size_t)D * (BM + (size_t)(i - 1) * a.sinks) : 0);
+}
 
 __device__ __forceinline__ int seq_len(const BwdArgs& a, int b) {
     if (!a.lens) return a.T;
@@ -433,16 +439,17 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         fence_after_sync();
         const bool parts = a.splits > 0 && J == 0;
         if (ok && parts) {
-            float* slot = a.part + ((size_t)bh * (1 + a.splits) + (item < a.nt ? 0 : 1 + item - a.nt)) * 2 * BM * D;
+            const int rows = item < a.nt ? BM : a.sinks;  // (far queries see the sinks alone)
+            float* slot = a.part + part_offset(a, bh, item < a.nt ? 0 : 1 + item - a.nt, D);
 #pragma unroll 1
             for (int x = 0; x < D / 64; ++x) {  // two parts for dK, two for dV
                 const int w = part >> 1, col = (D / 2) * (part & 1) + 32 * x;
                 uint32_t u[32];
                 tmem_ld32(trow + (w ? TK_DV : TK_DK) + col, u);
                 tmem_wait_ld();
-                float4* dst = reinterpret_cast<float4*>(slot + ((size_t)w * BM + r) * D + col);
+                float4* dst = reinterpret_cast<float4*>(slot + ((size_t)w * rows + r) * D + col);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < 8 && r < rows; ++e)
                     dst[e] = n > 0 ? make_float4(__uint_as_float(u[4 * e]), __uint_as_float(u[4 * e + 1]),
                                                  __uint_as_float(u[4 * e + 2]), __uint_as_float(u[4 * e + 3]))
                                    : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -484,12 +491,14 @@ window_sink_kernel(const View dk, const View dv, const BwdArgs a) {
     const int x = blockIdx.y * 256 + threadIdx.x, r = x / (D / 4), c = 4 * (x % (D / 4));
     const int w = blockIdx.x & 1, bh = blockIdx.x >> 1, b = bh / a.Hkv, hk = bh % a.Hkv;
     if (r >= min(BM, a.T)) return;
-    const float* src = a.part + ((size_t)bh * (1 + a.splits) * 2 + w) * BM * D + (size_t)r * D + c;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 s = *reinterpret_cast<const float4*>(a.part + part_offset(a, bh, 0, D) + ((size_t)w * BM + r) * D + c);
+    if (r < a.sinks) {
+        const float* src = a.part + part_offset(a, bh, 1, D) + ((size_t)w * a.sinks + r) * D + c;
 #pragma unroll 4
-    for (int i = 0; i <= a.splits; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(src + (size_t)i * 2 * BM * D);
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        for (int i = 0; i < a.splits; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(src + (size_t)i * 2 * a.sinks * D);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
     }
     const float m = w ? 1.f : a.scale;
     const View& o = w ? dv : dk;
@@ -510,9 +519,16 @@ constexpr uint32_t Q_SMEM = Q_OFF_SUM + BM * 4;
 static_assert(2 * (Q_SMEM + 1024) <= 233472, "two CTAs per SM");
 constexpr uint32_t TQ_S = 0, TQ_DP = 64, TQ_DQ = 128;
 
-// kSweep: the key tiles are walked twice, first for delta_t = sum_s P_ts dP_ts
-// (which also replaces the one from h, for the dK/dV kernel after this one).
-template <int D, bool kSweep>
+// Where rows see few keys the tiles are walked twice, first for delta_t = sum_s
+// P_ts dP_ts, which replaces the one from dh . h (for the dK/dV kernel after this one
+// too): h was rounded to bf16, and with few keys it is so large that the error
+// counts beside the rounding of dS.  (Relative errors of dq and dk against 64 bits
+// at T = 150, window 140: 0.0028 from h, 0.0024 from the sweep; with 1024 keys 0.0024
+// from h.)  The sweep adds two products to the three of a tile.
+constexpr int kSweepWindow = 128;  // windows up to so many keys, and
+constexpr int kSweepTokens = 512;  // the first tokens of a sequence
+
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
 window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -542,9 +558,9 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ns = min((a.sinks + BN - 1) / BN, w0);
         nt = ns + (min(t0 + BM, len) - 1) / BN + 1 - w0;
     }
-    const int once = nt;  // tiles of a sweep
-    if constexpr (kSweep) nt *= 2;
-    auto tile_of = [&](int j) { return kSweep && j >= once ? j - once : j; };
+    const int once = a.sweep || t0 < kSweepTokens ? nt : 0;  // tiles of the first sweep
+    nt += once;
+    auto tile_of = [&](int j) { return j >= once ? j - once : j; };
     auto tile_key = [&](int j) {
         const int x = tile_of(j);
         return (x < ns ? x : w0 + x - ns) * BN;
@@ -657,11 +673,10 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             fence_after_sync();
             const uint64_t kd = desc_add(kmdesc, (j & 1) * TILE_N);
             const int steps = tile_keys(j) / 16;
-            const int j0 = kSweep ? once : 0;  // the tile whose product comes first
             if (elect_one()) {
-                for (int kk = 0; kk < steps && j >= j0; ++kk)
+                for (int kk = 0; kk < steps && j >= once; ++kk)
                     mma_ts(tmem + TQ_DQ, tmem + TQ_DP + 32 * (kk >> 1) + 8 * (kk & 1), desc_add(kd, kk * 2048), idesc_g,
-                           j > j0 || kk > 0 ? 1u : 0u);
+                           j > once || kk > 0 ? 1u : 0u);
                 mma_commit(BAR(QB_KEMPTY + (j & 1)));
             }
             __syncwarp();
@@ -677,14 +692,14 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
         const int t = t0 + r, c0 = 32 * half;
         const size_t row = ((size_t)b * a.Hq + hq) * a.Tp + t;  // (rows are padded to whole tiles)
-        const float nl = a.nlse[row], nd = kSweep ? 0.f : a.ndelta[row];
+        const float nl = a.nlse[row], nd = once > 0 ? 0.f : a.ndelta[row];
         const f32x2 sl = mk2(a.scale_log2, a.scale_log2), nl2 = mk2(nl, nl);
         f32x2 nd2 = mk2(nd, nd);
-        float delta = 0.f;  // kSweep: sum of P dP over this half of the first sweep
+        float delta = 0.f;  // sum of P dP over this half of the first sweep
         float* sums = reinterpret_cast<float*>(gbase + Q_OFF_SUM);
         bool ok = true, voted = false;
         for (int j = 0; j < nt; ++j) {
-            if (kSweep && j == once) {  // the halves of delta, in order; the second sweep takes it, and dK/dV
+            if (j == once && once > 0) {  // the halves of delta, in order; the second sweep takes it, and dK/dV
                 if (half == 1) sums[r] = delta;
                 if (!bar_and(true, 1, kSoftmax)) {  // a warp has given up: this was the vote below
                     ok = false, voted = true;
@@ -747,10 +762,10 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         if (!(bits >> c & 1u)) e0 = 0.f;
                         if (!(bits >> (c + 1) & 1u)) e1 = 0.f;
                     }
-                    if (kSweep && j < once) delta += e0 + e1;
+                    if (j < once) delta += e0 + e1;
                     pk[c / 2] = pack_bf16(e0, e1);
                 }
-                if (!kSweep || j >= once) {
+                if (j >= once) {
                     tmem_st<16>(td, pk);
                     tmem_wait_st();
                 }
@@ -790,13 +805,6 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
 }
 
-// Up to so many keys to a row delta comes from a sweep of its own in dQ, not from
-// dh . h: h was rounded to bf16, and with few keys it is so large that the error
-// counts beside the rounding of dS (relative error of dq and dk against 64 bits
-// at T = 206, window 30, 0.0026 from h and 0.0024 from the sweep; with 1024 keys 0.0024
-// from h).  The sweep adds two products of three to a tile.
-constexpr int kSweepKeys = 128;
-
 // Shape of a call: padded rows, reach and stretches of the first key tile.
 struct Plan {
     int window, sinks, nt, Tp, splits;
@@ -817,7 +825,8 @@ Plan plan_of(const ssa_window_params_t& p) {
     }
     x.rows = align_up((size_t)p.B * p.Hq * x.Tp * sizeof(float), 256);
     x.bytes = 2 * x.rows;
-    if (x.splits) x.bytes += align_up((size_t)p.B * p.Hkv * (1 + x.splits) * 2 * BM * p.D * sizeof(float), 256);
+    if (x.splits)
+        x.bytes += align_up((size_t)p.B * p.Hkv * 2 * p.D * (BM + (size_t)x.splits * x.sinks) * sizeof(float), 256);
     return x;
 }
 
@@ -825,8 +834,7 @@ template <int D>
 int run(const ssa_window_params_t& p, const View& q, const View& k, const View& v, const View& h, const float* lse,
         const View& dh, const View& dq, const View& dk, const View& dv, BwdArgs a, cudaStream_t s) {
     int st = opt_in_max_smem<window_dkdv_kernel<D>>("window_dkdv_kernel");
-    if (st == SSA_OK) st = opt_in_max_smem<window_dq_kernel<D, false>>("window_dq_kernel");
-    if (st == SSA_OK) st = opt_in_max_smem<window_dq_kernel<D, true>>("window_dq_kernel");
+    if (st == SSA_OK) st = opt_in_max_smem<window_dq_kernel<D>>("window_dq_kernel");
     CUtensorMap k128, v128, mdk, mdv, q128, do128, k64, v64, k16, v16, mdq;
     struct { CUtensorMap* m; const View* x; int H, rows; } maps[] = {
         {&k128, &k, p.Hkv, BM}, {&v128, &v, p.Hkv, BM},
@@ -840,8 +848,7 @@ int run(const ssa_window_params_t& p, const View& q, const View& k, const View& 
     window_rows_kernel<D><<<dim3((unsigned)(a.Tp / rows), (unsigned)p.Hq, (unsigned)p.B), 256, 0, s>>>(
         h, dh, lse, const_cast<float*>(a.nlse), const_cast<float*>(a.ndelta), a);
     const unsigned tiles = (unsigned)p.B * p.Hq * a.nt;
-    if (a.sweep) window_dq_kernel<D, true><<<tiles, kThreads, Q_SMEM, s>>>(q128, do128, k64, v64, k16, v16, mdq, a);
-    else window_dq_kernel<D, false><<<tiles, kThreads, Q_SMEM, s>>>(q128, do128, k64, v64, k16, v16, mdq, a);
+    window_dq_kernel<D><<<tiles, kThreads, Q_SMEM, s>>>(q128, do128, k64, v64, k16, v16, mdq, a);
     const unsigned items = (unsigned)p.B * p.Hkv * (a.nt + a.splits);
     window_dkdv_kernel<D><<<items, kThreadsK, K_SMEM, s>>>(q128, do128, k128, v128, mdk, mdv, a);
     if (a.splits)
@@ -868,7 +875,7 @@ int launch_window_bwd_tc(const ssa_window_params_t& p, const View& q, const View
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * x.rows);
     a.B = p.B, a.Hq = p.Hq, a.Hkv = p.Hkv, a.G = p.Hq / p.Hkv, a.T = p.T, a.Tp = x.Tp;
     a.window = x.window, a.sinks = x.sinks, a.nt = x.nt, a.splits = x.splits;
-    a.sweep = x.window <= kSweepKeys;
+    a.sweep = x.window <= kSweepWindow;
     a.scale = p.sm_scale, a.scale_log2 = p.sm_scale * kLog2e;
     a.timeout_ns = wait_limit_ns();
     return p.D == 64 ? run<64>(p, q, k, v, h, lse, dh, dq, dk, dv, a, s)

@@ -619,10 +619,8 @@ class PagedCache:
         self.prefix_len = prefix_len
         self.prefix_pages = B * width + torch.arange(shared, dtype=torch.int32, device=device)
         self.inv_freq, self.interleaved = inv_freq, interleaved
-        n = ssa_cache_workspace_size(self.params, prefix_len)
-        if n == ctypes.c_size_t(-1).value:
+        if ssa_cache_workspace_size(self.params, prefix_len) == ctypes.c_size_t(-1).value:
             raise SsaError("ssa_cache_workspace_size", SSA_ERR_INVALID_ARG, ssa_last_error())
-        self.ws = torch.empty(n, dtype=torch.uint8, device=device)
 
     def append(self, k, v, q=None, q_start=None, q_out=None, k_out=None):
         """Appends new tokens (see ``cache_append``) -> the rotated queries."""
@@ -643,5 +641,5 @@ class PagedCache:
         """Attention of each sequence's newest token, q [B,Hq,D] rotated -> dict(h, lse)."""
         if self.prefix_len:
             return prefix_decode(self.params, q, self.k_pages, self.v_pages, self.prefix_pages, self.prefix_len,
-                                 self.table, self.lens, self.ws, out)
-        return paged_decode(self.params, q, self.k_pages, self.v_pages, self.table, self.lens, self.ws, out)
+                                 self.table, self.lens, None, out)
+        return paged_decode(self.params, q, self.k_pages, self.v_pages, self.table, self.lens, None, out)

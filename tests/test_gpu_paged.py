@@ -473,3 +473,132 @@ def test_tensors_are_checked():
         ssa.window_bwd(w, x, y, y, f, y)
     with pytest.raises(ValueError, match="lse must be"):
         ssa.window_bwd(w, x, y, y, {**f, "lse": f["lse"].double()}, x)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strided_queries_and_outputs(dtype):
+    # queries as slices of a fused projection, outputs into another strided buffer
+    B, Hq, Hkv, D, page, n = 3, 6, 2, 64, 32, 90
+    g = torch.Generator().manual_seed(21)
+    kp, vp, table, _ = _pool(B, Hkv, D, page, 3, dtype, 22)
+    lens = [90, 1, 33]
+    toks = _fill(kp, vp, table, lens, Hkv, D, page, dtype, g)
+    x = torch.randn(B, (Hq + 2 * Hkv) * D, generator=g).to(DT[dtype])
+    q = x.view(B, -1, D)[:, :Hq]
+    xd, kpd, vpd, td = (t.to(DEV) for t in (x, kp, vp, table))
+    qd = xd.view(B, -1, D)[:, :Hq]
+    buf = torch.full((B, 2 * Hq, D), 7.0, dtype=DT[dtype], device=DEV)
+    out = {"h": buf[:, ::2], "lse": torch.empty(B, Hq, device=DEV)}
+    p = ssa.cache_params_for(qd, kpd, td)
+    ssa.paged_decode(p, qd, kpd, vpd, td, torch.tensor(lens, dtype=torch.int32, device=DEV), out=out)
+    torch.cuda.synchronize()
+    ssa.device_status()
+    R.check(out, _reference(q, toks, 0, None, 1 / math.sqrt(D), q.dtype), ["h", "lse"])
+    assert (buf[:, 1::2] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefix_pass_captured(dtype):
+    # a batch large enough for the 128-row pass, captured; replays follow the lengths, and two
+    # graphs of one cache on two streams do not disturb each other
+    B, Hq, Hkv, D, page, P = 20, 8, 2, 128, 16, 300
+    c = ssa.PagedCache(B, Hq, Hkv, D, 64, DT[dtype], DEV, page=page, prefix_len=P)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(DT[dtype])  # noqa: E731
+    c.fill_prefix(rnd(P, Hkv, D), rnd(P, Hkv, D))
+    c.append(rnd(B * 40, Hkv, D), rnd(B * 40, Hkv, D))
+    q = rnd(B, Hq, D)
+    want = c.attend(q)
+    side = [torch.cuda.Stream() for _ in range(2)]
+    graphs, outs = [], []
+    torch.cuda.synchronize()
+    for s in side:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=s):
+            outs.append(c.attend(q))
+        graphs.append(gr)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, gr in zip(side, graphs):
+            with torch.cuda.stream(s):
+                gr.replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o["h"], want["h"]) and torch.equal(o["lse"], want["lse"])
+    c.lens.copy_(torch.arange(B, dtype=torch.int32, device=DEV))
+    graphs[0].replay()
+    want = c.attend(q)
+    torch.cuda.synchronize()
+    ssa.device_status()
+    assert torch.equal(outs[0]["h"], want["h"])
+
+
+def test_first_calls_inside_a_capture():
+    # every call captured before it has ever run in the process: nothing in it synchronises
+    import subprocess
+    import sys
+
+    code = """
+import torch
+from block_sparse_full_b200 import ssa
+for dt in (torch.bfloat16, torch.float32):
+    q = torch.randn(2, 20, 4, 64, device="cuda", dtype=dt).transpose(1, 2)
+    k = torch.randn(2, 20, 2, 64, device="cuda", dtype=dt).transpose(1, 2)
+    p = ssa.window_params_for(q, k, 7, 2)
+    c = ssa.PagedCache(20, 4, 2, 64, 40, dt, "cuda", page=16, prefix_len=20)
+    x, y = torch.randn(20, 4, 64, device="cuda", dtype=dt), torch.randn(20, 2, 64, device="cuda", dtype=dt)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        f = ssa.window_fwd(p, q, k, k)
+        grads = ssa.window_bwd(p, q, k, k, f, q)
+        c.append(y, y, x)
+        out = c.attend(x)
+    g.replay()
+    torch.cuda.synchronize()
+    ssa.device_status()
+    want = ssa.window_fwd(p, q, k, k)
+    assert torch.equal(f["h"], want["h"]) and c.lens.tolist() == [1] * 20
+    for a, b in zip(grads, ssa.window_bwd(p, q, k, k, want, q)):
+        assert torch.equal(a, b)
+    assert torch.equal(out["h"], c.attend(x)["h"])
+print("fine")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+def test_short_wait_limit_leaves_the_context_usable():
+    # the tensor-core kernels' waits give up after 100 ns: the calls end, are reported, and later
+    # calls give the same results as before
+    g = torch.Generator(device=DEV).manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).bfloat16()  # noqa: E731
+    q, k, v, dh = rnd(2, 4, 700, 128), rnd(2, 2, 700, 128), rnd(2, 2, 700, 128), rnd(2, 4, 700, 128)
+    c = ssa.PagedCache(20, 4, 2, 128, 64, torch.bfloat16, DEV, prefix_len=500)
+    c.fill_prefix(rnd(500, 2, 128), rnd(500, 2, 128))
+    c.append(rnd(100, 2, 128), rnd(100, 2, 128))
+    x = rnd(20, 4, 128)
+
+    def all_calls(window):
+        p = ssa.window_params_for(q, k, window, 5)
+        f = ssa.window_fwd(p, q, k, v)
+        return [f["h"], f["lse"], *ssa.window_bwd(p, q, k, v, f, dh), *c.attend(x).values()]
+
+    want = {w: all_calls(w) for w in (100, 300)}
+    torch.cuda.synchronize()
+    ssa.device_status()
+    stream = torch.cuda.current_stream().cuda_stream
+    for w in (100, 300):
+        ssa.ssa_debug_set_wait_limit_ns(100)
+        try:
+            all_calls(w)
+            assert ssa.ssa_device_status(stream) in (ssa.SSA_OK, ssa.SSA_ERR_TIMEOUT)
+            while ssa.ssa_device_status(stream) == ssa.SSA_ERR_TIMEOUT:  # one record per kernel
+                pass
+        finally:
+            ssa.ssa_debug_set_wait_limit_ns(0)
+        got = all_calls(w)
+        torch.cuda.synchronize()
+        ssa.device_status()
+        for a, b in zip(want[w], got):
+            assert torch.equal(a, b)
