@@ -7,6 +7,13 @@
 
 namespace ssa {
 
+// Programmatic launches: the next kernel in the stream may start once every CTA of
+// this one has said so or ended; wait_for_previous() returns when the kernel
+// before has completed and its writes are visible (at once in a kernel that was
+// launched in the ordinary way).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 

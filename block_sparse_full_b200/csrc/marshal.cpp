@@ -15,6 +15,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <climits>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <initializer_list>
@@ -313,10 +315,74 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// The structure for these tensors, an instance of the ctypes class cls.
+template <typename P>
+PyObject* instance(PyObject* cls, const P& p) {
+    PyObject* bytes = PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&p), sizeof p);
+    PyObject* r = bytes ? PyObject_CallMethod(cls, "from_buffer_copy", "O", bytes) : nullptr;
+    Py_XDECREF(bytes);
+    return r;
+}
+
+int number(PyObject* o, const char* name) {
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) throw python_error();
+    if (v < INT_MIN || v > INT_MAX) throw ValueError("%s does not fit into an int (%ld)", name, v);
+    return (int)v;
+}
+float scale_of(PyObject* o, int64_t D) {
+    if (o == Py_None) return (float)(1.0 / std::sqrt((double)D));
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw python_error();
+    return (float)v;
+}
+int dtype_of(const Tensor& t, const char* name) {
+    if (t.scalar_type() == at::kBFloat16) return SSA_BF16;
+    if (t.scalar_type() == at::kFloat) return SSA_F32;
+    throw ValueError("%s must be bfloat16 or float32, got %s", name, c10::toString(t.scalar_type()));
+}
+const Tensor& ranked(PyObject* o, const char* name, int64_t dim) {
+    const Tensor& t = tensor(o, name);
+    if (t.dim() != dim) throw ValueError("%s must have %d axes, got shape %s", name, (int)dim, dims(t.sizes()).c_str());
+    for (const int64_t n : t.sizes())
+        if (n > INT_MAX) throw ValueError("%s: an axis of %lld is too long", name, (long long)n);
+    return t;
+}
+
+// (cls, q, k, window, sinks, sm_scale, flags)
+PyObject* window_params_for(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 7, "window_params_for");
+    const Tensor &q = ranked(a[1], "q", 4), &k = ranked(a[2], "k", 4);
+    ssa_window_params_t p{};
+    p.B = (int)q.size(0), p.Hq = (int)q.size(1), p.Hkv = (int)k.size(1), p.T = (int)q.size(2), p.D = (int)q.size(3);
+    p.window = number(a[3], "window"), p.sinks = number(a[4], "sinks");
+    p.dtype = dtype_of(q, "q"), p.sm_scale = scale_of(a[5], p.D), p.flags = (unsigned)number(a[6], "flags");
+    return instance(a[0], p);
+    END_HANDLE_TH_ERRORS
+}
+
+// (cls, q, k_pages, table, window, sinks, sm_scale)
+PyObject* cache_params_for(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 7, "cache_params_for");
+    const Tensor &q = tensor(a[1], "q"), &kp = ranked(a[2], "k_pages", 4), &table = ranked(a[3], "table", 2);
+    if (q.dim() < 2) throw ValueError("q must have head and row axes, got shape %s", dims(q.sizes()).c_str());
+    ssa_cache_params_t p{};
+    p.B = (int)table.size(0), p.Hq = (int)q.size(-2), p.Hkv = (int)kp.size(1), p.D = (int)kp.size(3);
+    p.page = (int)kp.size(2), p.n_pages = (int)kp.size(0), p.max_pages = (int)table.size(1);
+    p.window = number(a[4], "window"), p.sinks = number(a[5], "sinks");
+    p.dtype = dtype_of(kp, "k_pages"), p.sm_scale = scale_of(a[6], p.D), p.page_stride = kp.stride(0);
+    return instance(a[0], p);
+    END_HANDLE_TH_ERRORS
+}
+
 using FastCall = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
 PyCFunction fast(FastCall f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)); }
 
 PyMethodDef methods[] = {
+    {"window_params_for", fast(window_params_for), METH_FASTCALL, nullptr},
+    {"cache_params_for", fast(cache_params_for), METH_FASTCALL, nullptr},
     {"window_fwd", fast(window_fwd), METH_FASTCALL, nullptr},
     {"window_bwd", fast(window_bwd), METH_FASTCALL, nullptr},
     {"cache_append", fast(cache_append), METH_FASTCALL, nullptr},

@@ -164,11 +164,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Programmatic launches: the kernels of a call may overlap where they do not
-// depend on one another.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // A place in the list of units.
 struct Cursor {
     long long u;  // unit
@@ -816,25 +811,6 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc
 }
 
 constexpr int kCtas = 296;  // two CTAs on each of 148 SMs
-
-// Launch that may begin while the kernel before it in the stream still runs.
-template <typename... Params, typename... Args>
-int launch_beside(const char* what, void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                  const Args&... args) {
-    cudaLaunchConfig_t c{};
-    c.gridDim = grid;
-    c.blockDim = dim3((unsigned)threads);
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = &at;
-    c.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
-    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    return check_launch(what);
-}
 
 template <typename T, int D, int RG>
 int launch_pass(const DecodeArgs& a, const Pass& p, bool beside, cudaStream_t s) {

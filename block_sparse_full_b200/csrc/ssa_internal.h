@@ -56,6 +56,26 @@ int opt_in_max_smem(const char* what, size_t* dyn_limit = nullptr) {
     return SSA_OK;
 }
 
+// Launch that may begin while the kernel before it in the stream still runs; the
+// kernel itself waits (griddepcontrol.wait) before it touches that one's results.
+template <typename... Params, typename... Args>
+int launch_beside(const char* what, void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                  const Args&... args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
+    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return check_launch(what);
+}
+
 // Wall-clock limit of the kernels' bounded waits (default 2 s; tests shorten it).
 unsigned long long wait_limit_ns();
 

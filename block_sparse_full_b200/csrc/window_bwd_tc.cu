@@ -138,6 +138,7 @@ template <int D>
 __global__ void __launch_bounds__(256)
 window_rows_kernel(const View h, const View dh, const float* lse, float* nlse, float* ndelta, const BwdArgs a) {
     constexpr int L = D / 8;  // lanes of a row, 16 bytes each
+    launch_dependents();
     const int t = blockIdx.x * (256 / L) + (int)threadIdx.x / L, c = 8 * ((int)threadIdx.x % L);
     const int hq = blockIdx.y, b = blockIdx.z;
     if (t >= a.Tp) return;  // (Tp is a multiple of the rows of a block: whole blocks)
@@ -230,6 +231,7 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
+    launch_dependents();
     const uint32_t tmem = *reinterpret_cast<uint32_t*>(gbase + K_OFF_MISC);
     const unsigned FULL = 0xffffffffu;
     auto wait = [&](int bar, uint32_t ph) -> bool {
@@ -273,6 +275,7 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         }
         __syncwarp();
+        wait_for_previous();  // the row values are the kernels' before this one; K and V may come sooner
         ring(KB_QFULL, KB_QEMPTY, &tm_q, K_OFF_Q, true);
         if (n > 0) wait_drain(BAR(KB_KV), 0);
     } else if (warp == 2) {
@@ -488,6 +491,7 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 template <int D>
 __global__ void __launch_bounds__(256)
 window_sink_kernel(const View dk, const View dv, const BwdArgs a) {
+    wait_for_previous();
     const int x = blockIdx.y * 256 + threadIdx.x, r = x / (D / 4), c = 4 * (x % (D / 4));
     const int w = blockIdx.x & 1, bh = blockIdx.x >> 1, b = bh / a.Hkv, hk = bh % a.Hkv;
     if (r >= min(BM, a.T)) return;
@@ -582,6 +586,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
+    launch_dependents();
     const uint32_t tmem = *reinterpret_cast<uint32_t*>(gbase + Q_OFF_MISC);
     const unsigned FULL = 0xffffffffu;
     auto wait = [&](int bar, uint32_t ph) -> bool {
@@ -692,6 +697,7 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
         const int t = t0 + r, c0 = 32 * half;
         const size_t row = ((size_t)b * a.Hq + hq) * a.Tp + t;  // (rows are padded to whole tiles)
+        wait_for_previous();  // (the products start without the row values)
         const float nl = a.nlse[row], nd = once > 0 ? 0.f : a.ndelta[row];
         const f32x2 sl = mk2(a.scale_log2, a.scale_log2), nl2 = mk2(nl, nl);
         f32x2 nd2 = mk2(nd, nd);
@@ -844,16 +850,22 @@ int run(const ssa_window_params_t& p, const View& q, const View& k, const View& 
     for (const auto& m : maps)
         if (st == SSA_OK) st = make_view_map(m.m, *m.x, D, p.T, m.H, p.B, m.rows);
     if (st != SSA_OK) return st;
+    // Each kernel may begin while the one before runs out: it waits for that one only
+    // where it needs its results (and so completes after it).
     constexpr int rows = 256 / (D / 8);
     window_rows_kernel<D><<<dim3((unsigned)(a.Tp / rows), (unsigned)p.Hq, (unsigned)p.B), 256, 0, s>>>(
         h, dh, lse, const_cast<float*>(a.nlse), const_cast<float*>(a.ndelta), a);
-    const unsigned tiles = (unsigned)p.B * p.Hq * a.nt;
-    window_dq_kernel<D><<<tiles, kThreads, Q_SMEM, s>>>(q128, do128, k64, v64, k16, v16, mdq, a);
-    const unsigned items = (unsigned)p.B * p.Hkv * (a.nt + a.splits);
-    window_dkdv_kernel<D><<<items, kThreadsK, K_SMEM, s>>>(q128, do128, k128, v128, mdk, mdv, a);
-    if (a.splits)
-        window_sink_kernel<D><<<dim3(2u * p.B * p.Hkv, (unsigned)(BM * D / 4 / 256)), 256, 0, s>>>(dk, dv, a);
-    return check_launch("window backward (tensor cores)");
+    st = check_launch("window_rows_kernel");
+    if (st == SSA_OK)
+        st = launch_beside("window_dq_kernel", window_dq_kernel<D>, dim3((unsigned)p.B * p.Hq * a.nt), kThreads, Q_SMEM, s,
+                           q128, do128, k64, v64, k16, v16, mdq, a);
+    if (st == SSA_OK)
+        st = launch_beside("window_dkdv_kernel", window_dkdv_kernel<D>, dim3((unsigned)p.B * p.Hkv * (a.nt + a.splits)),
+                           kThreadsK, K_SMEM, s, q128, do128, k128, v128, mdk, mdv, a);
+    if (st == SSA_OK && a.splits)
+        st = launch_beside("window_sink_kernel", window_sink_kernel<D>,
+                           dim3(2u * p.B * p.Hkv, (unsigned)(BM * D / 4 / 256)), 256, 0, s, dk, dv, a);
+    return st;
 }
 
 }  // namespace

@@ -46,6 +46,7 @@
 #include <mutex>
 
 #include "ssa_internal.h"
+#include "device_util.cuh"
 #include "tc_util.cuh"
 #include "tmap.h"
 
@@ -174,7 +175,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    if constexpr (kPrefix) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (kPrefix) ssa::launch_dependents();
     const uint32_t tmem = *reinterpret_cast<uint32_t*>(gbase + OFF_MISC);
     const unsigned FULL = 0xffffffffu;
 

@@ -508,8 +508,7 @@ def window_params(B, Hq, Hkv, T, D, window, sinks, dtype, sm_scale=None, flags=0
 
 def window_params_for(q, k, window, sinks=0, sm_scale=None, flags=0) -> ssa_window_params_t:
     """For q [B,Hq,T,D] and k [B,Hkv,T,D]."""
-    B, Hq, T, D = q.shape
-    return window_params(B, Hq, k.shape[1], T, D, window, sinks, q.dtype, sm_scale, flags)
+    return _marshal.window_params_for(ssa_window_params_t, q, k, window, sinks, sm_scale, flags)
 
 
 def cache_params(B, Hq, Hkv, D, page, n_pages, max_pages, dtype, window=0, sinks=0, sm_scale=None,
@@ -527,10 +526,7 @@ def cache_params(B, Hq, Hkv, D, page, n_pages, max_pages, dtype, window=0, sinks
 
 def cache_params_for(q, k_pages, table, window=0, sinks=0, sm_scale=None) -> ssa_cache_params_t:
     """For q [..., Hq, D], k_pages [n_pages, Hkv, page, D] and table [B, max_pages]."""
-    n_pages, Hkv, page, D = k_pages.shape
-    B, width = table.shape
-    return cache_params(B, q.shape[-2], Hkv, D, page, n_pages, width, k_pages.dtype, window, sinks, sm_scale,
-                        k_pages.stride(0))
+    return _marshal.cache_params_for(ssa_cache_params_t, q, k_pages, table, window, sinks, sm_scale)
 
 
 _NO_PAIR = (None, None)

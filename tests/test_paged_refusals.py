@@ -143,6 +143,25 @@ def test_decode_arguments():
     assert pre(p=cp(window=5)) == ssa.SSA_ERR_UNSUPPORTED
 
 
+def test_params_from_tensors():
+    q, k = torch.zeros(2, 6, 30, 64), torch.zeros(2, 3, 30, 64)
+    a = ssa.window_params_for(q, k, 7, 2)
+    b = ssa.window_params(2, 6, 3, 30, 64, 7, 2, torch.float32)
+    assert bytes(a) == bytes(b) and isinstance(a, ssa.ssa_window_params_t)
+    a = ssa.window_params_for(q.bfloat16(), k, 0, sm_scale=0.25, flags=2)
+    assert (a.dtype, a.sm_scale, a.flags, a.window) == (ssa.SSA_BF16, 0.25, 2, 0)
+    pool, table = torch.zeros(9, 2, 3, 16, 64, dtype=torch.bfloat16)[:, 0], torch.zeros(5, 4, dtype=torch.int32)
+    a = ssa.cache_params_for(q[0], pool, table, 9, 1)
+    assert bytes(a) == bytes(ssa.cache_params(5, 30, 3, 64, 16, 9, 4, torch.bfloat16, 9, 1, None, 2 * 3 * 16 * 64))
+    for bad in (lambda: ssa.window_params_for(q[0], k, 7), lambda: ssa.window_params_for(q.half(), k, 7),
+                lambda: ssa.cache_params_for(q, pool[0], table), lambda: ssa.cache_params_for(q, pool, table[0]),
+                lambda: ssa.window_params_for(q, k, 1 << 40)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        ssa.window_params_for(q, k, "7")
+
+
 def test_tensor_helpers_check_shape_type_and_device():
     t = torch.zeros(1, 2, 8, 64)
     p = ssa.window_params_for(t, t, 4)
