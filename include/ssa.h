@@ -356,8 +356,9 @@ int ssa_window_bwd(const ssa_window_params_t* params, const ssa_view_t* q, const
  *   window, sinks : as above, for ssa_paged_decode (the newest token is the
  *                query's own); not read by the other calls.
  *   Hq         : query heads.  dtype, sm_scale: as above.  flags: 0.
- * A length, page number or row count read on the device that is outside its
- * range is skipped and recorded; ssa_device_status then reports it.
+ * A length or page number read on the device that is outside its range is
+ * recorded, ssa_device_status then reports it, and nothing out of range is
+ * read or written; the outputs of the sequences concerned are undefined.
  */
 typedef struct {
     int B, Hq, Hkv, D, page, n_pages, max_pages, window, sinks;
