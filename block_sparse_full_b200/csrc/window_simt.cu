@@ -6,19 +6,19 @@
 //   dp_ts = dh_t . v_s, delta_t = dh_t . h_t, ds_ts = p_ts (dp_ts - delta_t) sm_scale,
 //   dq_t = sum_s ds_ts k_s, dk_s = sum_t ds_ts q_t, dv_s = sum_t p_ts dh_t.
 //
-// float32 products run on the FMA pipe, which bounds these kernels: 64 x 64
-// tiles, 256 threads of 4 x 4 scores and 4 x D/16 outputs each, operands in
-// shared memory with rows of D + 4 floats (16 lanes read 16 rows without bank
-// conflicts).  Only the tiles that the window and the sinks reach are
-// visited.  The gradients take two kernels, one per query tile for dq and one
-// over key tiles for dk and dv: a tile's list of (query head of the group, query
+// float32 products run on the FMA pipe, fed from shared memory, whose reads bound
+// these kernels: 64 x 64 tiles with rows of D + 4 floats (no bank conflicts), 8 x 8
+// or 8 x 4 scores to a thread.  Only the tiles that the window and the sinks reach
+// are visited.  The gradients take two kernels, one per query tile for dq and one
+// over key tiles for dk and dv, which run beside one another (each forms delta from
+// dh and h itself: 73 us against 93 one after the other with 4 x 4 scores and a
+// kernel for delta, for two sequences of 777 tokens, 4/2 heads of 64, window 128,
+// 4 sinks, forward included).  A key tile's list of (query head of the group, query
 // tile) is one CTA's, or, where there are too few key tiles to fill the SMs and
 // for tiles that hold sinks (every later query sees them), is cut into
-// stretches whose parts window_parts_kernel sums in order.  (Two sequences of
-// 777 tokens, 4/2 heads of 64, window 128, 4 sinks: 92 us for both directions,
-// 332 us with one CTA to a key tile.)  Clusters of CTAs share a query tile of dq
-// as they do in the forward (976 tokens, 4/2 heads of 128, all keys: 258 us for
-// both directions, 365 us without).
+// stretches whose parts window_parts_kernel sums in order (without: 332 us).
+// Clusters of CTAs share a query tile of dq as they do in the forward (976 tokens,
+// 4/2 heads of 128, all keys: 219 us for both directions).
 #include <cooperative_groups.h>
 
 #include "device_util.cuh"
@@ -37,7 +37,6 @@ __device__ unsigned int g_window_status;
 struct WinArgs {
     View q, k, v, h, dh, dq, dk, dv;
     float* lse;
-    float* delta;
     const int32_t* lens;
     int B, Hq, Hkv, G, T, window, sinks;
     int nsink, cuts, sink_cuts;  // key tiles with sinks; stretches of a tile's list without and with them
@@ -82,90 +81,11 @@ __device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// A tile's rows t0 .. t0 + 63 of one head, on their way through registers; rows
-// from len on are zero, whatever is stored there.
-template <typename T, int D>
-struct Fetch {
-    static constexpr int N = BT * D / 4 / kThreads;
-    float4 x[N];
-    __device__ __forceinline__ void load(const View& v, int b, int h, int t0, int len) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = threadIdx.x + i * kThreads, r = e / (D / 4), c = 4 * (e % (D / 4));
-            x[i] = t0 + r < len ? ld4(at<const T>(v, b, h, t0 + r) + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-    }
-    __device__ __forceinline__ void store(float* dst) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = threadIdx.x + i * kThreads, r = e / (D / 4), c = 4 * (e % (D / 4));
-            *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = x[i];
-        }
-    }
-};
-
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
     return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
 }
-
-// s[i][j] = row (4 ty + i) of A . row (tx + 16 j) of B
-template <int D>
-__device__ __forceinline__ void scores(const float* A, const float* Bm, int ty, int tx, float (&s)[4][4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
-    for (int d = 0; d < D; d += 4) {
-        float4 x[4], y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = ld4(A + (4 * ty + i) * (D + 4) + d);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = ld4(Bm + (tx + 16 * j) * (D + 4) + d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
-    }
-}
-
 __device__ __forceinline__ void axpy(float w, float4 v, float4& o) {
     o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
-}
-
-// o[i][c] += sum_n W[4 ty + i][n] X[n][4 tx + 64 c ..]   (W rows of PP, X rows of D + 4)
-template <int D>
-__device__ __forceinline__ void gather(const float* W, const float* X, int ty, int tx, float4 (&o)[4][D / 64]) {
-#pragma unroll 2
-    for (int n = 0; n < BT; n += 4) {
-        float4 w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = ld4(W + (4 * ty + i) * PP + n);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const float4 x = ld4(X + (n + m) * (D + 4) + 4 * tx + 64 * c);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) axpy((&w[i].x)[m], x, o[i][c]);
-            }
-    }
-}
-// o[i][c] += sum_n W[n][4 ty + i] X[n][4 tx + 64 c ..]
-template <int D>
-__device__ __forceinline__ void scatter(const float* W, const float* X, int ty, int tx, float4 (&o)[4][D / 64]) {
-#pragma unroll 4
-    for (int n = 0; n < BT; ++n) {
-        const float4 w = ld4(W + n * PP + 4 * ty);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            const float4 x = ld4(X + n * (D + 4) + 4 * tx + 64 * c);
-            axpy(w.x, x, o[0][c]);
-            axpy(w.y, x, o[1][c]);
-            axpy(w.z, x, o[2][c]);
-            axpy(w.w, x, o[3][c]);
-        }
-    }
 }
 
 // Key tiles of the queries t0 .. tl: [0, ns) with sinks only, then [w0, w0 + nw).
@@ -372,134 +292,238 @@ window_fwd_simt_kernel(const WinArgs a) {
     if (cs > 1) cluster.sync();  // the shares stay until every CTA has read them
 }
 
-// delta_t = dh_t . h_t, one warp per row
+// Gradients: two groups of 128 threads.  The first forms q k^T and from it p, the
+// second dh v^T and, once p is in shared memory, ds.  A thread holds 8 x 4 scores
+// (rows row_of(ty, i): its warp's other half lies 4 rows on, in other banks;
+// keys tx + 16 x) and 8 x D / 16 outputs: 12 reads of 16 bytes to 128 FMAs, where
+// 4 x 4 scores take 16.
+constexpr int kHalf = kThreads / 2;
+
+__device__ __forceinline__ int row_of(int ty, int i) { return 16 * (ty >> 1) + 4 * (ty & 1) + (i & 3) + 8 * (i >> 2); }
+
+// Rows t0 .. t0 + 63 of one head -> shared memory; rows from len on are zero,
+// whatever is stored there.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
-window_delta_kernel(const WinArgs a) {
-    const int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), hq = blockIdx.y, b = blockIdx.z;
-    const int lane = threadIdx.x & 31;
-    if (t >= a.T) return;
-    float s = 0.f;
-    if (t < seq_len(a, b) && 4 * lane < D)
-        s = dot4(ld4(at<const T>(a.dh, b, hq, t) + 4 * lane), ld4(at<const T>(a.h, b, hq, t) + 4 * lane), 0.f);
-    s = warp_sum(s);
-    if (lane == 0) a.delta[((size_t)b * a.Hq + hq) * a.T + t] = s;
+__device__ __forceinline__ void load_tile(const View& v, int b, int h, int t0, int len, float* dst) {
+    constexpr int L = D / 4, N = BT * L / kThreads;
+    float4 x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = threadIdx.x + i * kThreads, r = e / L, c = 4 * (e % L);
+        x[i] = t0 + r < len ? ld4(at<const T>(v, b, h, t0 + r) + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = threadIdx.x + i * kThreads, r = e / L, c = 4 * (e % L);
+        *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = x[i];
+    }
 }
 
-// p and ds of the score tile (queries t0 .., keys s0 ..), s and dp given
-__device__ __forceinline__ void weights(const WinArgs& a, const float* lse, const float* delta, int t0, int s0,
-                                        int len, int ty, int tx, const float (&s)[4][4],
-                                        const float (&dp)[4][4], float* P, float* dS) {
-    const float sl2 = a.sm_scale * kLog2e;
+// A tile of q and dh, and of its rows' values: -lse log2 e and delta = dh . h.
+template <typename T, int D>
+__device__ __forceinline__ void load_queries(const WinArgs& a, int b, int hq, int t0, int len, float* Q, float* dO,
+                                             float* row) {
+    constexpr int L = D / 4, N = BT * L / kThreads;
+    float4 x[N], y[N], z[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = t0 + 4 * ty + i;
-        const float ls = t < len ? lse[t] * kLog2e : 0.f, de = t < len ? delta[t] : 0.f;
+    for (int i = 0; i < N; ++i) {
+        const int e = threadIdx.x + i * kThreads, r = e / L, c = 4 * (e % L);
+        x[i] = y[i] = z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t0 + r < len) {
+            x[i] = ld4(at<const T>(a.q, b, hq, t0 + r) + c);
+            y[i] = ld4(at<const T>(a.dh, b, hq, t0 + r) + c);
+            z[i] = ld4(at<const T>(a.h, b, hq, t0 + r) + c);
+        }
+    }
+    const int t = t0 + (int)threadIdx.x;
+    if (threadIdx.x < BT) row[threadIdx.x] = t < len ? -kLog2e * a.lse[((size_t)b * a.Hq + hq) * a.T + t] : 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = threadIdx.x + i * kThreads, r = e / L, c = 4 * (e % L);
+        *reinterpret_cast<float4*>(Q + r * (D + 4) + c) = x[i];
+        *reinterpret_cast<float4*>(dO + r * (D + 4) + c) = y[i];
+        float d = dot4(y[i], z[i], 0.f);
+#pragma unroll
+        for (int sh = 1; sh < L; sh <<= 1) d += __shfl_xor_sync(0xffffffffu, d, sh);
+        if (c == 0) row[BT + r] = d;
+    }
+}
+
+// s[i][x] = row row_of(ty, i) of A . row tx + 16 x of B
+template <int D>
+__device__ __forceinline__ void scores(const float* A, const float* Bm, int ty, int tx, float (&s)[8][4]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[i][x] = 0.f;
+#pragma unroll 2
+    for (int d = 0; d < D; d += 4) {
+        float4 q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = ld4(A + row_of(ty, i) * (D + 4) + d);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const int key = s0 + tx + 16 * x;
-            const float p = t < len && sees(a, t, key) ? exp2f(fmaf(s[i][x], sl2, -ls)) : 0.f;
-            if (P) P[(4 * ty + i) * PP + tx + 16 * x] = p;
-            dS[(4 * ty + i) * PP + tx + 16 * x] = p * (dp[i][x] - de) * a.sm_scale;
+            const float4 k = ld4(Bm + (tx + 16 * x) * (D + 4) + d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i][x] = dot4(q[i], k, s[i][x]);
+        }
+    }
+}
+
+// The first group's p, and from them the second's ds, at the same places of P and dS
+// (which may be one array: a thread overwrites what it alone has read).
+__device__ __forceinline__ void put_p(const WinArgs& a, const float* row, int t0, int s0, int len, int ty, int tx,
+                                      const float (&s)[8][4], float* P) {
+    const float sl2 = a.sm_scale * kLog2e;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = row_of(ty, i), t = t0 + r;
+        const float nl = row[r];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            P[r * PP + tx + 16 * x] =
+                t < len && sees(a, t, s0 + tx + 16 * x) ? exp2f(fmaf(s[i][x], sl2, nl)) : 0.f;
+    }
+}
+__device__ __forceinline__ void put_ds(const WinArgs& a, const float* row, int ty, int tx, const float (&dp)[8][4],
+                                       const float* P, float* dS) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = row_of(ty, i);
+        const float de = row[BT + r];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int e = r * PP + tx + 16 * x;
+            dS[e] = P[e] * (dp[i][x] - de) * a.sm_scale;
+        }
+    }
+}
+
+template <int D>
+using Out = float4[8][D / 64];
+template <int D>
+__device__ __forceinline__ void clear(Out<D>& o) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// o[i][c] += sum over n0 <= n < n0 + 32 of W[row_of(ty, i)][n] X[n][4 tx + 64 c ..]
+template <int D>
+__device__ __forceinline__ void gather(const float* W, const float* X, int n0, int ty, int tx, Out<D>& o) {
+#pragma unroll 2
+    for (int n = n0; n < n0 + BT / 2; n += 4) {
+        float4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = ld4(W + row_of(ty, i) * PP + n);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const float4 x = ld4(X + (n + m) * (D + 4) + 4 * tx + 64 * c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) axpy((&w[i].x)[m], x, o[i][c]);
+            }
+    }
+}
+// o[i][c] += sum_n W[n][8 ty + i] X[n][4 tx + 64 c ..]
+template <int D>
+__device__ __forceinline__ void scatter(const float* W, const float* X, int ty, int tx, Out<D>& o) {
+#pragma unroll 8
+    for (int n = 0; n < BT; ++n) {
+        const float4 w0 = ld4(W + n * PP + 8 * ty), w1 = ld4(W + n * PP + 8 * ty + 4);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const float4 x = ld4(X + n * (D + 4) + 4 * tx + 64 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                axpy((&w0.x)[i], x, o[i][c]);
+                axpy((&w1.x)[i], x, o[4 + i][c]);
+            }
         }
     }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
 window_dq_simt_kernel(const WinArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr size_t N = tile_floats<D>();
-    float *Q = sm, *dO = Q + N, *K = dO + N, *V = K + N, *dS = V + N;
+    float *Q = sm, *dO = Q + N, *K = dO + N, *V = K + N, *P = V + N, *row = P + BT * PP;
     // (a cluster shares a query tile as in the forward)
     const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int cs = cluster.num_blocks(), rank = cluster.block_rank();
     const int t0 = blockIdx.x / cs * BT, hq = blockIdx.y, b = blockIdx.z, hk = hq / a.G;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int group = threadIdx.x / kHalf, tx = threadIdx.x & 15, ty = (threadIdx.x % kHalf) >> 4;
     const int len = seq_len(a, b);
-    const float* lse = a.lse + ((size_t)b * a.Hq + hq) * a.T;
-    const float* delta = a.delta + ((size_t)b * a.Hq + hq) * a.T;
-    float4 o[4][D / 64];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    launch_dependents();
+    Out<D> o;
+    clear<D>(o);
     if (t0 < len) {
         const KeyTiles kt(a, t0, min(t0 + BT, len) - 1);
-        Fetch<T, D> f;
-        f.load(a.q, b, hq, t0, len);
-        f.store(Q);
-        f.load(a.dh, b, hq, t0, len);
-        f.store(dO);
+        load_queries<T, D>(a, b, hq, t0, len, Q, dO, row);
         for (int j = rank; j < kt.n; j += cs) {
             const int s0 = kt.tile(j) * BT;
             __syncthreads();
-            f.load(a.k, b, hk, s0, len);
-            f.store(K);
-            f.load(a.v, b, hk, s0, len);
-            f.store(V);
+            load_tile<T, D>(a.k, b, hk, s0, len, K);
+            load_tile<T, D>(a.v, b, hk, s0, len, V);
             __syncthreads();
-            float s[4][4], dp[4][4];
-            scores<D>(Q, K, ty, tx, s);
-            scores<D>(dO, V, ty, tx, dp);
-            weights(a, lse, delta, t0, s0, len, ty, tx, s, dp, nullptr, dS);
+            float s[8][4];
+            scores<D>(group ? dO : Q, group ? V : K, ty, tx, s);
+            if (group == 0) put_p(a, row, t0, s0, len, ty, tx, s, P);
             __syncthreads();
-            gather<D>(dS, K, ty, tx, o);
+            if (group == 1) put_ds(a, row, ty, tx, s, P, P);
+            __syncthreads();
+            gather<D>(P, K, group * (BT / 2), ty, tx, o);  // each group half of the keys
         }
     }
-    if (cs > 1) {  // sums in the order of the ranks, the rows of a tile spread over the CTAs
-        __syncthreads();
+    // the groups' sums, then the CTAs' in the order of the ranks, the rows of a tile
+    // spread over the CTAs
+    __syncthreads();
+    float* mine = group ? dO : Q;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) *reinterpret_cast<float4*>(Q + (4 * ty + i) * (D + 4) + 4 * tx + 64 * c) = o[i][c];
-        cluster.sync();
-        for (int e = rank * kThreads + threadIdx.x; e < BT * D / 4; e += cs * kThreads) {
-            const int r = e / (D / 4), c = 4 * (e % (D / 4));
-            if (t0 + r >= a.T) continue;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = 0; k < cs; ++k) {
-                const float4 y = ld4(cluster.map_shared_rank(Q, k) + r * (D + 4) + c);
-                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-            }
-            st4(at<T>(a.dq, b, hq, t0 + r) + c, x);
+        for (int c = 0; c < D / 64; ++c)
+            *reinterpret_cast<float4*>(mine + row_of(ty, i) * (D + 4) + 4 * tx + 64 * c) = o[i][c];
+    if (cs > 1) cluster.sync();
+    else __syncthreads();
+    for (int e = rank * kThreads + threadIdx.x; e < BT * D / 4; e += cs * kThreads) {
+        const int r = e / (D / 4), c = 4 * (e % (D / 4));
+        if (t0 + r >= a.T) continue;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < cs; ++k) {
+            const float* base = k == rank ? Q : cluster.map_shared_rank(Q, k);
+            axpy(1.f, ld4(base + r * (D + 4) + c), x);
+            axpy(1.f, ld4(base + N + r * (D + 4) + c), x);
         }
-        cluster.sync();  // the shares stay until every CTA has read them
-        return;
+        st4(at<T>(a.dq, b, hq, t0 + r) + c, x);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = t0 + 4 * ty + i;
-        if (t >= a.T) continue;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) st4(at<T>(a.dq, b, hq, t) + 4 * tx + 64 * c, o[i][c]);
-    }
+    if (cs > 1) cluster.sync();  // the shares stay until every CTA has read them
 }
 
+// Launched beside the kernel for dq, which it does not depend on: only the last
+// CTA waits for that one, so that this kernel's end is both kernels'.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
 window_dkdv_simt_kernel(const WinArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr size_t N = tile_floats<D>();
-    float *Q = sm, *dO = Q + N, *K = dO + N, *V = K + N, *P = V + N, *dS = P + BT * PP;
+    float *Q = sm, *dO = Q + N, *K = dO + N, *V = K + N, *P = V + N, *dS = P + BT * PP, *row = dS + BT * PP;
     // item -> (tile, stretch): the tiles with sinks first
     const int hk = blockIdx.y, b = blockIdx.z, nsc = a.nsink * a.sink_cuts;
     const bool sink = (int)blockIdx.x < nsc;
     const int cuts = sink ? a.sink_cuts : a.cuts, x0 = sink ? (int)blockIdx.x : (int)blockIdx.x - nsc;
     const int tile = (sink ? 0 : a.nsink) + x0 / cuts, cut = x0 % cuts, s0 = tile * BT;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int group = threadIdx.x / kHalf, tx = threadIdx.x & 15, ty = (threadIdx.x % kHalf) >> 4;
     const int len = seq_len(a, b);
-    float4 ok[4][D / 64], ov[4][D / 64];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) ok[i][c] = ov[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    launch_dependents();
+    Out<D> o;  // dv in the first group, dk in the second
+    clear<D>(o);
     if (s0 < len) {
-        Fetch<T, D> f;
-        f.load(a.k, b, hk, s0, len);
-        f.store(K);
-        f.load(a.v, b, hk, s0, len);
-        f.store(V);
+        load_tile<T, D>(a.k, b, hk, s0, len, K);
+        load_tile<T, D>(a.v, b, hk, s0, len, V);
         // the last query that sees a key of the tile (a sink: the last of all)
         const int tl = s0 < a.sinks ? len - 1 : (int)min((long long)len - 1, (long long)s0 + BT - 1 + a.window - 1);
         const int per = tl / BT - tile + 1;  // query tiles of a head
@@ -507,51 +531,42 @@ window_dkdv_simt_kernel(const WinArgs a) {
         const int i1 = (int)(all * (cut + 1) / cuts);
         for (int i = (int)(all * cut / cuts); i < i1; ++i) {
             const int hq = hk * a.G + i / per, t0 = s0 + i % per * BT;
-            const float* lse = a.lse + ((size_t)b * a.Hq + hq) * a.T;
-            const float* delta = a.delta + ((size_t)b * a.Hq + hq) * a.T;
             __syncthreads();
-            f.load(a.q, b, hq, t0, len);
-            f.store(Q);
-            f.load(a.dh, b, hq, t0, len);
-            f.store(dO);
+            load_queries<T, D>(a, b, hq, t0, len, Q, dO, row);
             __syncthreads();
-            float s[4][4], dp[4][4];
-            scores<D>(Q, K, ty, tx, s);
-            scores<D>(dO, V, ty, tx, dp);
-            weights(a, lse, delta, t0, s0, len, ty, tx, s, dp, P, dS);
+            float s[8][4];
+            scores<D>(group ? dO : Q, group ? V : K, ty, tx, s);
+            if (group == 0) put_p(a, row, t0, s0, len, ty, tx, s, P);
             __syncthreads();
-            scatter<D>(P, dO, ty, tx, ov);
-            scatter<D>(dS, Q, ty, tx, ok);
+            if (group == 1) {
+                put_ds(a, row, ty, tx, s, P, dS);
+                asm volatile("bar.sync 1, %0;" ::"n"(kHalf) : "memory");
+            }
+            scatter<D>(group ? dS : P, group ? Q : dO, ty, tx, o);
         }
     }
+    float* slot = nullptr;
     if (cuts > 1) {
         const int nt = (a.T + BT - 1) / BT;
-        float* slot = a.part + ((size_t)(b * a.Hkv + hk) * first_slot(a, nt) + first_slot(a, tile) + cut) * 2 * BT * D;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                st4(slot + (4 * ty + i) * D + 4 * tx + 64 * c, ok[i][c]);
-                st4(slot + (BT + 4 * ty + i) * D + 4 * tx + 64 * c, ov[i][c]);
-            }
-        return;
+        slot = a.part + ((size_t)(b * a.Hkv + hk) * first_slot(a, nt) + first_slot(a, tile) + cut) * 2 * BT * D;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = s0 + 4 * ty + i;
-        if (t >= a.T) continue;
+    for (int i = 0; i < 8; ++i) {
+        const int r = 8 * ty + i;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-            st4(at<T>(a.dk, b, hk, t) + 4 * tx + 64 * c, ok[i][c]);
-            st4(at<T>(a.dv, b, hk, t) + 4 * tx + 64 * c, ov[i][c]);
+            if (slot) st4(slot + ((group ? 0 : BT) + r) * D + 4 * tx + 64 * c, o[i][c]);
+            else if (s0 + r < a.T) st4(at<T>(group ? a.dk : a.dv, b, hk, s0 + r) + 4 * tx + 64 * c, o[i][c]);
         }
     }
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) wait_for_previous();
 }
 
 // dk and dv of the tiles whose lists are in stretches: their parts in order
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 window_parts_kernel(const WinArgs a) {
+    wait_for_previous();
     constexpr int kBlocks = 2 * BT * D / 4 / kThreads;  // of a tile
     const int tile = blockIdx.x / kBlocks, hk = blockIdx.y, b = blockIdx.z, nt = (a.T + BT - 1) / BT;
     const int cuts = tile < a.nsink ? a.sink_cuts : a.cuts;
@@ -636,22 +651,22 @@ int fwd(const WinArgs& a, cudaStream_t s) {
 
 template <typename T, int D>
 int bwd(const WinArgs& a, cudaStream_t s) {
-    constexpr size_t smem_q = (4 * tile_floats<D>() + BT * PP) * sizeof(float);
+    constexpr size_t smem_q = (4 * tile_floats<D>() + BT * PP + 2 * BT) * sizeof(float);
     constexpr size_t smem_k = smem_q + BT * PP * sizeof(float);
     static_assert(smem_k <= kMaxSmemPerCta, "shared memory");
     int st = opt_in_max_smem<window_dq_simt_kernel<T, D>>("window_dq_simt_kernel");
     if (st == SSA_OK) st = opt_in_max_smem<window_dkdv_simt_kernel<T, D>>("window_dkdv_simt_kernel");
-    if (st != SSA_OK) return st;
-    const unsigned nt = (unsigned)((a.T + BT - 1) / BT);
-    window_delta_kernel<T, D><<<dim3((unsigned)((a.T + 7) / 8), (unsigned)a.Hq, (unsigned)a.B), kThreads, 0, s>>>(a);
+    if (st == SSA_OK) st = launch_clusters("window_dq_simt_kernel", window_dq_simt_kernel<T, D>, a, kThreads, smem_q, s);
+    const unsigned nt = (unsigned)((a.T + BT - 1) / BT), Hkv = (unsigned)a.Hkv, B = (unsigned)a.B;
     const unsigned items = (unsigned)(a.nsink * a.sink_cuts + ((int)nt - a.nsink) * a.cuts);
-    window_dkdv_simt_kernel<T, D><<<dim3(items, (unsigned)a.Hkv, (unsigned)a.B), kThreads, smem_k, s>>>(a);
-    if (a.cuts > 1 || a.sink_cuts > 1)
-        window_parts_kernel<T, D><<<dim3((a.cuts > 1 ? nt : (unsigned)a.nsink) * (2 * BT * D / 4 / kThreads), (unsigned)a.Hkv,
-                                          (unsigned)a.B), kThreads, 0, s>>>(a);
-    st = check_launch("window backward (CUDA cores)");
-    if (st != SSA_OK) return st;
-    return launch_clusters("window_dq_simt_kernel", window_dq_simt_kernel<T, D>, a, kThreads, smem_q, s);
+    if (st == SSA_OK)
+        st = launch_beside("window_dkdv_simt_kernel", window_dkdv_simt_kernel<T, D>, dim3(items, Hkv, B), kThreads, smem_k,
+                           s, a);
+    if (st == SSA_OK && (a.cuts > 1 || a.sink_cuts > 1))
+        st = launch_beside("window_parts_kernel", window_parts_kernel<T, D>,
+                           dim3((a.cuts > 1 ? nt : (unsigned)a.nsink) * (2 * BT * D / 4 / kThreads), Hkv, B), kThreads, 0, s,
+                           a);
+    return st;
 }
 
 }  // namespace
@@ -664,16 +679,14 @@ int launch_window_fwd_simt(const ssa_window_params_t& p, const View& q, const Vi
 }
 
 size_t window_bwd_simt_workspace(const ssa_window_params_t& p) {
-    return align_up((size_t)p.B * p.Hq * p.T * sizeof(float), 256) +  // delta
-           align_up(part_bytes(args(p, View{}, View{}, View{}, nullptr, View{}, nullptr), p.D), 256);
+    return align_up(part_bytes(args(p, View{}, View{}, View{}, nullptr, View{}, nullptr), p.D), 256);
 }
 
 int launch_window_bwd_simt(const ssa_window_params_t& p, const View& q, const View& k, const View& v,
                            const int32_t* lens, const View& h, const float* lse, const View& dh,
                            const View& dq, const View& dk, const View& dv, void* ws, cudaStream_t s) {
     WinArgs a = args(p, q, k, v, lens, h, const_cast<float*>(lse));
-    a.dh = dh, a.dq = dq, a.dk = dk, a.dv = dv, a.delta = static_cast<float*>(ws);
-    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up((size_t)p.B * p.Hq * p.T * sizeof(float), 256));
+    a.dh = dh, a.dq = dq, a.dk = dk, a.dv = dv, a.part = static_cast<float*>(ws);
     if (p.dtype == SSA_BF16) return p.D == 64 ? bwd<__nv_bfloat16, 64>(a, s) : bwd<__nv_bfloat16, 128>(a, s);
     return p.D == 64 ? bwd<float, 64>(a, s) : bwd<float, 128>(a, s);
 }
