@@ -159,6 +159,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
     }
     const int hk = kPrefix ? h : h / a.G;
+    // bytes between the 64-column parts of a K or V row and between groups of eight
+    // rows: a view's tile is two boxes of 64 rows, a page's rows come in one box
+    constexpr uint32_t kCols = kPrefix ? 1024 : KV_BOX, kEight = kPrefix ? 16 * D : 1024;
     auto tile_key = [&](int j) { return (j < ns ? j : w0 + j - ns) * BN; };
     // keys that tile j loads and multiplies: of a sink tile whole steps of 16
     auto tile_keys = [&](int j) { return j < ns ? min(BN, (a.sinks - j * BN + 15) & ~15) : BN; };
@@ -217,11 +220,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
                 if (lane == 0) mbar_expect_tx(bar, (uint32_t)(np * step) * D * 2);
                 __syncwarp();
-                if (lane < np) {
-#pragma unroll
-                    for (int x = 0; x < D / 64; ++x)
-                        tma_load_4d(dst + x * KV_BOX + lane * step * 128, tm, bar, 64 * x, s0 % a.page, hk, pg);
-                }
+                if (lane < np)
+                    tma_load_5d(dst + lane * step * 2 * D, tm, bar, 0, 0, 0, (hk * a.page + s0 % a.page) / 8, pg);
             } else if (elect_one()) {
                 mbar_expect_tx(bar, (uint32_t)keys * D * 2);
                 if (keys < BN) {
@@ -268,8 +268,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
         const uint64_t qdesc = smem_desc_sw128(base + OFF_Q, 16, 1024);      // K-major
-        const uint64_t kdesc = smem_desc_sw128(base + OFF_K, 16, 1024);      // K-major
-        const uint64_t vdesc = smem_desc_sw128(base + OFF_V, KV_BOX, 1024);  // MN-major
+        const uint64_t kdesc = smem_desc_sw128(base + OFF_K, 16, kEight);    // K-major
+        const uint64_t vdesc = smem_desc_sw128(base + OFF_V, kCols, kEight); // MN-major
         constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, true);
         auto wait = [&](int bar, int j) -> bool {
             return __all_sync(FULL, mbar_wait(BAR(bar + (j & 1)), (j >> 1) & 1, abort_flag, status, lim));
@@ -283,7 +283,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_ss(tmem + TM_S + BN * (j & 1), desc_add(qdesc, (kk >> 2) * Q_BOX + (kk & 3) * 32),
-                           desc_add(kd, (kk >> 2) * KV_BOX + (kk & 3) * 32), idesc_qk, kk > 0 ? 1u : 0u);
+                           desc_add(kd, (kk >> 2) * kCols + (kk & 3) * 32), idesc_qk, kk > 0 ? 1u : 0u);
                 mma_commit(BAR(B_SREADY + (j & 1)));
                 mma_commit(BAR(B_KEMPTY + j % kK));
             }
@@ -301,7 +301,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int steps = tile_keys(j) / 16;
             if (elect_one()) {
                 for (int kk = 0; kk < steps; ++kk)
-                    mma_ts(tmem + TM_O, p + 8 * kk, desc_add(vd, kk * 2048), idesc_pv, j > 0 || kk > 0 ? 1u : 0u);
+                    mma_ts(tmem + TM_O, p + 8 * kk, desc_add(vd, kk * 2 * kEight), idesc_pv, j > 0 || kk > 0 ? 1u : 0u);
                 mma_commit(BAR(B_VEMPTY + (j & 1)));
             }
             __syncwarp();
@@ -362,7 +362,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 if (!ok) break;
                 const int vr = r & (BN - 1), box = r / BN;  // 128 threads: 64 rows of two boxes
                 if (vr >= end && box < D / 64) {
-                    uint4* p = reinterpret_cast<uint4*>(gbase + OFF_V + (j & 1) * KV_BYTES + box * KV_BOX + vr * 128);
+                    uint4* p = reinterpret_cast<uint4*>(gbase + OFF_V + (j & 1) * KV_BYTES + box * kCols + vr / 8 * kEight +
+                                                        vr % 8 * 128);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) p[i] = make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -536,8 +537,8 @@ int launch(const CUtensorMap (&m)[6], const AttnArgs& a, long long grid, cudaStr
 
 }  // namespace
 
-int make_map4(CUtensorMap* m, void* ptr, const unsigned long long (&dims)[4], const long long (&strides)[3],
-              const unsigned (&box)[4]) {
+int make_map(CUtensorMap* m, void* ptr, int rank, const unsigned long long* dims, const long long* strides,
+             const unsigned* box) {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -548,11 +549,11 @@ int make_map4(CUtensorMap* m, void* ptr, const unsigned long long (&dims)[4], co
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     });
     if (!fn) return fail(SSA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
-    cuuint64_t d[4], st[3];
-    cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
-    for (int i = 0; i < 4; ++i) d[i] = dims[i], bx[i] = box[i];
-    for (int i = 0; i < 3; ++i) st[i] = (cuuint64_t)strides[i] * 2;
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5], es[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) d[i] = dims[i], bx[i] = box[i];
+    for (int i = 0; i + 1 < rank; ++i) st[i] = (cuuint64_t)strides[i] * 2;
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, ptr, d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(SSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
@@ -560,8 +561,11 @@ int make_map4(CUtensorMap* m, void* ptr, const unsigned long long (&dims)[4], co
 }
 
 int make_view_map(CUtensorMap* m, const View& v, int D, int T, int H, int B, int rows) {
-    return make_map4(m, v.data, {(unsigned long long)D, (unsigned long long)T, (unsigned long long)H, (unsigned long long)B},
-                     {v.st, v.sh, v.sb}, {64, (unsigned)rows, 1, 1});
+    const unsigned long long dims[4] = {(unsigned long long)D, (unsigned long long)T, (unsigned long long)H,
+                                        (unsigned long long)B};
+    const long long strides[3] = {v.st, v.sh, v.sb};
+    const unsigned box[4] = {64, (unsigned)rows, 1, 1};
+    return make_map(m, v.data, 4, dims, strides, box);
 }
 
 bool window_tc_supported(const ssa_window_params_t& p) {
@@ -616,13 +620,15 @@ int launch_prefix_tc(const ssa_cache_params_t& p, const View& q, const void* k_p
     const int G = p.Hq / p.Hkv;
     using U = unsigned long long;
     CUtensorMap m[6];
-    int st = make_map4(&m[0], q.data, {(U)p.D, (U)G, (U)p.Hkv, (U)p.B}, {q.sh, q.sh * G, q.sb},
-                       {64, (unsigned)G, 1, (unsigned)x.nb});
-    const U dims[4] = {(U)p.D, (U)p.page, (U)p.Hkv, (U)p.n_pages};
-    const long long strides[3] = {p.D, (long long)p.page * p.D, p.page_stride};
-    const unsigned box[4] = {64, (unsigned)(p.page < BN ? p.page : BN), 1, 1};
-    if (st == SSA_OK) st = make_map4(&m[1], const_cast<void*>(k_pages), dims, strides, box);
-    if (st == SSA_OK) st = make_map4(&m[2], const_cast<void*>(v_pages), dims, strides, box);
+    const U qdims[4] = {(U)p.D, (U)G, (U)p.Hkv, (U)p.B};
+    const long long qstrides[3] = {q.sh, q.sh * G, q.sb};
+    const unsigned qbox[4] = {64, (unsigned)G, 1, (unsigned)x.nb};
+    int st = make_map(&m[0], q.data, 4, qdims, qstrides, qbox);
+    const U dims[5] = {64, 8, (U)p.D / 64, (U)p.Hkv * p.page / 8, (U)p.n_pages};
+    const long long strides[4] = {p.D, 64, 8ll * p.D, p.page_stride};
+    const unsigned box[5] = {64, 8, (unsigned)p.D / 64, (unsigned)(p.page < BN ? p.page : BN) / 8, 1};
+    if (st == SSA_OK) st = make_map(&m[1], const_cast<void*>(k_pages), 5, dims, strides, box);
+    if (st == SSA_OK) st = make_map(&m[2], const_cast<void*>(v_pages), 5, dims, strides, box);
     if (st != SSA_OK) return st;
     m[3] = m[1], m[4] = m[2], m[5] = m[0];  // not used by this pass
     AttnArgs a{};
