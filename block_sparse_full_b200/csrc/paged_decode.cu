@@ -9,7 +9,8 @@
 // the lengths are (they are read on the device, so a captured launch follows
 // them).  A row tile's end counts as one unit more, about what starting and
 // joining it costs, so that CTAs with many short sequences get fewer of them
-// (64 sequences of up to 1024 tokens, 32/8 heads: 44 us without, 36 with).  Walking its stretch a CTA keeps a running maximum, sum and output
+// (64 sequences of up to 1024 tokens, 32/8 heads: 44 us without, 36 with).  Few row
+// tiles of few keys have a cluster each instead, see cluster_of.  Walking its stretch a CTA keeps a running maximum, sum and output
 // (float32) per row and writes them down as a partial result where a
 // (sequence, head, row tile) is split between CTAs; a second kernel joins the
 // partials of each row:  h = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
@@ -24,6 +25,7 @@
 // tile of 16 query rows cannot fill a larger tensor tile; the prefix of a batch
 // of more rows goes to the 128-row kernel of window_fwd_tc.cu).  float32: CUDA
 // cores, a warp takes 8 keys.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "device_util.cuh"
@@ -36,6 +38,8 @@ constexpr int kThreads = 128;
 constexpr int kWarps = 4;
 constexpr int kRows = 16;  // query rows of a unit
 constexpr int kStages = 3;
+constexpr int kFew = 2;  // units that a CTA takes at least: with one, the join of so many partials costs more
+                         // (4096 tokens behind 8 sequences: 14.6 us, 14.1 with two, 15 with three)
 constexpr float kLn2 = 0.693147180559945309f;
 
 __device__ unsigned int g_paged_status;
@@ -52,6 +56,7 @@ struct Pass {
     int nseq, R, RT, width, cap, fixed_len, window, sinks;
     int C;         // CTAs
     bool direct;   // rows held by one CTA go to the output, else to its own slot
+    int one;       // CTAs of a cluster that takes a row tile, 0: the list of units
     float* part;   // slots [2C + nseq*Hkv*RT] x 16 rows x (D outputs, then m, l)
 };
 
@@ -112,7 +117,10 @@ __device__ __forceinline__ long long units_before(const Pass& p, int upto, int t
 }
 
 // CTAs that take part: each has a unit
-__device__ __forceinline__ int used_ctas(long long total, int C) { return total < C ? (int)total : C; }
+__device__ __forceinline__ int used_ctas(long long total, int C) {
+    const long long n = (total + kFew - 1) / kFew;
+    return n < C ? (int)n : C;
+}
 // first unit of CTA c's stretch, and the CTA whose stretch holds unit u
 __device__ __forceinline__ long long stretch(long long total, int C, int c) { return total * c / C; }
 __device__ __forceinline__ int cta_of(long long total, int C, long long u) {
@@ -162,6 +170,13 @@ __device__ __forceinline__ float ex2f(float x) {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void put4(float* dst, float4 v, float f) {
+    *reinterpret_cast<float4*>(dst) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+}
+__device__ __forceinline__ void put4(__nv_bfloat16* dst, float4 v, float f) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(v.x * f, v.y * f), pack2(v.z * f, v.w * f));
 }
 
 // A place in the list of units.
@@ -434,7 +449,9 @@ constexpr size_t decode_smem() {
     return ring_bytes<T, D>() + kRows * D * 4 * (sizeof(T) == 4 ? 2 : 1) + (kWarps + 2) * kRows * 4;
 }
 
-template <typename T, int D, int RG>
+// kOne: a cluster of CTAs takes one row tile, each CTA an equal stretch of its key
+// tiles, and joins their shares through distributed shared memory.
+template <typename T, int D, int RG, bool kOne>
 __global__ void __launch_bounds__(kThreads, 2)
 decode_kernel(const DecodeArgs a, const Pass p) {
     constexpr int TK = Tile<T>::keys;
@@ -450,18 +467,26 @@ decode_kernel(const DecodeArgs a, const Pass p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int HR = a.Hkv * p.RT;
 
-    launch_dependents();  // every CTA is on its SM: the next kernel's may come in beside them
-    const long long total = units_before(p, p.nseq, TK) * HR;
-    const int C = used_ctas(total, p.C);
-    if ((int)blockIdx.x >= C) {
-        wait_for_previous();
-        return;
-    }
-    const long long ubeg = stretch(total, C, blockIdx.x), uend = stretch(total, C, blockIdx.x + 1);
-
-    // the place of unit ubeg: the sequence by a warp-wide scan
     Cursor ld;
-    {
+    long long ubeg, uend;
+    if constexpr (kOne) {
+        const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        const int cs = cluster.num_blocks(), rank = cluster.block_rank(), x = (int)blockIdx.x / cs;
+        ld.b = x / HR, ld.hr = x % HR;
+        ld.s = seen_tiles(p, seq_len(p, ld.b), TK);
+        ubeg = ld.s.nt * rank / cs, uend = ld.s.nt * (rank + 1) / cs;
+        ld.u = ubeg, ld.t = (int)ubeg;
+        if (threadIdx.x < kRows) top[threadIdx.x] = -INFINITY;  // (a CTA without a tile)
+    } else {
+        launch_dependents();  // every CTA is on its SM: the next kernel's may come in beside them
+        const long long total = units_before(p, p.nseq, TK) * HR;
+        const int C = used_ctas(total, p.C);
+        if ((int)blockIdx.x >= C) {
+            wait_for_previous();
+            return;
+        }
+        ubeg = stretch(total, C, blockIdx.x), uend = stretch(total, C, blockIdx.x + 1);
+        // the place of unit ubeg: the sequence by a warp-wide scan
         long long before = 0;
         int found = -1;
         for (int b0 = 0; found < 0; b0 += 32) {
@@ -505,10 +530,12 @@ decode_kernel(const DecodeArgs a, const Pass p) {
             c.s = seen_tiles(p, seq_len(p, c.b), TK);
         } while (c.s.nt == 0);
     };
-    if (ld.t == ld.s.nt) advance(ld);
-    if (ld.u >= uend) {  // nothing but an end
-        wait_for_previous();
-        return;
+    if constexpr (!kOne) {
+        if (ld.t == ld.s.nt) advance(ld);
+        if (ld.u >= uend) {  // nothing but an end
+            wait_for_previous();
+            return;
+        }
     }
     Cursor cu = ld;
     // The page numbers of a tile: lane g holds that of its g-th 16 keys (a page
@@ -545,7 +572,7 @@ decode_kernel(const DecodeArgs a, const Pass p) {
         }
     };
 
-    int pg = page_of(ld);
+    int pg = ld.u < uend ? page_of(ld) : 0;
     auto copy_next = [&](int st) {
         if (ld.u < uend) {
             copy(ld, st, pg);
@@ -618,6 +645,11 @@ decode_kernel(const DecodeArgs a, const Pass p) {
             };
             const bool whole = last && t0 == 0;
             const int hd = cu.hr / p.RT;
+            if constexpr (kOne) {  // for the other CTAs: the sums at their first place
+                for (int x = threadIdx.x; x < nr * D / 4; x += kThreads) reinterpret_cast<float4*>(sum)[x] = out4(x);
+                if ((int)threadIdx.x < nr) lsum[threadIdx.x] = sum_of(threadIdx.x);
+                break;
+            }
             if (whole && p.direct) {
                 for (int x = threadIdx.x; x < nr * D / 4; x += kThreads) {
                     const int r = x / (D / 4), c = 4 * (x % (D / 4));
@@ -625,11 +657,7 @@ decode_kernel(const DecodeArgs a, const Pass p) {
                     const float inv = 1.f / sum_of(r);
                     T* dst = static_cast<T*>(a.h.data) + (size_t)(cu.b + (r0 + r) / a.G) * a.h.sb +
                              (size_t)(hd * a.G + (r0 + r) % a.G) * a.h.sh + c;
-                    if constexpr (sizeof(T) == 2) {
-                        *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
-                    } else {
-                        *reinterpret_cast<float4*>(dst) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-                    }
+                    put4(dst, v, inv);
                 }
                 if ((int)threadIdx.x < nr) {
                     const int r = r0 + threadIdx.x;
@@ -652,6 +680,32 @@ decode_kernel(const DecodeArgs a, const Pass p) {
         cu = nx;
     }
     cp_wait<0>();
+    if constexpr (kOne) {
+        const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        const int cs = cluster.num_blocks(), rank = cluster.block_rank(), x = (int)blockIdx.x / cs;
+        const int b = x / HR, hd = x % HR / p.RT, r0 = x % HR % p.RT * kRows, nr = min(kRows, p.R - r0);
+        cluster.sync();
+        // four outputs to a thread, the shares in the order of the ranks
+        for (int e = rank * kThreads + threadIdx.x; e < nr * D / 4; e += cs * kThreads) {
+            const int r = e / (D / 4), c = 4 * (e % (D / 4)), head = hd * a.G + r0 + r;
+            float M = -INFINITY, L = 0.f;
+            for (int k = 0; k < cs; ++k) M = fmaxf(M, cluster.map_shared_rank(top, k)[r]);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < cs; ++k) {
+                const float m = cluster.map_shared_rank(top, k)[r];
+                if (m == -INFINITY) continue;
+                const float w = ex2f(m - M);
+                const float4 y = reinterpret_cast<const float4*>(cluster.map_shared_rank(sum, k))[e];
+                L = fmaf(w, cluster.map_shared_rank(lsum, k)[r], L);
+                v.x = fmaf(w, y.x, v.x), v.y = fmaf(w, y.y, v.y), v.z = fmaf(w, y.z, v.z), v.w = fmaf(w, y.w, v.w);
+            }
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            put4(static_cast<T*>(a.h.data) + (size_t)b * a.h.sb + (size_t)head * a.h.sh + c, v, inv);
+            if (c == 0) a.lse[(size_t)b * a.Hq + head] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+        }
+        cluster.sync();  // the shares stay until every CTA has read them
+        return;
+    }
     // The pass over a shared prefix may still be running beside this one; the join
     // waits for this kernel only, so this kernel ends after it.
     wait_for_previous();
@@ -682,8 +736,11 @@ struct PrefixTc {
 
 // Joins the partials of the rows of one sequence and head.  pre: the pass over
 // the shared prefix (nseq = 0: none), or ptc.  Few rows leave several of the eight
-// warps to each: they take its partials in turn and are joined in order.
-constexpr int kJoinWarps = 8;
+// warps to each, all eight where a row has a block of its own: they take its
+// partials in turn and are joined in order (one sequence of 65536 tokens, 74
+// partials to each of 16 rows: 41 us with two warps to a row, 32 with eight; 64 sequences behind a
+// prefix of 32768: 87 us, 101 with a block to each of their 2048 rows).
+constexpr int kJoinWarps = 8, kJoinBlocks = 592;  // warps of a block; blocks up to which each row has its own
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
@@ -694,13 +751,14 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc
     __shared__ float o_of[kJoinWarps][D];
     const int b = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int HR = a.Hkv * p.RT;
-    const int per = a.G >= 5 ? 1 : a.G >= 3 ? 2 : a.G == 2 ? 4 : 8;  // warps of a row
+    const bool alone = gridDim.z > 1;  // a block to a row
+    const int per = alone ? 8 : a.G >= 5 ? 1 : a.G >= 3 ? 2 : a.G == 2 ? 4 : 8;  // warps of a row
     const int sub = warp % per;
     // the lengths were there before the passes began: the lists are laid out while they still run
     const Seen s = seen_tiles(p, seq_len(p, b), TK);
     const long long before = units_before(p, b, TK);
     const long long total = units_before(p, p.nseq, TK) * HR;
-    for (int g0 = 0; g0 < a.G; g0 += kJoinWarps / per) {
+    for (int g0 = blockIdx.z; g0 < (alone ? (int)blockIdx.z + 1 : a.G); g0 += kJoinWarps / per) {
         const int g = min(g0 + warp / per, a.G - 1);
         const bool row = g0 + warp / per < a.G;
         // own partials: a first one, then every `step` floats; then the prefix's likewise
@@ -811,16 +869,43 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc
 }
 
 constexpr int kCtas = 296;  // two CTAs on each of 148 SMs
+// Row tiles of few keys are a cluster's each, if the GPU holds all clusters at once:
+// one launch, no partials in memory.  Eight CTAs a cluster with up to eight key tiles
+// each, or as many as keep the total at 256, then with up to 16 (at 288 CTAs in
+// clusters of eight not all are placed at once: 17 us instead of 11).  One sequence,
+// 16/4 heads of 128, window 1024: 8.6 us, 10.1 by the list of units; 32 sequences:
+// 17.8 and 22; one, window 8000 (16 tiles a CTA): 20.9 and 12.3, so left to the list.
+constexpr int kOneCtas = 256;  // CTAs of all clusters at most
 
 template <typename T, int D, int RG>
 int launch_pass(const DecodeArgs& a, const Pass& p, bool beside, cudaStream_t s) {
-    const int st = opt_in_max_smem<decode_kernel<T, D, RG>>("decode_kernel");
+    const int st = opt_in_max_smem<decode_kernel<T, D, RG, false>>("decode_kernel");
     if (st != SSA_OK) return st;
     if (beside)
-        return launch_beside("decode_kernel", decode_kernel<T, D, RG>, dim3((unsigned)p.C), kThreads, decode_smem<T, D>(),
-                             s, a, p);
-    decode_kernel<T, D, RG><<<p.C, kThreads, decode_smem<T, D>(), s>>>(a, p);
+        return launch_beside("decode_kernel", decode_kernel<T, D, RG, false>, dim3((unsigned)p.C), kThreads,
+                             decode_smem<T, D>(), s, a, p);
+    decode_kernel<T, D, RG, false><<<p.C, kThreads, decode_smem<T, D>(), s>>>(a, p);
     return check_launch("decode_kernel");
+}
+// One launch: a cluster to a row tile.
+template <typename T, int D, int RG>
+int launch_one(const DecodeArgs& a, const Pass& p, cudaStream_t s) {
+    const int st = opt_in_max_smem<decode_kernel<T, D, RG, true>>("decode_kernel<cluster>");
+    if (st != SSA_OK) return st;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(p.one * p.nseq * a.Hkv * p.RT));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = decode_smem<T, D>();
+    c.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)p.one;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&c, decode_kernel<T, D, RG, true>, a, p);
+    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "decode_kernel<cluster>: %s", cudaGetErrorString(e));
+    return check_launch("decode_kernel<cluster>");
 }
 template <typename T, int D>
 int run_pass(const DecodeArgs& a, const Pass& p, bool beside, cudaStream_t s) {
@@ -832,12 +917,19 @@ int run_pass(const DecodeArgs& a, const Pass& p, bool beside, cudaStream_t s) {
 template <typename T, int D>
 int run(const DecodeArgs& a, const Pass& own, const Pass& pre, const PrefixTc& ptc, cudaStream_t s) {
     int st = SSA_OK;
+    if (own.one) {
+        if constexpr (sizeof(T) == 4)
+            if (own.R <= 4) return launch_one<T, D, 4>(a, own, s);
+        return launch_one<T, D, kRows>(a, own, s);
+    }
     if (pre.nseq) st = run_pass<T, D>(a, pre, false, s);
     // the sequences' own pages do not wait for the prefix (the kernel ends after it, though)
     if (st == SSA_OK) st = run_pass<T, D>(a, own, pre.nseq || ptc.splits, s);
     if (st != SSA_OK) return st;
-    return launch_beside("join_kernel", join_kernel<T, D>, dim3((unsigned)a.Hkv, (unsigned)a.B), 32 * kJoinWarps, 0, s, a,
-                         own, pre, ptc);
+    // few sequences leave many partials to a row: a block to each row, as far as that takes about four to an SM
+    const unsigned rows = (long long)a.B * a.Hq <= kJoinBlocks ? (unsigned)a.G : 1u;
+    return launch_beside("join_kernel", join_kernel<T, D>, dim3((unsigned)a.Hkv, (unsigned)a.B, rows), 32 * kJoinWarps, 0,
+                         s, a, own, pre, ptc);
 }
 
 int tile_keys(const ssa_cache_params_t& p) { return p.dtype == SSA_BF16 ? 64 : 32; }
@@ -854,6 +946,13 @@ long long seen_most(const ssa_cache_params_t& p) {
     const long long cap = (long long)p.max_pages * p.page;
     const long long w = p.window > 0 ? (long long)p.window + p.sinks + 2 * 64 : cap;
     return w < cap ? w : cap;
+}
+
+int cluster_of(const ssa_cache_params_t& p, int RT) {
+    const long long tiles = (seen_most(p) + tile_keys(p) - 1) / tile_keys(p), rows = (long long)p.B * p.Hkv * RT;
+    for (int cs = 8; cs > 1; cs /= 2)
+        if (rows * cs <= kOneCtas) return tiles <= cs * (rows * cs > kOneCtas / 2 ? 16 : 8) ? cs : 0;
+    return 0;
 }
 
 }  // namespace
@@ -887,6 +986,7 @@ int launch_paged_decode(const ssa_cache_params_t& p, const View& q, const void* 
     own.sinks = p.window > 0 ? p.sinks : 0;
     own.C = pass_ctas(p.B, p.Hkv, own.RT, seen_most(p), tk);
     own.direct = prefix_len == 0;
+    own.one = prefix_len == 0 ? cluster_of(p, own.RT) : 0;
     own.part = static_cast<float*>(ws);
     PrefixTc ptc{};
     void* pre_ws = static_cast<char*>(ws) + pass_bytes(own.C, (long long)p.B * p.Hkv * own.RT, p.D);

@@ -229,6 +229,26 @@ DECODE = [
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("case", DECODE, ids=str)
 def test_paged_decode(case, dtype):
+    _decode_case(case, dtype, 0)
+
+
+# The same over tables wide enough that the work is cut by the lengths, not by rows; more rows, and
+# more windows, than the clusters of one launch take.
+WIDE = [
+    (4, 2, 128, 16, [500, 41, 17] * 50, 16, 4),
+    (2, 1, 64, 64, [9000], 8500, 4),
+    (8, 8, 64, 32, [5000, 0, 3], 0, 0),
+    (2, 2, 128, 128, [1] * 200, 0, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", DECODE + WIDE, ids=str)
+def test_paged_decode_wide_table(case, dtype):
+    _decode_case(case, dtype, 1 << 15)
+
+
+def _decode_case(case, dtype, slots):
     Hq, Hkv, D, page, lens, window, sinks = case
     B, g = len(lens), torch.Generator().manual_seed(sum(lens))
     width = max(1, -(-max(lens) // page))
@@ -236,6 +256,8 @@ def test_paged_decode(case, dtype):
     toks = _fill(kp, vp, table, lens, Hkv, D, page, dtype, g, window, sinks)
     q = torch.randn(B, Hq, D, generator=g).to(DT[dtype])
     scale = 1 / math.sqrt(D)
+    if slots:  # (entries behind the lengths are not read)
+        table = torch.cat([table, torch.full((B, max(0, slots // page - width)), -1, dtype=torch.int32)], 1)
     qd, kpd, vpd, td = (x.to(DEV) for x in (q, kp, vp, table))
     p = ssa.cache_params_for(qd, kpd, td, window, sinks, scale)
     out = ssa.paged_decode(p, qd, kpd, vpd, td, torch.tensor(lens, dtype=torch.int32, device=DEV))
