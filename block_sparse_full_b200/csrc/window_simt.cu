@@ -7,8 +7,8 @@
 //   dq_t = sum_s ds_ts k_s, dk_s = sum_t ds_ts q_t, dv_s = sum_t p_ts dh_t.
 //
 // float32 products run on the FMA pipe, fed from shared memory, whose reads bound
-// these kernels: 64 x 64 tiles with rows of D + 4 floats (no bank conflicts), 8 x 8
-// or 8 x 4 scores to a thread.  Only the tiles that the window and the sinks reach
+// these kernels: 64 x 64 tiles with rows of D + 4 floats (no bank conflicts), 8 x 4
+// scores to a thread.  Only the tiles that the window and the sinks reach
 // are visited.  The gradients take two kernels, one per query tile for dq and one
 // over key tiles for dk and dv, which run beside one another (each forms delta from
 // dh and h itself: 73 us against 93 one after the other with 4 x 4 scores and a
@@ -17,8 +17,9 @@
 // tile) is one CTA's, or, where there are too few key tiles to fill the SMs and
 // for tiles that hold sinks (every later query sees them), is cut into
 // stretches whose parts window_parts_kernel sums in order (without: 332 us).
-// Clusters of CTAs share a query tile of dq as they do in the forward (976 tokens,
-// 4/2 heads of 128, all keys: 219 us for both directions).
+// Clusters of CTAs share a query tile of dq as they do in the forward.  The longest
+// tiles start first (4000 tokens, 2/1 heads of 128, all keys, forward: 247 us, 368 in
+// ascending order; the FMA pipe is then about 70 % busy; packed f32x2 products measured the same).
 #include <cooperative_groups.h>
 
 #include "device_util.cuh"
@@ -103,17 +104,19 @@ struct KeyTiles {
 template <int D>
 constexpr size_t tile_floats() { return (size_t)BT * (D + 4); }
 
-// Forward: groups of D threads walk the key tiles in turn, each with its own
+// Forward: groups of 128 threads walk the key tiles in turn, each with its own
 // buffers, running maximum, sum and output, and are joined at the end in group
-// order.  A thread holds 8 rows x 64 / (D / 8) keys of the scores and 8 x 8 outputs.
+// order.  A thread holds 8 rows x 4 keys of the scores and 8 x D / 16 outputs (8 x 8
+// scores in groups of 64 threads: 100 tokens, D = 64: 17.7 us instead of 12.8).
 // Key and value tiles are on their way while the other is in use.  Where the
 // query tiles do not fill the SMs a cluster of CTAs shares one, tile by tile,
 // and reads the others' shares through distributed shared memory (1000 tokens, 2
-// heads of 64, window 256: 32 us with one CTA to a query tile, 18 with four).
+// heads of 64, window 256: 32 us with one CTA to a query tile, 17 with four).
 template <int D>
 struct Fwd {
-    static constexpr int kGroup = D, kGroups = D == 64 ? 4 : 2;  // threads of a group; groups
-    static constexpr int TX = D / 8, KT = BT / TX;               // key columns of threads; keys of a thread
+    static constexpr int kGroup = 128, kGroups = D == 64 ? 4 : 2;  // threads of a group; groups
+    static constexpr int TX = kGroup / 8, KT = BT / TX;            // key columns of threads; keys of a thread
+    static constexpr int NC = D / (4 * TX);                        // outputs of a thread in a row, four each
     static constexpr size_t kFloats = 2 * (size_t)BT * (D + 4) + BT * PP;  // K, V, P of a group
     static constexpr size_t smem = (BT * (D + 4) + kGroups * kFloats) * sizeof(float);
 };
@@ -156,16 +159,19 @@ window_fwd_simt_kernel(const WinArgs a) {
     auto wait1 = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };
     const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int cs = cluster.num_blocks(), rank = cluster.block_rank();
-    const int t0 = blockIdx.x / cs * BT, hq = blockIdx.y, b = blockIdx.z, hk = hq / a.G;
+    // (the last tiles of all heads first: without a window they have the most keys)
+    const int x = blockIdx.x / cs, hq = x % a.Hq, b = x / a.Hq % a.B, hk = hq / a.G;
+    const int t0 = ((a.T + BT - 1) / BT - 1 - x / (a.Hq * a.B)) * BT;
     const int first = rank + cs * group, step = cs * G;  // this group's key tiles: CTAs first
     const int tx = tid % TX, ty = tid / TX;  // rows ty + 8 i, keys tx + TX j
     const int len = seq_len(a, b);
-    float4 o[8][2];
+    float4 o[8][F::NC];
     float m[8], l[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         m[i] = -INFINITY, l[i] = 0.f;
-        o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < F::NC; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     if (t0 < len) {
         const float sl2 = a.sm_scale * kLog2e;
@@ -219,7 +225,7 @@ window_fwd_simt_kernel(const WinArgs a) {
                 m[i] = mn;
                 l[i] *= al;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) o[i][c].x *= al, o[i][c].y *= al, o[i][c].z *= al, o[i][c].w *= al;
+                for (int c = 0; c < F::NC; ++c) o[i][c].x *= al, o[i][c].y *= al, o[i][c].z *= al, o[i][c].w *= al;
 #pragma unroll
                 for (int x = 0; x < KT; ++x) {
                     const float p = exp2f(s[i][x] - mz);
@@ -237,7 +243,7 @@ window_fwd_simt_kernel(const WinArgs a) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < F::NC; ++c) {
                         const float4 v = ld4(V + (n + k) * (D + 4) + 4 * tx + 4 * TX * c);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) axpy((&w[i].x)[k], v, o[i][c]);
@@ -258,7 +264,7 @@ window_fwd_simt_kernel(const WinArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) *reinterpret_cast<float4*>(K + (ty + 8 * i) * (D + 4) + 4 * tx + 4 * TX * c) = o[i][c];
+        for (int c = 0; c < F::NC; ++c) *reinterpret_cast<float4*>(K + (ty + 8 * i) * (D + 4) + 4 * tx + 4 * TX * c) = o[i][c];
         if (tx == 0) P[2 * (ty + 8 * i)] = m[i], P[2 * (ty + 8 * i) + 1] = l[i];
     }
     if (cs > 1) cluster.sync();
@@ -454,7 +460,9 @@ window_dq_simt_kernel(const WinArgs a) {
     // (a cluster shares a query tile as in the forward)
     const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int cs = cluster.num_blocks(), rank = cluster.block_rank();
-    const int t0 = blockIdx.x / cs * BT, hq = blockIdx.y, b = blockIdx.z, hk = hq / a.G;
+    // (the last tiles of all heads first: without a window they have the most keys)
+    const int x = blockIdx.x / cs, hq = x % a.Hq, b = x / a.Hq % a.B, hk = hq / a.G;
+    const int t0 = ((a.T + BT - 1) / BT - 1 - x / (a.Hq * a.B)) * BT;
     const int group = threadIdx.x / kHalf, tx = threadIdx.x & 15, ty = (threadIdx.x % kHalf) >> 4;
     const int len = seq_len(a, b);
     launch_dependents();
@@ -511,10 +519,12 @@ window_dkdv_simt_kernel(const WinArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr size_t N = tile_floats<D>();
     float *Q = sm, *dO = Q + N, *K = dO + N, *V = K + N, *P = V + N, *dS = P + BT * PP, *row = dS + BT * PP;
-    // item -> (tile, stretch): the tiles with sinks first
-    const int hk = blockIdx.y, b = blockIdx.z, nsc = a.nsink * a.sink_cuts;
-    const bool sink = (int)blockIdx.x < nsc;
-    const int cuts = sink ? a.sink_cuts : a.cuts, x0 = sink ? (int)blockIdx.x : (int)blockIdx.x - nsc;
+    // item -> (tile, stretch): the tiles with sinks first, of all heads, then the first tiles, which
+    // without a window have the longest lists
+    const int hk = blockIdx.x % a.Hkv, b = blockIdx.x / a.Hkv % a.B, item = blockIdx.x / (a.Hkv * a.B);
+    const int nsc = a.nsink * a.sink_cuts;
+    const bool sink = item < nsc;
+    const int cuts = sink ? a.sink_cuts : a.cuts, x0 = sink ? item : item - nsc;
     const int tile = (sink ? 0 : a.nsink) + x0 / cuts, cut = x0 % cuts, s0 = tile * BT;
     const int group = threadIdx.x / kHalf, tx = threadIdx.x & 15, ty = (threadIdx.x % kHalf) >> 4;
     const int len = seq_len(a, b);
@@ -559,7 +569,7 @@ window_dkdv_simt_kernel(const WinArgs a) {
             else if (s0 + r < a.T) st4(at<T>(group ? a.dk : a.dv, b, hk, s0 + r) + 4 * tx + 64 * c, o[i][c]);
         }
     }
-    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) wait_for_previous();
+    if (blockIdx.x == gridDim.x - 1) wait_for_previous();
 }
 
 // dk and dv of the tiles whose lists are in stretches: their parts in order
@@ -610,22 +620,25 @@ size_t part_bytes(const WinArgs& a, int D) {
     return (size_t)a.B * a.Hkv * first_slot(a, (a.T + BT - 1) / BT) * 2 * BT * D * sizeof(float);
 }
 
-// CTAs that share a query tile: as long as each has an SM (windows, whose tiles
-// are alike; with all keys the late tiles are the longest and three CTAs to an SM
-// even out) and a key tile.
+// CTAs that share a query tile: as long as each has an SM and a key tile.  With
+// all keys the late tiles are the longest: three CTAs to an SM even out (4000
+// tokens, 2 heads of 64: 137 us, 264 with one), if each has four key tiles of the
+// longest (1000 tokens, D = 128: 39 us, 54 with two).
 int cluster_of(const WinArgs& a) {
     const long long tiles = (a.T + BT - 1) / BT, ctas = tiles * a.Hq * a.B;
     const long long keys = (a.window + BT - 1) / BT + 1 + (a.sinks + BT - 1) / BT;
-    const long long most = 2 * (long long)a.window > a.T ? 444 : 148;
-    int cs = 1;
-    while (cs < 8 && 2 * cs * ctas <= most && 2 * cs <= keys && 2 * cs <= tiles) cs *= 2;
-    return cs;
+    const bool all = 2 * (long long)a.window > a.T;
+    for (int cs = 8; cs > 1; cs /= 2) {
+        const bool fits = cs * ctas <= 148 ? cs <= keys : all && cs * ctas <= 444 && 4 * cs <= keys;
+        if (fits && cs <= tiles) return cs;
+    }
+    return 1;
 }
 template <typename K>
 int launch_clusters(const char* what, K* kernel, const WinArgs& a, int threads, size_t smem, cudaStream_t s) {
     const int cs = cluster_of(a);
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)((a.T + BT - 1) / BT * cs), (unsigned)a.Hq, (unsigned)a.B);
+    c.gridDim = dim3((unsigned)((a.T + BT - 1) / BT) * cs * a.Hq * a.B);
     c.blockDim = dim3((unsigned)threads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
@@ -660,7 +673,7 @@ int bwd(const WinArgs& a, cudaStream_t s) {
     const unsigned nt = (unsigned)((a.T + BT - 1) / BT), Hkv = (unsigned)a.Hkv, B = (unsigned)a.B;
     const unsigned items = (unsigned)(a.nsink * a.sink_cuts + ((int)nt - a.nsink) * a.cuts);
     if (st == SSA_OK)
-        st = launch_beside("window_dkdv_simt_kernel", window_dkdv_simt_kernel<T, D>, dim3(items, Hkv, B), kThreads, smem_k,
+        st = launch_beside("window_dkdv_simt_kernel", window_dkdv_simt_kernel<T, D>, dim3(items * Hkv * B), kThreads, smem_k,
                            s, a);
     if (st == SSA_OK && (a.cuts > 1 || a.sink_cuts > 1))
         st = launch_beside("window_parts_kernel", window_parts_kernel<T, D>,
