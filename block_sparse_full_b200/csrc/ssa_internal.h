@@ -58,22 +58,31 @@ int opt_in_max_smem(const char* what, size_t* dyn_limit = nullptr) {
 
 // Launch that may begin while the kernel before it in the stream still runs; the
 // kernel itself waits (griddepcontrol.wait) before it touches that one's results.
+// cluster: CTAs of a cluster, along x.
 template <typename... Params, typename... Args>
-int launch_beside(const char* what, void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
-                  const Args&... args) {
+int launch_beside_clusters(const char* what, void (*kernel)(Params...), dim3 grid, unsigned cluster, unsigned threads,
+                           size_t smem, cudaStream_t s, const Args&... args) {
     cudaLaunchConfig_t c{};
     c.gridDim = grid;
     c.blockDim = dim3(threads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = &at;
-    c.numAttrs = 1;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
     if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     return check_launch(what);
+}
+template <typename... Params, typename... Args>
+int launch_beside(const char* what, void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                  const Args&... args) {
+    return launch_beside_clusters(what, kernel, grid, 1u, threads, smem, s, args...);
 }
 
 // Wall-clock limit of the kernels' bounded waits (default 2 s; tests shorten it).

@@ -47,6 +47,7 @@
 // Rows and keys behind a sequence's length may be NaN: weights are selected, not
 // multiplied, to zero, and such rows of a tile are cleared in shared memory
 // before they are an operand along the summed axis.
+#include <cooperative_groups.h>
 #include <cuda.h>
 
 #include "device_util.cuh"
@@ -78,6 +79,7 @@ struct BwdArgs {
     bool sweep;           // every query tile of dQ sweeps the keys for delta first
     int B, Hq, Hkv, G, T, Tp, window, sinks, nt;  // nt: tiles of 128
     int splits;           // stretches of queries past the reach of key tile 0
+    int cluster;          // CTAs that share a key tile's list
     float scale, scale_log2;
     unsigned long long timeout_ns;
 };
@@ -178,12 +180,13 @@ constexpr uint32_t K_SMEM = K_OFF_MISC + 16 + 1024;
 static_assert(K_SMEM <= kMaxSmemPerCta, "shared memory");
 constexpr uint32_t TK_S = 0, TK_DP = 128, TK_DK = 256, TK_DV = 384;
 
-template <int D>
+// kShared: a cluster of CTAs shares a key tile's list.
+template <int D, bool kShared>
 __global__ void __launch_bounds__(kThreadsK, 1)
 window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
-                   const BwdArgs a) {
+                   const View dk, const View dv, const BwdArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -196,7 +199,8 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     // ---- the key tile and the flattened list [i0, i1) of (query head of the group, query tile)
     const int BH = a.B * a.Hkv;
-    const int item = (int)(blockIdx.x / BH), bh = (int)(blockIdx.x % BH);  // early tiles first: the longest without a window
+    const int cs = kShared ? a.cluster : 1, rank = (int)blockIdx.x % cs, x0 = (int)blockIdx.x / cs;
+    const int item = x0 / BH, bh = x0 % BH;  // early tiles first: the longest without a window
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int J = item < a.nt ? item : 0;
     const int k0 = J * BM;
@@ -215,9 +219,15 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         i0 = (int)(n * sp / a.splits);
         i1 = (int)(n * (sp + 1) / a.splits);
     }
+    if constexpr (kShared) {  // the cluster's CTAs take a stretch each
+        const int all = i1 - i0;
+        i1 = i0 + (int)((long long)all * (rank + 1) / cs);
+        i0 += (int)((long long)all * rank / cs);
+    }
     const int n = i1 - i0;
     auto head_of = [&](int i) { return hk * a.G + (i0 + i) / q_count; };
     auto query_of = [&](int i) { return (q_first + (i0 + i) % q_count) * BM; };
+    const bool parts = a.splits > 0 && J == 0;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < KB_COUNT; ++i) mbar_init(BAR(i), i == KB_PREADY || i == KB_DSREADY ? kSoftmaxK : 1);
@@ -440,8 +450,22 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (ok) ok = wait(KB_DRAIN, 0);
         ok = bar_and(ok && !*abort_flag, 1, kSoftmaxK);
         fence_after_sync();
-        const bool parts = a.splits > 0 && J == 0;
-        if (ok && parts) {
+        if (kShared) {  // the shares, float32, over the tiles: [dK, dV][row][D], 16-byte pieces swizzled by row
+            if (ok) {
+#pragma unroll 1
+                for (int x = 0; x < D / 64; ++x) {
+                    const int w = part >> 1, col = (D / 2) * (part & 1) + 32 * x;
+                    uint32_t u[32];
+                    tmem_ld32(trow + (w ? TK_DV : TK_DK) + col, u);
+                    tmem_wait_ld();
+                    uint4* dst = reinterpret_cast<uint4*>(gbase) + (w * BM + r) * (D / 4);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[(col / 4 + e) ^ (r & 7)] = n > 0 ? make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3])
+                                                             : make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        } else if (ok && parts) {
             const int rows = item < a.nt ? BM : a.sinks;  // (far queries see the sinks alone)
             float* slot = a.part + part_offset(a, bh, item < a.nt ? 0 : 1 + item - a.nt, D);
 #pragma unroll 1
@@ -484,6 +508,33 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (warp == 1) {
         fence_after_sync();
         tmem_dealloc(tmem, 512);
+    }
+    if constexpr (kShared) {  // the shares are summed in the order of the ranks, the rows spread over the CTAs
+        __syncwarp();
+        const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        cluster.sync();
+        constexpr int kAll = 2 * BM * D / 4;
+        float* slot = a.part + part_offset(a, bh, item < a.nt ? 0 : 1 + item - a.nt, D);
+        const int rows = !parts ? min(BM, a.T - k0) : item < a.nt ? BM : a.sinks;
+        for (int e = rank * kAll / cs + (int)threadIdx.x; e < (rank + 1) * kAll / cs; e += kThreadsK) {
+            const int w = e / (BM * D / 4), r = e / (D / 4) % BM, c = e % (D / 4);
+            if (r >= rows) continue;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < cs; ++k) {
+                const float4 v = reinterpret_cast<const float4*>(cluster.map_shared_rank(gbase, k))[e - c + (c ^ (r & 7))];
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            }
+            if (parts) {
+                *reinterpret_cast<float4*>(slot + ((size_t)w * rows + r) * D + 4 * c) = s;
+            } else {
+                const View& o = w ? dv : dk;
+                const float m = w ? 1.f : a.scale;
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.data) + (size_t)b * o.sb + (size_t)hk * o.sh +
+                                          (size_t)(k0 + r) * o.st + 4 * c) =
+                    make_uint2(pack_bf16(s.x * m, s.y * m), pack_bf16(s.z * m, s.w * m));
+            }
+        }
+        cluster.sync();  // the shares stay until every CTA has read them
     }
 }
 
@@ -812,8 +863,9 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 }
 
 // Shape of a call: padded rows, reach and stretches of the first key tile.
+constexpr int kClusterCtas = 148;
 struct Plan {
-    int window, sinks, nt, Tp, splits;
+    int window, sinks, nt, Tp, splits, cluster;
     size_t rows, bytes;
 };
 Plan plan_of(const ssa_window_params_t& p) {
@@ -829,6 +881,12 @@ Plan plan_of(const ssa_window_params_t& p) {
         const long long n = (far + usual - 1) / usual;
         x.splits = (int)(n < 64 ? n : 64);
     }
+    // Few key tiles: clusters share their lists, as far as every CTA has an SM and two query tiles
+    // (8/1 heads of 128, 1000 tokens, all keys, both directions: 171 -> 66 us; 4096 tokens, window
+    // 1024: 246 -> 129 us).
+    const long long items = (long long)p.B * p.Hkv * (x.nt + x.splits), list = p.Hq / p.Hkv * (reach < last ? reach + 1 : last + 1);
+    x.cluster = 1;
+    while (x.cluster < 8 && 2 * x.cluster * items <= kClusterCtas && 4 * x.cluster <= list) x.cluster *= 2;
     x.rows = align_up((size_t)p.B * p.Hq * x.Tp * sizeof(float), 256);
     x.bytes = 2 * x.rows;
     if (x.splits)
@@ -839,7 +897,9 @@ Plan plan_of(const ssa_window_params_t& p) {
 template <int D>
 int run(const ssa_window_params_t& p, const View& q, const View& k, const View& v, const View& h, const float* lse,
         const View& dh, const View& dq, const View& dk, const View& dv, BwdArgs a, cudaStream_t s) {
-    int st = opt_in_max_smem<window_dkdv_kernel<D>>("window_dkdv_kernel");
+    const bool shared = a.cluster > 1;
+    int st = shared ? opt_in_max_smem<window_dkdv_kernel<D, true>>("window_dkdv_kernel")
+                    : opt_in_max_smem<window_dkdv_kernel<D, false>>("window_dkdv_kernel");
     if (st == SSA_OK) st = opt_in_max_smem<window_dq_kernel<D>>("window_dq_kernel");
     CUtensorMap k128, v128, mdk, mdv, q128, do128, k64, v64, k16, v16, mdq;
     struct { CUtensorMap* m; const View* x; int H, rows; } maps[] = {
@@ -860,8 +920,9 @@ int run(const ssa_window_params_t& p, const View& q, const View& k, const View& 
         st = launch_beside("window_dq_kernel", window_dq_kernel<D>, dim3((unsigned)p.B * p.Hq * a.nt), kThreads, Q_SMEM, s,
                            q128, do128, k64, v64, k16, v16, mdq, a);
     if (st == SSA_OK)
-        st = launch_beside("window_dkdv_kernel", window_dkdv_kernel<D>, dim3((unsigned)p.B * p.Hkv * (a.nt + a.splits)),
-                           kThreadsK, K_SMEM, s, q128, do128, k128, v128, mdk, mdv, a);
+        st = launch_beside_clusters("window_dkdv_kernel", shared ? window_dkdv_kernel<D, true> : window_dkdv_kernel<D, false>,
+                                    dim3((unsigned)p.B * p.Hkv * (a.nt + a.splits) * a.cluster), (unsigned)a.cluster,
+                                    kThreadsK, K_SMEM, s, q128, do128, k128, v128, mdk, mdv, dk, dv, a);
     if (st == SSA_OK && a.splits)
         st = launch_beside("window_sink_kernel", window_sink_kernel<D>,
                            dim3(2u * p.B * p.Hkv, (unsigned)(BM * D / 4 / 256)), 256, 0, s, dk, dv, a);
@@ -886,7 +947,7 @@ int launch_window_bwd_tc(const ssa_window_params_t& p, const View& q, const View
     a.ndelta = reinterpret_cast<float*>(static_cast<char*>(ws) + x.rows);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * x.rows);
     a.B = p.B, a.Hq = p.Hq, a.Hkv = p.Hkv, a.G = p.Hq / p.Hkv, a.T = p.T, a.Tp = x.Tp;
-    a.window = x.window, a.sinks = x.sinks, a.nt = x.nt, a.splits = x.splits;
+    a.window = x.window, a.sinks = x.sinks, a.nt = x.nt, a.splits = x.splits, a.cluster = x.cluster;
     a.sweep = x.window <= kSweepWindow;
     a.scale = p.sm_scale, a.scale_log2 = p.sm_scale * kLog2e;
     a.timeout_ns = wait_limit_ns();

@@ -73,6 +73,13 @@ SHAPES = [
     (1, 2, 1, 515, 64, 4096, 4),
     (2, 4, 2, 900, 128, 130, 80),  # the sinks' second tile is a 16-row step
     (1, 2, 1, 2500, 64, 40, 97),
+    # few key and query tiles with long lists (clusters share them), and many
+    (1, 8, 1, 700, 128, 0, 0),
+    (1, 8, 1, 1500, 128, 300, 4),
+    (2, 8, 2, 901, 64, 0, 0),
+    (1, 16, 1, 130, 128, 0, 0),
+    (1, 9, 3, 1100, 64, 700, 70),
+    (3, 12, 12, 1000, 64, 260, 4),
 ]
 
 
