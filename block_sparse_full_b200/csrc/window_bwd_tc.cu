@@ -516,22 +516,35 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         constexpr int kAll = 2 * BM * D / 4;
         float* slot = a.part + part_offset(a, bh, item < a.nt ? 0 : 1 + item - a.nt, D);
         const int rows = !parts ? min(BM, a.T - k0) : item < a.nt ? BM : a.sinks;
-        for (int e = rank * kAll / cs + (int)threadIdx.x; e < (rank + 1) * kAll / cs; e += kThreadsK) {
-            const int w = e / (BM * D / 4), r = e / (D / 4) % BM, c = e % (D / 4);
-            if (r >= rows) continue;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kBatch = 4;  // reads in flight
+        const int e1 = (rank + 1) * kAll / cs;
+        for (int e0 = rank * kAll / cs + (int)threadIdx.x; e0 < e1; e0 += kBatch * kThreadsK) {
+            float4 s[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int k = 0; k < cs; ++k) {
-                const float4 v = reinterpret_cast<const float4*>(cluster.map_shared_rank(gbase, k))[e - c + (c ^ (r & 7))];
-                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+                const float4* share = reinterpret_cast<const float4*>(cluster.map_shared_rank(gbase, k));
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int e = e0 + i * kThreadsK, r = e / (D / 4) % BM, c = e % (D / 4);
+                    if (e >= e1) continue;
+                    const float4 v = share[e - c + (c ^ (r & 7))];
+                    s[i].x += v.x, s[i].y += v.y, s[i].z += v.z, s[i].w += v.w;
+                }
             }
-            if (parts) {
-                *reinterpret_cast<float4*>(slot + ((size_t)w * rows + r) * D + 4 * c) = s;
-            } else {
-                const View& o = w ? dv : dk;
-                const float m = w ? 1.f : a.scale;
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.data) + (size_t)b * o.sb + (size_t)hk * o.sh +
-                                          (size_t)(k0 + r) * o.st + 4 * c) =
-                    make_uint2(pack_bf16(s.x * m, s.y * m), pack_bf16(s.z * m, s.w * m));
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int e = e0 + i * kThreadsK, w = e / (BM * D / 4), r = e / (D / 4) % BM, c = e % (D / 4);
+                if (e >= e1 || r >= rows) continue;
+                if (parts) {
+                    *reinterpret_cast<float4*>(slot + ((size_t)w * rows + r) * D + 4 * c) = s[i];
+                } else {
+                    const View& o = w ? dv : dk;
+                    const float m = w ? 1.f : a.scale;
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.data) + (size_t)b * o.sb + (size_t)hk * o.sh +
+                                              (size_t)(k0 + r) * o.st + 4 * c) =
+                        make_uint2(pack_bf16(s[i].x * m, s[i].y * m), pack_bf16(s[i].z * m, s[i].w * m));
+                }
             }
         }
         cluster.sync();  // the shares stay until every CTA has read them

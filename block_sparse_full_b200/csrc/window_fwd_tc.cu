@@ -40,6 +40,7 @@
 // Every mbarrier wait is bounded; on expiry the kernel records
 // SSA_ERR_TIMEOUT, the other roles stop, MMAs and copies in flight land, and
 // TMEM is released.
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -71,6 +72,7 @@ constexpr uint32_t OFF_MISC = OFF_BAR + B_COUNT * 8;  // [0] tmem base, [1] abor
 // round the base up, it is 1024-byte aligned by declaration (and checked)
 constexpr uint32_t SMEM_BYTES = OFF_MISC + 16;
 static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
+constexpr int kSharedCtas = 296, kSharedTiles = 4;  // CTAs of clusters at most, key tiles of each at least
 constexpr int kPrefixCtas = 296, kPrefixTiles = 2;  // CTAs of a pass over a prefix, at least so many key tiles each
 constexpr uint32_t TM_S = 0, TM_O = 128, kTmemCols = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -87,6 +89,8 @@ struct AttnArgs {
     int H;                // heads of the grid: query heads (window), key/value heads (prefix)
     int B, G, T, window, sinks;
     int ntq;              // query tiles of a sequence (window), row tiles of a head (prefix)
+    View h;               // window, where a cluster shares a query tile
+    int cluster;          // its CTAs
     int splits, page, n_pages, nb;  // prefix: CTAs per row tile, tokens of a page, batch entries of a row tile
     float scale_log2;
     unsigned long long timeout_ns;
@@ -101,8 +105,9 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
 
 // kPrefix: rows are (batch entry, query head of the group), keys the pages of
 // the prefix, all of them seen; the CTA takes one stretch of the key tiles and
-// writes a partial result.
-template <int D, bool kPrefix>
+// writes a partial result.  kShared: a cluster of CTAs shares a query tile, each
+// takes a stretch of its key tiles.
+template <int D, bool kPrefix, bool kShared>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k16,
@@ -125,6 +130,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     int b = 0, h, t0 = 0, len, I;  // I: query tile / row tile
     int ns = 0, w0, nt;            // tiles: ns sink tiles (0 to 2), then w0 .. w0 + nt - ns - 1
     int split = 0;
+    int j0 = 0;                    // first tile of a cluster's stretch
+    const int cs = kShared ? a.cluster : 1, rank = (int)blockIdx.x % cs;
     if constexpr (kPrefix) {
         split = (int)(blockIdx.x % a.splits);
         const int x = (int)(blockIdx.x / a.splits);
@@ -136,8 +143,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         nt = (int)((long long)n * (split + 1) / a.splits) - w0;
     } else {
         const int BH = a.B * a.H;
-        I = a.ntq - 1 - (int)(blockIdx.x / BH);  // late tiles first: without a window they are the longest
-        const int bh = (int)(blockIdx.x % BH);
+        const int x = (int)blockIdx.x / cs;
+        I = a.ntq - 1 - x / BH;  // late tiles first: without a window they are the longest
+        const int bh = x % BH;
         b = bh / a.H;
         h = bh % a.H;
         t0 = I * BM;
@@ -157,14 +165,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             ns = min((a.sinks + BN - 1) / BN, w0);  // tiles of sinks that every row's window has left behind
             nt = ns + (min(t0 + BM, len) - 1) / BN + 1 - w0;
         }
+        if constexpr (kShared) {  // tiles j0 .. of the list, counted from 0 again
+            const int all = nt;
+            j0 = all * rank / cs;
+            nt = all * (rank + 1) / cs - j0;
+            if (j0 >= ns) w0 += j0 - ns, ns = j0 = 0;
+            else ns = min(ns - j0, nt);
+        }
     }
     const int hk = kPrefix ? h : h / a.G;
     // bytes between the 64-column parts of a K or V row and between groups of eight
     // rows: a view's tile is two boxes of 64 rows, a page's rows come in one box
     constexpr uint32_t kCols = kPrefix ? 1024 : KV_BOX, kEight = kPrefix ? 16 * D : 1024;
-    auto tile_key = [&](int j) { return (j < ns ? j : w0 + j - ns) * BN; };
+    auto tile_key = [&](int j) { return (j < ns ? j0 + j : w0 + j - ns) * BN; };
     // keys that tile j loads and multiplies: of a sink tile whole steps of 16
-    auto tile_keys = [&](int j) { return j < ns ? min(BN, (a.sinks - j * BN + 15) & ~15) : BN; };
+    auto tile_keys = [&](int j) { return j < ns ? min(BN, (a.sinks - (j0 + j) * BN + 15) & ~15) : BN; };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < B_COUNT; ++i) mbar_init(BAR(i), i >= B_PREADY && i < B_DRAIN ? 128 : 1);
@@ -481,6 +496,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
                 if (row) *reinterpret_cast<float2*>(slot + BM * D + 2 * r) = make_float2(m2, l);
             }
+        } else if constexpr (kShared) {
+            // the share over the tiles, float32: [row][D], 16-byte pieces swizzled by row; then [row] (m, l)
+#pragma unroll 1
+            for (int c = 0; ok && c < D / 32; ++c) {
+                uint32_t u[32];
+                tmem_ld32(trow + TM_O + 32 * c, u);
+                tmem_wait_ld();
+                uint4* dst = reinterpret_cast<uint4*>(gbase) + r * (D / 4);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dst[(8 * c + e) ^ (r & 7)] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+            }
+            reinterpret_cast<float2*>(gbase + BM * D * 4)[r] = make_float2(m2, l);  // (no tile: -inf, 0)
         } else {
             const bool row = t < len;
             const float inv = row ? 1.f / l : 0.f;
@@ -524,15 +552,100 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
+    if constexpr (kShared) {  // the shares are joined in the order of the ranks, the rows spread over the CTAs
+        static_assert(BM * D * 4 + BM * 8 <= OFF_BAR, "shares");
+        __syncwarp();
+        const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        cluster.sync();
+        const int rows = BM / cs, r0 = rank * rows;  // this CTA's
+        float* weight = reinterpret_cast<float*>(gbase + OFF_V);  // [share][row], 1 / the sum among it
+        if ((int)threadIdx.x < rows) {
+            const int r = r0 + threadIdx.x, t = t0 + r;
+            float2 ml[8];
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                if (k < cs) ml[k] = reinterpret_cast<const float2*>(cluster.map_shared_rank(gbase, k) + BM * D * 4)[r];
+                M = fmaxf(M, ml[k].x);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                ml[k].x = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
+                L = fmaf(ml[k].x, ml[k].y, L);
+            }
+            const float inv = t < len ? 1.f / L : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < cs) weight[k * BM + r] = t < len ? ml[k].x * inv : 0.f;
+            if (t < a.T) a.lse[((size_t)b * a.H + h) * a.T + t] = t < len ? (M + log2f(L)) * kLn2 : -INFINITY;
+        }
+        __syncthreads();
+        constexpr int kBatch = 4;  // reads in flight
+        for (int e0 = threadIdx.x; e0 < rows * D / 4; e0 += kBatch * kThreads) {
+            float4 o[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < cs; ++k) {
+                const float4* share = reinterpret_cast<const float4*>(cluster.map_shared_rank(gbase, k));
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int e = e0 + i * kThreads, r = r0 + e / (D / 4), c = e % (D / 4);
+                    if (e >= rows * D / 4) continue;
+                    const float w = weight[k * BM + r];
+                    const float4 v = share[r * (D / 4) + (c ^ (r & 7))];
+                    if (w == 0.f) continue;  // (a share without a tile holds anything)
+                    o[i].x = fmaf(w, v.x, o[i].x), o[i].y = fmaf(w, v.y, o[i].y);
+                    o[i].z = fmaf(w, v.z, o[i].z), o[i].w = fmaf(w, v.w, o[i].w);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int e = e0 + i * kThreads, t = t0 + r0 + e / (D / 4), c = e % (D / 4);
+                if (e < rows * D / 4 && t < a.T)
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.h.data) + (size_t)b * a.h.sb +
+                                              (size_t)h * a.h.sh + (size_t)t * a.h.st + 4 * c) =
+                        make_uint2(pack_bf16(o[i].x, o[i].y), pack_bf16(o[i].z, o[i].w));
+            }
+        }
+        cluster.sync();  // the shares stay until every CTA has read them
+    }
 }
 
-template <int D, bool kPrefix>
+template <int D, bool kPrefix, bool kShared>
 int launch(const CUtensorMap (&m)[6], const AttnArgs& a, long long grid, cudaStream_t s) {
     const char* name = kPrefix ? "attn_tc_kernel<prefix>" : "attn_tc_kernel<window>";
-    const int st = opt_in_max_smem<attn_tc_kernel<D, kPrefix>>(name);
+    const int st = opt_in_max_smem<attn_tc_kernel<D, kPrefix, kShared>>(name);
     if (st != SSA_OK) return st;
-    attn_tc_kernel<D, kPrefix><<<(unsigned)grid, kThreads, SMEM_BYTES, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], a);
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = SMEM_BYTES;
+    c.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)a.cluster;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.attrs = &at;
+    c.numAttrs = kShared ? 1 : 0;
+    const cudaError_t e =
+        cudaLaunchKernelEx(&c, attn_tc_kernel<D, kPrefix, kShared>, m[0], m[1], m[2], m[3], m[4], m[5], a);
+    if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
     return check_launch(name);
+}
+
+// Few query tiles: clusters share their key tiles, as far as every CTA has an SM, or
+// half of one where all keys are seen and the late tiles are the longest, and four
+// tiles; lists of 16 tiles at least (one head of 128: 8192 tokens, all keys 98 -> 38
+// us; 4000 tokens, window 1024 19 -> 15; 512 tokens of 8 heads 11 us, 13 shared).
+int cluster_of(const AttnArgs& a) {
+    const long long ctas = (long long)a.B * a.H * a.ntq, all = (a.T + BN - 1) / BN;
+    const long long reach = ((long long)a.window + BM - 2) / BN + 1 + (a.sinks + BN - 1) / BN;
+    const long long list = reach < all ? reach : all;
+    const long long most = 2 * (long long)a.window > a.T ? kSharedCtas : kSharedCtas / 2;
+    int cs = 1;
+    while (cs < 8 && 2 * cs * ctas <= most && 2 * kSharedTiles * cs <= list) cs *= 2;
+    return list < 4 * kSharedTiles ? 1 : cs;
 }
 
 }  // namespace
@@ -591,7 +704,10 @@ int launch_window_fwd_tc(const ssa_window_params_t& p, const View& q, const View
     a.scale_log2 = p.sm_scale * 1.4426950408889634f;
     a.timeout_ns = wait_limit_ns();
     const long long grid = (long long)p.B * p.Hq * a.ntq;
-    return p.D == 64 ? launch<64, false>(m, a, grid, s) : launch<128, false>(m, a, grid, s);
+    a.h = h, a.cluster = cluster_of(a);
+    if (a.cluster > 1)
+        return p.D == 64 ? launch<64, false, true>(m, a, grid * a.cluster, s) : launch<128, false, true>(m, a, grid * a.cluster, s);
+    return p.D == 64 ? launch<64, false, false>(m, a, grid, s) : launch<128, false, false>(m, a, grid, s);
 }
 
 // One row tile reads the prefix once; up to 16 rows a head the kernel for single
@@ -639,7 +755,7 @@ int launch_prefix_tc(const ssa_cache_params_t& p, const View& q, const void* k_p
     a.timeout_ns = wait_limit_ns();
     const long long grid = (long long)p.Hkv * x.ntq * x.splits;
     if (grid > 0x7fffffffll) return fail(SSA_ERR_UNSUPPORTED, "prefix_decode: too many row tiles");
-    return p.D == 64 ? launch<64, true>(m, a, grid, s) : launch<128, true>(m, a, grid, s);
+    return p.D == 64 ? launch<64, true, false>(m, a, grid, s) : launch<128, true, false>(m, a, grid, s);
 }
 
 int attn_tc_take_status() {

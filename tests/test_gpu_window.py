@@ -80,6 +80,8 @@ SHAPES = [
     (1, 16, 1, 130, 128, 0, 0),
     (1, 9, 3, 1100, 64, 700, 70),
     (3, 12, 12, 1000, 64, 260, 4),
+    (1, 2, 1, 1500, 128, 0, 0),
+    (1, 2, 2, 2200, 64, 1300, 100),
 ]
 
 
@@ -96,6 +98,8 @@ def test_padded_batch(dtype, D):
     # lengths of 0, 1, a tile's end and the whole; NaN behind each of them
     _run(5, 4, 2, 300, D, dtype, 70, 4, lens=[0, 1, 128, 300, 257], seed=3)
     _run(3, 2, 1, 200, D, dtype, 0, 0, lens=[199, 64, 0], rows=True, seed=4)
+    _run(3, 2, 1, 1300, D, dtype, 0, 0, lens=[5, 1300, 700], seed=5)
+    _run(2, 4, 1, 1700, D, dtype, 1100, 90, lens=[1601, 0], rows=True, seed=6)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
