@@ -596,12 +596,17 @@ constexpr uint32_t TQ_S = 0, TQ_DP = 64, TQ_DQ = 128;
 constexpr int kSweepWindow = 128;  // windows up to so many keys, and
 constexpr int kSweepTokens = 512;  // the first tokens of a sequence
 
-template <int D>
+struct None {};
+// kShared: a cluster of CTAs shares a query tile, each takes a stretch of its key
+// tiles (a tile that is swept for delta, of few keys, is the first CTA's).  Out:
+// the view of dq then, None for the unshared kernel (with the view among its
+// arguments it measured 474 us, 440 without).
+template <int D, bool kShared, typename Out>
 __global__ void __launch_bounds__(kThreads, 2)
 window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
-                 const __grid_constant__ CUtensorMap tm_dq, const BwdArgs a) {
+                 const __grid_constant__ CUtensorMap tm_dq, const BwdArgs a, const Out dq) {
     extern __shared__ __align__(1024) uint8_t smem_q[];
     uint8_t* gbase = smem_q;
     const uint32_t base = smem_u32(smem_q);
@@ -616,7 +621,9 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     auto BAR = [&](int i) { return base + Q_OFF_BAR + 8u * (uint32_t)i; };
 
     const int BH = a.B * a.Hq;
-    const int I = a.nt - 1 - (int)(blockIdx.x / BH), bh = (int)(blockIdx.x % BH);
+    const int cs = kShared ? (int)(gridDim.x / (unsigned)(BH * a.nt)) : 1, rank = kShared ? (int)blockIdx.x % cs : 0;
+    const unsigned x0 = kShared ? blockIdx.x / cs : blockIdx.x;
+    const int I = a.nt - 1 - (int)(x0 / BH), bh = (int)(x0 % BH);
     const int b = bh / a.Hq, hq = bh % a.Hq, hk = hq / a.G;
     const int t0 = I * BM, len = seq_len(a, b);
     int ns = 0, w0 = 0, nt = 0;  // as in the forward: tiles of sinks alone, then those the window reaches
@@ -626,16 +633,28 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ns = min((a.sinks + BN - 1) / BN, w0);
         nt = ns + (min(t0 + BM, len) - 1) / BN + 1 - w0;
     }
+    int j0 = 0;  // first tile of a cluster's stretch
+    if constexpr (kShared) {
+        if (a.sweep || t0 < kSweepTokens) {
+            nt = rank > 0 ? 0 : nt;
+        } else {  // tiles j0 .. of the list, counted from 0 again
+            const int all = nt;
+            j0 = all * rank / cs;
+            nt = all * (rank + 1) / cs - j0;
+            if (j0 >= ns) w0 += j0 - ns, ns = j0 = 0;
+            else ns = min(ns - j0, nt);
+        }
+    }
     const int once = a.sweep || t0 < kSweepTokens ? nt : 0;  // tiles of the first sweep
     nt += once;
     auto tile_of = [&](int j) { return j >= once ? j - once : j; };
     auto tile_key = [&](int j) {
         const int x = tile_of(j);
-        return (x < ns ? x : w0 + x - ns) * BN;
+        return (x < ns ? (kShared ? j0 : 0) + x : w0 + x - ns) * BN;
     };
     auto tile_keys = [&](int j) {
         const int x = tile_of(j);
-        return x < ns ? min(BN, (a.sinks - x * BN + 15) & ~15) : BN;
+        return x < ns ? min(BN, (a.sinks - ((kShared ? j0 : 0) + x) * BN + 15) & ~15) : BN;
     };
 
     if (threadIdx.x == 0) {
@@ -851,20 +870,36 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (ok) ok = wait(QB_DRAIN, 0);
         if (!voted) ok = bar_and(ok && !*abort_flag, 1, kSoftmax);
         fence_after_sync();
-        if (ok) {
+        if constexpr (kShared) {  // the share over the tiles, float32: [row][D], 16-byte pieces swizzled by row
+#pragma unroll 1
+            for (int x = 0; ok && x < D / 64; ++x) {
+                const int col = (D / 2) * half + 32 * x;
+                uint32_t u[32];
+                tmem_ld32(trow + TQ_DQ + col, u);
+                tmem_wait_ld();
+                uint4* dst = reinterpret_cast<uint4*>(gbase) + r * (D / 4);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dst[(col / 4 + e) ^ (r & 7)] = nt > 0 && t < len
+                                                       ? make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3])
+                                                       : make_uint4(0u, 0u, 0u, 0u);
+            }
+        } else if (ok) {
 #pragma unroll 1
             for (int x = 0; x < D / 64; ++x) {  // the queries are used up
                 const int col = (D / 2) * half + 32 * x;
                 stage32(trow + TQ_DQ + col, a.scale, nt > 0 && t < len, gbase + Q_OFF_Q, col, r);
             }
         }
-        fence_async();
-        bar_sync(1, kSoftmax);
-        if (warp == 2 && lane == 0 && ok) {
+        if constexpr (!kShared) {
+            fence_async();
+            bar_sync(1, kSoftmax);
+            if (warp == 2 && lane == 0 && ok) {
 #pragma unroll
-            for (int x = 0; x < D / 64; ++x) tma_store_4d(&tm_dq, base + Q_OFF_Q + x * BOX_M, 64 * x, t0, hq, b);
-            bulk_commit_group();
-            bulk_wait_group_read0();
+                for (int x = 0; x < D / 64; ++x) tma_store_4d(&tm_dq, base + Q_OFF_Q + x * BOX_M, 64 * x, t0, hq, b);
+                bulk_commit_group();
+                bulk_wait_group_read0();
+            }
         }
     }
     fence_before_sync();
@@ -873,12 +908,45 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         fence_after_sync();
         tmem_dealloc(tmem, 256);
     }
+    if constexpr (kShared) {  // the shares are summed in the order of the ranks, the rows spread over the CTAs
+        static_assert(BM * D * 4 <= Q_OFF_BAR, "shares");
+        __syncwarp();
+        const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        cluster.sync();
+        constexpr int kAll = BM * D / 4, kBatch = 4;  // reads in flight
+        const int e1 = (rank + 1) * kAll / cs;
+        for (int e0 = rank * kAll / cs + (int)threadIdx.x; e0 < e1; e0 += kBatch * kThreads) {
+            float4 s[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < cs; ++k) {
+                const float4* share = reinterpret_cast<const float4*>(cluster.map_shared_rank(gbase, k));
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int e = e0 + i * kThreads, r = e / (D / 4), c = e % (D / 4);
+                    if (e >= e1) continue;
+                    const float4 v = share[e - c + (c ^ (r & 7))];
+                    s[i].x += v.x, s[i].y += v.y, s[i].z += v.z, s[i].w += v.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int e = e0 + i * kThreads, t = t0 + e / (D / 4), c = e % (D / 4);
+                if (e < e1 && t < a.T)
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(dq.data) + (size_t)b * dq.sb +
+                                              (size_t)hq * dq.sh + (size_t)t * dq.st + 4 * c) =
+                        make_uint2(pack_bf16(s[i].x * a.scale, s[i].y * a.scale),
+                                   pack_bf16(s[i].z * a.scale, s[i].w * a.scale));
+            }
+        }
+        cluster.sync();  // the shares stay until every CTA has read them
+    }
 }
 
 // Shape of a call: padded rows, reach and stretches of the first key tile.
 constexpr int kClusterCtas = 148;
 struct Plan {
-    int window, sinks, nt, Tp, splits, cluster;
+    int window, sinks, nt, Tp, splits, cluster, cluster_q;
     size_t rows, bytes;
 };
 Plan plan_of(const ssa_window_params_t& p) {
@@ -900,6 +968,13 @@ Plan plan_of(const ssa_window_params_t& p) {
     const long long items = (long long)p.B * p.Hkv * (x.nt + x.splits), list = p.Hq / p.Hkv * (reach < last ? reach + 1 : last + 1);
     x.cluster = 1;
     while (x.cluster < 8 && 2 * x.cluster * items <= kClusterCtas && 4 * x.cluster <= list) x.cluster *= 2;
+    // Few query tiles likewise, of 32 key tiles at least, as in the forward (one head of 128, 8192
+    // tokens, all keys, both directions: 280 -> 179 us).
+    const long long ctas = (long long)p.B * p.Hq * x.nt, most = 2 * (long long)x.window > p.T ? 2 * kClusterCtas : kClusterCtas;
+    long long keys = ((long long)x.window + BN - 2) / BN + 1 + (x.sinks + BN - 1) / BN;
+    keys = keys < 2 * x.nt ? keys : 2 * x.nt;
+    x.cluster_q = 1;
+    while (keys >= 32 && x.cluster_q < 8 && 2 * x.cluster_q * ctas <= most && 8 * x.cluster_q <= keys) x.cluster_q *= 2;
     x.rows = align_up((size_t)p.B * p.Hq * x.Tp * sizeof(float), 256);
     x.bytes = 2 * x.rows;
     if (x.splits)
@@ -909,11 +984,14 @@ Plan plan_of(const ssa_window_params_t& p) {
 
 template <int D>
 int run(const ssa_window_params_t& p, const View& q, const View& k, const View& v, const View& h, const float* lse,
-        const View& dh, const View& dq, const View& dk, const View& dv, BwdArgs a, cudaStream_t s) {
+        const View& dh, const View& dq, const View& dk, const View& dv, BwdArgs a, int cluster_q, cudaStream_t s) {
     const bool shared = a.cluster > 1;
     int st = shared ? opt_in_max_smem<window_dkdv_kernel<D, true>>("window_dkdv_kernel")
                     : opt_in_max_smem<window_dkdv_kernel<D, false>>("window_dkdv_kernel");
-    if (st == SSA_OK) st = opt_in_max_smem<window_dq_kernel<D>>("window_dq_kernel");
+    const bool shared_q = cluster_q > 1;
+    if (st == SSA_OK)
+        st = shared_q ? opt_in_max_smem<window_dq_kernel<D, true, View>>("window_dq_kernel")
+                      : opt_in_max_smem<window_dq_kernel<D, false, None>>("window_dq_kernel");
     CUtensorMap k128, v128, mdk, mdv, q128, do128, k64, v64, k16, v16, mdq;
     struct { CUtensorMap* m; const View* x; int H, rows; } maps[] = {
         {&k128, &k, p.Hkv, BM}, {&v128, &v, p.Hkv, BM},
@@ -930,8 +1008,11 @@ int run(const ssa_window_params_t& p, const View& q, const View& k, const View& 
         h, dh, lse, const_cast<float*>(a.nlse), const_cast<float*>(a.ndelta), a);
     st = check_launch("window_rows_kernel");
     if (st == SSA_OK)
-        st = launch_beside("window_dq_kernel", window_dq_kernel<D>, dim3((unsigned)p.B * p.Hq * a.nt), kThreads, Q_SMEM, s,
-                           q128, do128, k64, v64, k16, v16, mdq, a);
+        st = shared_q ? launch_beside_clusters("window_dq_kernel", window_dq_kernel<D, true, View>,
+                                               dim3((unsigned)p.B * p.Hq * a.nt * cluster_q), (unsigned)cluster_q,
+                                               kThreads, Q_SMEM, s, q128, do128, k64, v64, k16, v16, mdq, a, dq)
+                      : launch_beside("window_dq_kernel", window_dq_kernel<D, false, None>, dim3((unsigned)p.B * p.Hq * a.nt),
+                                      kThreads, Q_SMEM, s, q128, do128, k64, v64, k16, v16, mdq, a, None{});
     if (st == SSA_OK)
         st = launch_beside_clusters("window_dkdv_kernel", shared ? window_dkdv_kernel<D, true> : window_dkdv_kernel<D, false>,
                                     dim3((unsigned)p.B * p.Hkv * (a.nt + a.splits) * a.cluster), (unsigned)a.cluster,
@@ -964,8 +1045,8 @@ int launch_window_bwd_tc(const ssa_window_params_t& p, const View& q, const View
     a.sweep = x.window <= kSweepWindow;
     a.scale = p.sm_scale, a.scale_log2 = p.sm_scale * kLog2e;
     a.timeout_ns = wait_limit_ns();
-    return p.D == 64 ? run<64>(p, q, k, v, h, lse, dh, dq, dk, dv, a, s)
-                     : run<128>(p, q, k, v, h, lse, dh, dq, dk, dv, a, s);
+    return p.D == 64 ? run<64>(p, q, k, v, h, lse, dh, dq, dk, dv, a, x.cluster_q, s)
+                     : run<128>(p, q, k, v, h, lse, dh, dq, dk, dv, a, x.cluster_q, s);
 }
 
 int window_bwd_take_status() {
