@@ -870,11 +870,12 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc
 
 constexpr int kCtas = 296;  // two CTAs on each of 148 SMs
 // Row tiles of few keys are a cluster's each, if the GPU holds all clusters at once:
-// one launch, no partials in memory.  Eight CTAs a cluster with up to eight key tiles
+// one launch, no partials in memory.  Eight CTAs a cluster with up to four key tiles
 // each, or as many as keep the total at 256, then with up to 16 (at 288 CTAs in
-// clusters of eight not all are placed at once: 17 us instead of 11).  One sequence,
-// 16/4 heads of 128, window 1024: 8.6 us, 10.1 by the list of units; 32 sequences:
-// 17.8 and 22; one, window 8000 (16 tiles a CTA): 20.9 and 12.3, so left to the list.
+// clusters of eight not all are placed at once: 17 us instead of 11).  16/4 heads of
+// 128, window 1024: one sequence 8.6 us, 9.1 by the list of units (and a launch more
+// for the host); 32 sequences 17.8 and 21.8; 8, window 4000: 18.2 and 20.3; one,
+// window 3000 (6 tiles a CTA): 11.8 and 9.9, so left to the list.
 constexpr int kOneCtas = 256;  // CTAs of all clusters at most
 
 template <typename T, int D, int RG>
@@ -951,7 +952,7 @@ long long seen_most(const ssa_cache_params_t& p) {
 int cluster_of(const ssa_cache_params_t& p, int RT) {
     const long long tiles = (seen_most(p) + tile_keys(p) - 1) / tile_keys(p), rows = (long long)p.B * p.Hkv * RT;
     for (int cs = 8; cs > 1; cs /= 2)
-        if (rows * cs <= kOneCtas) return tiles <= cs * (rows * cs > kOneCtas / 2 ? 16 : 8) ? cs : 0;
+        if (rows * cs <= kOneCtas) return tiles <= cs * (rows * cs > kOneCtas / 2 ? 16 : 4) ? cs : 0;
     return 0;
 }
 
