@@ -228,6 +228,41 @@ def test_captured_and_on_another_stream(dtype):
         assert torch.equal(a, c)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_two_streams_at_once_with_shared_tiles(dtype):
+    # few tiles with long lists: clusters of CTAs share them; two calls in flight, eager and replayed
+    def make(seed):
+        q, k, v, dh = map(_dev, _make(1, 4, 1, 1700, 128, dtype, False, seed))
+        return ssa.window_params_for(q, k, 1300, 5), q, k, v, dh
+
+    def both(c):
+        p, q, k, v, dh = c
+        out = ssa.window_fwd(p, q, k, v)
+        return (out["h"], out["lse"]) + tuple(ssa.window_bwd(p, q, k, v, out, dh))
+
+    calls = [make(1), make(2)]
+    want = [both(c) for c in calls]
+    streams = [torch.cuda.Stream(DEV) for _ in calls]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(both(calls[i]))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = both(calls[0])
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    got[0].append(held)
+    ssa.device_status()
+    for w, runs in zip(want, got):
+        for r in runs:
+            assert all(torch.equal(x, y) for x, y in zip(w, r))
+
+
 def test_length_out_of_range_is_reported():
     q, k, v, _ = (x.to(DEV) for x in _make(2, 1, 1, 100, 64, "bf16"))
     p = ssa.window_params_for(q, k, 10, 0)
