@@ -15,7 +15,10 @@
 // (sequence, head, row tile) is split between CTAs; a second kernel joins the
 // partials of each row:  h = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 // Which CTAs hold a row's partials follows from the lengths alone, so nothing
-// is counted or cleared, and the order of the sums is fixed.
+// is counted or cleared, and the order of the sums is fixed.  Every share of a row
+// counts, also one whose maximum is -inf: its sum may be NaN (the maximum ignores
+// NaN scores), or 0 where every score is -inf, and then the row's output is NaN as
+// by the formula, however the row was split.
 //
 // Keys and values come in by 16-byte asynchronous copies through a ring of
 // shared-memory stages (3 x 32 KB per CTA and two CTAs per SM keep the
@@ -469,6 +472,7 @@ decode_kernel(const DecodeArgs a, const Pass p) {
 
     Cursor ld;
     long long ubeg, uend;
+    bool none = false;  // kOne: the sequence is empty
     if constexpr (kOne) {
         const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
         const int cs = cluster.num_blocks(), rank = cluster.block_rank(), x = (int)blockIdx.x / cs;
@@ -476,7 +480,11 @@ decode_kernel(const DecodeArgs a, const Pass p) {
         ld.s = seen_tiles(p, seq_len(p, ld.b), TK);
         ubeg = ld.s.nt * rank / cs, uend = ld.s.nt * (rank + 1) / cs;
         ld.u = ubeg, ld.t = (int)ubeg;
-        if (threadIdx.x < kRows) top[threadIdx.x] = -INFINITY;  // (a CTA without a tile)
+        none = ld.s.nt == 0;
+        if (ubeg == uend) {  // no tile: a share of zeros
+            for (int e = threadIdx.x; e < kRows * D; e += kThreads) sum[e] = 0.f;
+            if (threadIdx.x < kRows) top[threadIdx.x] = -INFINITY, lsum[threadIdx.x] = 0.f;
+        }
     } else {
         launch_dependents();  // every CTA is on its SM: the next kernel's may come in beside them
         const long long total = units_before(p, p.nseq, TK) * HR;
@@ -693,15 +701,14 @@ decode_kernel(const DecodeArgs a, const Pass p) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int k = 0; k < cs; ++k) {
                 const float m = cluster.map_shared_rank(top, k)[r];
-                if (m == -INFINITY) continue;
-                const float w = ex2f(m - M);
+                const float w = m == -INFINITY ? 0.f : ex2f(m - M);
                 const float4 y = reinterpret_cast<const float4*>(cluster.map_shared_rank(sum, k))[e];
                 L = fmaf(w, cluster.map_shared_rank(lsum, k)[r], L);
                 v.x = fmaf(w, y.x, v.x), v.y = fmaf(w, y.y, v.y), v.z = fmaf(w, y.z, v.z), v.w = fmaf(w, y.w, v.w);
             }
-            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const float inv = none ? 0.f : 1.f / L;
             put4(static_cast<T*>(a.h.data) + (size_t)b * a.h.sb + (size_t)head * a.h.sh + c, v, inv);
-            if (c == 0) a.lse[(size_t)b * a.Hq + head] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+            if (c == 0) a.lse[(size_t)b * a.Hq + head] = none ? -INFINITY : (M + log2f(L)) * kLn2;
         }
         cluster.sync();  // the shares stay until every CTA has read them
         return;
@@ -811,8 +818,8 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc
                 ml = *reinterpret_cast<const float2*>(part(i) + (i < n_own ? kRows * D + 2 * r : prows * D + 2 * pr));
             }
             const float up = fmaxf(M, warp_max(ml.x));
-            if (up == -INFINITY) continue;  // nothing was seen
-            const float al = ex2f(M - up), w = ex2f(ml.x - up);
+            const float al = M == up ? 1.f : ex2f(M - up);  // both may be -inf
+            const float w = ml.x == -INFINITY ? 0.f : ex2f(ml.x - up);
             M = up;
             L = L * al + warp_sum(w * ml.y);
 #pragma unroll
@@ -853,7 +860,8 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc
             }
         }
         if (!row || written || sub != 0) continue;
-        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const bool none = np == 0;  // no key at all
+        const float inv = none ? 0.f : 1.f / L;
         T* dst = static_cast<T*>(a.h.data) + (size_t)b * a.h.sb + (size_t)(h * a.G + g) * a.h.sh + E * lane;
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -864,7 +872,7 @@ join_kernel(const DecodeArgs a, const Pass p, const Pass pre, const PrefixTc ptc
             for (int e = 0; e < E; ++e) dst[e] = acc[e] * inv;
         }
         if (lane == 0)
-            a.lse[(size_t)b * a.Hq + h * a.G + g] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+            a.lse[(size_t)b * a.Hq + h * a.G + g] = none ? -INFINITY : (M + log2f(L)) * kLn2;
     }
 }
 

@@ -409,7 +409,8 @@ size_t ssa_cache_workspace_size(const ssa_cache_params_t* params, int prefix_len
  * iff s < lens[b] and (window == 0 or s >= lens[b] - window or s < sinks).
  * q and h are views [b, head] (stride_t not read), lse is float32 [B,Hq]; a
  * sequence of length 0 gets h = 0, lse = -inf.  Slots that are not seen are
- * not read.
+ * not read.  A row with a score of NaN or +inf, or with none above -inf, gets
+ * h = NaN, and its lse is not finite either; other rows are not affected by it.
  */
 int ssa_paged_decode(const ssa_cache_params_t* params, const ssa_view_t* q, const void* k_pages,
                      const void* v_pages, const int32_t* table, const int32_t* lens,
