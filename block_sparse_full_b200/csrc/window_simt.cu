@@ -282,7 +282,7 @@ window_fwd_simt_kernel(const WinArgs a) {
                     const float* own = sm + BT * (D + 4) + g * F::kFloats;
                     const float* base = k == rank ? own : cluster.map_shared_rank(own, k);
                     const float2 ml = *reinterpret_cast<const float2*>(base + 2 * BT * (D + 4) + 2 * r);
-                    if (ml.x == -INFINITY) continue;
+                    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing seen (a sum of NaN counts)
                     const float mn = fmaxf(mx, ml.x), w0 = exp2f(mx - mn), w1 = exp2f(ml.x - mn);
                     mx = mn;
                     L = fmaf(L, w0, w1 * ml.y);
