@@ -492,7 +492,10 @@ def attn_bwd(params, q, k, v, mask, fwd, dh_full=None, dh_sparse=None, w_sparsit
 
 
 def device_status(device=None):
-    check(ssa_device_status(_stream(device)), "ssa_device_status")
+    """Waits for torch's current stream of ``device`` (None: the current device) and raises
+    ``SsaError`` if a kernel on that device has recorded an error since the last call."""
+    with torch.cuda.device(device):  # the records are each device's own
+        check(ssa_device_status(_stream(device)), "ssa_device_status")
 
 
 # ------------------------------------------------------------ paged cache and window attention

@@ -432,7 +432,8 @@ int ssa_prefix_decode(const ssa_cache_params_t* params, const ssa_view_t* q, con
  * previous call recorded an expired wait (and clears the record),
  * SSA_ERR_INVALID_ARG if one recorded a page number, slot or length out of
  * range (and clears that record), else SSA_ERR_CUDA on a pending CUDA error,
- * else SSA_OK. */
+ * else SSA_OK.  The records are those of the current device, which must be the
+ * stream's. */
 int ssa_device_status(void* stream);
 
 /* Static text for a status code. */
