@@ -577,18 +577,30 @@ int ssa_device_status(void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "stream: %s", cudaGetErrorString(e));
-    int st = fwd_tc_take_status(s);
-    if (st == SSA_OK) st = bwd_tc_take_status(s);
-    if (st == SSA_OK) st = selftest_take_status();
-    if (st == SSA_OK) st = decode_take_status();
-    if (st == SSA_OK) st = select_take_status();
-    if (st == SSA_OK) st = attn_tc_take_status();
-    if (st == SSA_OK) st = window_bwd_take_status();
-    if (st == SSA_OK) st = append_take_status();
-    if (st == SSA_OK) st = paged_take_status();
-    if (st == SSA_OK) st = window_take_status();
-    if (st != SSA_OK) return st;
-    return check_launch("pending");
+    // Every record is read and cleared; the gravest is returned, with its message.
+    auto grave = [](int st) {
+        return st == SSA_ERR_TIMEOUT ? 3 : st == SSA_ERR_INVALID_ARG ? 2 : st != SSA_OK ? 1 : 0;
+    };
+    int worst = SSA_OK;
+    char message[sizeof g_last_error] = "";
+    auto take = [&](int st) {
+        if (grave(st) <= grave(worst)) return;
+        worst = st;
+        memcpy(message, g_last_error, sizeof message);
+    };
+    take(fwd_tc_take_status(s));
+    take(bwd_tc_take_status(s));
+    take(selftest_take_status());
+    take(decode_take_status());
+    take(select_take_status());
+    take(attn_tc_take_status());
+    take(window_bwd_take_status());
+    take(append_take_status());
+    take(paged_take_status());
+    take(window_take_status());
+    if (worst == SSA_OK) return check_launch("pending");
+    memcpy(g_last_error, message, sizeof message);
+    return worst;
 }
 
 const char* ssa_status_string(int status) {

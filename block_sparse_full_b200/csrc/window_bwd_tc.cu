@@ -1055,15 +1055,11 @@ int window_bwd_take_status() {
     if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&w, g_bwd_range, sizeof w);
     if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
     const unsigned int zero = 0;
-    if (v) {
-        cudaMemcpyToSymbol(g_bwd_status, &zero, sizeof zero);
-        return v & 1u ? fail(SSA_ERR_TIMEOUT, "window backward: a bounded mbarrier wait expired")
-                      : fail(SSA_ERR_CUDA, "window_dq_kernel: shared memory is not aligned");
-    }
-    if (w) {
-        cudaMemcpyToSymbol(g_bwd_range, &zero, sizeof zero);
-        return fail(SSA_ERR_INVALID_ARG, "window attention: a length was out of range");
-    }
+    if (v) cudaMemcpyToSymbol(g_bwd_status, &zero, sizeof zero);
+    if (w) cudaMemcpyToSymbol(g_bwd_range, &zero, sizeof zero);
+    if (v & 1u) return fail(SSA_ERR_TIMEOUT, "window backward: a bounded mbarrier wait expired");
+    if (w) return fail(SSA_ERR_INVALID_ARG, "window attention: a length was out of range");
+    if (v) return fail(SSA_ERR_CUDA, "window_dq_kernel: shared memory is not aligned");
     return SSA_OK;
 }
 

@@ -764,15 +764,11 @@ int attn_tc_take_status() {
     if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&w, g_attn_tc_range, sizeof w);
     if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
     const unsigned int zero = 0;
-    if (v) {
-        cudaMemcpyToSymbol(g_attn_tc_status, &zero, sizeof zero);
-        return v & 1u ? fail(SSA_ERR_TIMEOUT, "attn_tc_kernel: a bounded mbarrier wait expired")
-                      : fail(SSA_ERR_CUDA, "attn_tc_kernel: shared memory is not aligned");
-    }
-    if (w) {
-        cudaMemcpyToSymbol(g_attn_tc_range, &zero, sizeof zero);
-        return fail(SSA_ERR_INVALID_ARG, "attention: a %s was out of range", w & 2u ? "page number" : "length");
-    }
+    if (v) cudaMemcpyToSymbol(g_attn_tc_status, &zero, sizeof zero);
+    if (w) cudaMemcpyToSymbol(g_attn_tc_range, &zero, sizeof zero);
+    if (v & 1u) return fail(SSA_ERR_TIMEOUT, "attn_tc_kernel: a bounded mbarrier wait expired");
+    if (w) return fail(SSA_ERR_INVALID_ARG, "attention: a %s was out of range", w & 2u ? "page number" : "length");
+    if (v) return fail(SSA_ERR_CUDA, "attn_tc_kernel: shared memory is not aligned");
     return SSA_OK;
 }
 
