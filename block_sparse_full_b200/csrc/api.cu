@@ -525,6 +525,8 @@ static int prefix_shape(const ssa_cache_params_t* p, int prefix_len) {
     SSA_TRY(validate(p));
     if (prefix_len < 0) return fail(SSA_ERR_INVALID_ARG, "prefix_len must not be negative (got %d)", prefix_len);
     if (prefix_len > 0x7fffffff - 256) return fail(SSA_ERR_UNSUPPORTED, "prefix_len must be below 2^31 - 256");
+    if (prefix_len > 0 && p->window != 0)
+        return fail(SSA_ERR_UNSUPPORTED, "prefix_decode: window must be 0 (got %d)", p->window);
     return SSA_OK;
 }
 

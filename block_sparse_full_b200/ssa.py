@@ -604,12 +604,14 @@ class PagedCache:
     cache up to them, so that one captured decode step can be replayed.  The
     table gives every sequence pages of its own, in order; ``table`` may be
     overwritten with other page numbers.  ``prefix_pages`` (of the same pool) and
-    ``prefix_len`` put one shared prefix before every sequence."""
+    ``prefix_len`` put one shared prefix before every sequence (without a window)."""
 
     def __init__(self, B, Hq, Hkv, D, capacity, dtype, device, page=64, window=0, sinks=0, sm_scale=None,
                  inv_freq=None, interleaved=False, prefix_len=0):
         width, shared = max(1, -(-capacity // page)), -(-prefix_len // page)
         self.params = cache_params(B, Hq, Hkv, D, page, B * width + shared, width, dtype, window, sinks, sm_scale)
+        if ssa_cache_workspace_size(self.params, prefix_len) == ctypes.c_size_t(-1).value:
+            raise SsaError("ssa_cache_workspace_size", SSA_ERR_INVALID_ARG, ssa_last_error())
         shape = (B * width + shared, Hkv, page, D)
         self.k_pages = torch.zeros(shape, dtype=dtype, device=device)
         self.v_pages = torch.zeros_like(self.k_pages)
@@ -618,8 +620,6 @@ class PagedCache:
         self.prefix_len = prefix_len
         self.prefix_pages = B * width + torch.arange(shared, dtype=torch.int32, device=device)
         self.inv_freq, self.interleaved = inv_freq, interleaved
-        if ssa_cache_workspace_size(self.params, prefix_len) == ctypes.c_size_t(-1).value:
-            raise SsaError("ssa_cache_workspace_size", SSA_ERR_INVALID_ARG, ssa_last_error())
 
     def append(self, k, v, q=None, q_start=None, q_out=None, k_out=None):
         """Appends new tokens (see ``cache_append``) -> the rotated queries."""

@@ -400,7 +400,8 @@ int ssa_cache_append(const ssa_cache_params_t* params, int n_tokens, const ssa_v
                      void* stream);
 
 /* Bytes of scratch for ssa_paged_decode (prefix_len = 0) or ssa_prefix_decode
- * ((size_t)-1 on invalid arguments).  Nothing in it needs clearing. */
+ * ((size_t)-1 on invalid arguments, a window behind a prefix among them).
+ * Nothing in it needs clearing. */
 size_t ssa_cache_workspace_size(const ssa_cache_params_t* params, int prefix_len);
 
 /*
