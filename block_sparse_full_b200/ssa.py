@@ -630,6 +630,9 @@ class PagedCache:
         """Writes the shared prefix's keys and values [prefix_len, Hkv, D], rotated to 0, 1, ..."""
         if not self.prefix_len:
             raise ValueError("this cache has no shared prefix")
+        for name, x in (("k", k), ("v", v)):
+            if x.shape[:1] != (self.prefix_len,):
+                raise ValueError(f"{name} must hold the prefix's {self.prefix_len} tokens, got shape {tuple(x.shape)}")
         p, dev = self.params, self.k_pages.device
         one = cache_params(1, p.Hq, p.Hkv, p.D, p.page, p.n_pages, max(1, self.prefix_pages.numel()), p.dtype)
         cache_append(one, self.k_pages, self.v_pages, self.prefix_pages.view(1, -1),
