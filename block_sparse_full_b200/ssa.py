@@ -16,7 +16,8 @@ decode loop, in ``csrc/marshal.cpp``):
   raise ``SsaError`` on a non-zero status.
 
 Every compute step runs in the library's CUDA kernels.  There is no fallback:
-importing this module without a built ``libssa.so`` raises.
+importing this module without a built ``libssa.so`` raises, and so does the
+first call that needs ``_marshal.so`` without that.
 """
 from __future__ import annotations
 
@@ -147,7 +148,24 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
-from . import _marshal  # noqa: E402  (tensor checks and calls of the paged cache and window attention; needs libssa)
+
+
+class _Marshal:
+    """Stands for the module _marshal (tensor checks and calls of the paged cache and window
+    attention) until its first use: the other calls do without it."""
+
+    def __getattr__(self, name):
+        global _marshal
+        try:
+            from . import _marshal as module
+        except ImportError as e:
+            raise ImportError(f"the paged cache and window attention need _marshal.so, built for this torch and Python "
+                              f"with `python -m block_sparse_full_b200.build` ({e})") from e
+        _marshal = module
+        return getattr(module, name)
+
+
+_marshal = _Marshal()
 
 
 def lib() -> ctypes.CDLL:
