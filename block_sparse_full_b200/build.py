@@ -4,13 +4,15 @@ _marshal.so (argument marshalling for Python, against torch's headers) with g++.
 Compiles every ``csrc/*.cu`` to an object under ``_build/`` (in parallel) and
 links them into ``block_sparse_full_b200/libssa.so``; ``csrc/marshal.cpp``
 becomes ``block_sparse_full_b200/_marshal.so``.  They are rebuilt only when a
-source or a header is newer.  Run as ``python -m
-block_sparse_full_b200.build``.
+source or a header is newer, ``_marshal.so`` also when torch or Python is
+another.  Run as ``python -m block_sparse_full_b200.build``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -59,10 +61,19 @@ def _compile(src: str, obj: str, extra, verbose: bool):
     return r.stderr
 
 
+def _built_for() -> str:
+    """The Python and the torch that _marshal.so is compiled against."""
+    torch = importlib.util.find_spec("torch")
+    return f"{sys.implementation.cache_tag} torch {importlib.metadata.version('torch')} {torch.origin}"
+
+
 def _build_marshal(verbose: bool, force: bool):
     src = os.path.join(CSRC, "marshal.cpp")
-    if not force and not _stale(MARSHAL, [src, os.path.join(INCLUDE, "ssa.h")]):
-        return
+    stamp, key = os.path.join(BUILD, "marshal.txt"), _built_for()
+    if not force and not _stale(MARSHAL, [src, os.path.join(INCLUDE, "ssa.h")]) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == key:
+                return
     import torch  # only its location and ABI
 
     t = os.path.dirname(torch.__file__)
@@ -77,6 +88,8 @@ def _build_marshal(verbose: bool, force: bool):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for marshal.cpp:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(key)
 
 
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) -> str:
