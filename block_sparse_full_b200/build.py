@@ -61,15 +61,18 @@ def _compile(src: str, obj: str, extra, verbose: bool):
     return r.stderr
 
 
-def _built_for() -> str:
+def _built_for(torch) -> str:
     """The Python and the torch that _marshal.so is compiled against."""
-    torch = importlib.util.find_spec("torch")
     return f"{sys.implementation.cache_tag} torch {importlib.metadata.version('torch')} {torch.origin}"
 
 
 def _build_marshal(verbose: bool, force: bool):
+    spec = importlib.util.find_spec("torch")
+    if spec is None:  # the library stands without it
+        print("torch is not installed: _marshal.so is left out", flush=True)
+        return
     src = os.path.join(CSRC, "marshal.cpp")
-    stamp, key = os.path.join(BUILD, "marshal.txt"), _built_for()
+    stamp, key = os.path.join(BUILD, "marshal.txt"), _built_for(spec)
     if not force and not _stale(MARSHAL, [src, os.path.join(INCLUDE, "ssa.h")]) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read() == key:

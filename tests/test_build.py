@@ -59,3 +59,11 @@ def test_a_failed_compilation_is_tried_again(compiled, monkeypatch):
     monkeypatch.setattr(subprocess, "run", good)
     b._build_marshal(False, False)
     assert len(compiled) == 1 and os.path.exists(b.MARSHAL)
+
+
+def test_the_library_is_built_without_torch(compiled, monkeypatch, capsys):
+    # libssa.so is for C programs too: nothing but its own binding needs torch
+    find = b.importlib.util.find_spec
+    monkeypatch.setattr(b.importlib.util, "find_spec", lambda n, *a: None if n == "torch" else find(n, *a))
+    b._build_marshal(False, False)
+    assert not compiled and "torch" in capsys.readouterr().out
