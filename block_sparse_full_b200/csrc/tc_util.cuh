@@ -456,30 +456,5 @@ __device__ __forceinline__ f32x2 exp2_poly2(f32x2 x) {
     return mk2(p0, p1);
 }
 
-// The same with a degree-4 polynomial (fitted here in the same way; measured
-// max relative error 2.7e-6 in float32 Horner form), where the sum of the
-// weights is an output of its own.
-__device__ __forceinline__ f32x2 exp2_poly4_2(f32x2 x) {
-    constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
-    constexpr float C0 = 0.9999992847442627f, C1 = 0.6931217908859253f, C2 = 0.240247443318367f;
-    constexpr float C3 = 0.05591785907745361f, C4 = 0.009570102207362652f;
-    float x0, x1;
-    un2(x, x0, x1);
-    x = mk2(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
-    const f32x2 t = add2(x, mk2(kShift, kShift));
-    const f32x2 j = add2(t, mk2(-kShift, -kShift));
-    const f32x2 r = fma2(j, mk2(-1.f, -1.f), x);
-    f32x2 p = fma2(mk2(C4, C4), r, mk2(C3, C3));
-    p = fma2(p, r, mk2(C2, C2));
-    p = fma2(p, r, mk2(C1, C1));
-    p = fma2(p, r, mk2(C0, C0));
-    float p0, p1, t0, t1;
-    un2(p, p0, p1);
-    un2(t, t0, t1);
-    p0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
-    p1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
-    return mk2(p0, p1);
-}
-
 }  // namespace tc
 }  // namespace ssa
