@@ -87,6 +87,10 @@ int launch_beside(const char* what, void (*kernel)(Params...), dim3 grid, unsign
 
 // Wall-clock limit of the kernels' bounded waits (default 2 s; tests shorten it).
 unsigned long long wait_limit_ns();
+// Under this limit the window and prefix kernels on the tensor cores set up the
+// barrier of the scores with one arrival more than it gets, so that the waits for
+// them do run out (ssa_debug_set_wait_limit_ns).
+constexpr unsigned long long kLostScoresNs = 1;
 
 // Byte budget of the tensor-core backward's dS workspace (default 4 GiB;
 // tests shrink it so that small problems run in several head groups).

@@ -68,7 +68,7 @@ constexpr uint32_t BOX_M = BM * 128, BOX_N = BN * 128;  // boxes of 64 columns
 constexpr uint32_t TILE_M = 2 * BOX_M, TILE_N = 2 * BOX_N;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ unsigned int g_bwd_status;  // bit 0: a wait expired
+__device__ unsigned int g_bwd_status[2];  // dQ, dK/dV: bit 0: a wait expired, bit 1: misaligned shared memory
 __device__ unsigned int g_bwd_range;   // a length was out of range
 
 struct BwdArgs {
@@ -192,7 +192,7 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + K_OFF_MISC + 4);
-    unsigned int* status = &g_bwd_status;
+    unsigned int* status = &g_bwd_status[1];
     const uint64_t lim = a.timeout_ns;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto BAR = [&](int i) { return base + K_OFF_BAR + 8u * (uint32_t)i; };
@@ -230,7 +230,8 @@ window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const bool parts = a.splits > 0 && J == 0;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < KB_COUNT; ++i) mbar_init(BAR(i), i == KB_PREADY || i == KB_DSREADY ? kSoftmaxK : 1);
+        for (int i = 0; i < KB_COUNT; ++i)
+            mbar_init(BAR(i), i == KB_PREADY || i == KB_DSREADY ? kSoftmaxK : i == KB_SREADY && lim == kLostScoresNs ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -611,11 +612,11 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint8_t* gbase = smem_q;
     const uint32_t base = smem_u32(smem_q);
     if (base & 1023u) {  // not reached: the tiles' swizzle needs the alignment
-        if (threadIdx.x == 0) atomicOr(&g_bwd_status, 2u);
+        if (threadIdx.x == 0) atomicOr(&g_bwd_status[0], 2u);
         return;
     }
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + Q_OFF_MISC + 4);
-    unsigned int* status = &g_bwd_status;
+    unsigned int* status = &g_bwd_status[0];
     const uint64_t lim = a.timeout_ns;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto BAR = [&](int i) { return base + Q_OFF_BAR + 8u * (uint32_t)i; };
@@ -658,7 +659,8 @@ window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < QB_COUNT; ++i) mbar_init(BAR(i), i == QB_DSREADY || i == QB_SFREE ? kSoftmax : 1);
+        for (int i = 0; i < QB_COUNT; ++i)
+            mbar_init(BAR(i), i == QB_DSREADY || i == QB_SFREE ? kSoftmax : i == QB_SREADY && lim == kLostScoresNs ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -1050,16 +1052,18 @@ int launch_window_bwd_tc(const ssa_window_params_t& p, const View& q, const View
 }
 
 int window_bwd_take_status() {
-    unsigned int v = 0, w = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_bwd_status, sizeof v);
+    unsigned int v[2] = {0, 0}, w = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(v, g_bwd_status, sizeof v);
     if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&w, g_bwd_range, sizeof w);
     if (e != cudaSuccess) return fail(SSA_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
-    const unsigned int zero = 0;
-    if (v) cudaMemcpyToSymbol(g_bwd_status, &zero, sizeof zero);
-    if (w) cudaMemcpyToSymbol(g_bwd_range, &zero, sizeof zero);
-    if (v & 1u) return fail(SSA_ERR_TIMEOUT, "window backward: a bounded mbarrier wait expired");
+    const unsigned int zero[2] = {0, 0};
+    if (v[0] | v[1]) cudaMemcpyToSymbol(g_bwd_status, zero, sizeof zero);
+    if (w) cudaMemcpyToSymbol(g_bwd_range, zero, sizeof w);
+    if ((v[0] | v[1]) & 1u)
+        return fail(SSA_ERR_TIMEOUT, "%s%s%s: a bounded mbarrier wait expired", v[0] & 1u ? "window_dq_kernel" : "",
+                    v[0] & v[1] & 1u ? " and " : "", v[1] & 1u ? "window_dkdv_kernel" : "");
     if (w) return fail(SSA_ERR_INVALID_ARG, "window attention: a length was out of range");
-    if (v) return fail(SSA_ERR_CUDA, "window_dq_kernel: shared memory is not aligned");
+    if (v[0]) return fail(SSA_ERR_CUDA, "window_dq_kernel: shared memory is not aligned");
     return SSA_OK;
 }
 

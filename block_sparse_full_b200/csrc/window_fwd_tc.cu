@@ -182,7 +182,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     auto tile_keys = [&](int j) { return j < ns ? min(BN, (a.sinks - (j0 + j) * BN + 15) & ~15) : BN; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(BAR(i), i >= B_PREADY && i < B_DRAIN ? 128 : 1);
+        for (int i = 0; i < B_COUNT; ++i)
+            mbar_init(BAR(i), i >= B_PREADY && i < B_DRAIN ? 128 : i == B_SREADY && lim == kLostScoresNs ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }

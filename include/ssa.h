@@ -472,6 +472,9 @@ int ssa_selftest_wait_timeout(unsigned long long limit_ns, int* gave_up, void* s
  * default of 2 s).  A wait that runs past it makes the kernel stop, let
  * copies and MMAs in flight land, free TMEM and return; ssa_device_status
  * then reports SSA_ERR_TIMEOUT and the outputs of that call are undefined.
+ * With a limit of 1 the tensor-core kernels of ssa_window_fwd, ssa_window_bwd
+ * and ssa_prefix_decode do not learn that their first scores are there, so that
+ * their waits run out in every call with a token to attend to.
  * Process-wide; not synchronised with calls running on other threads. */
 void ssa_debug_set_wait_limit_ns(unsigned long long ns);
 
