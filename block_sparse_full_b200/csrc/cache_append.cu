@@ -6,7 +6,10 @@
 // The angle is formed in float64 and reduced to half turns there, because a
 // float32 product p * f_i is off by p * 2^-24 radians (0.004 at p = 65536);
 // the reduced angle, the sines and the products are float32 and each output
-// element is rounded once.
+// element is rounded once.  (The reduced angle, at most pi, is rounded by at most
+// 2^-24 of itself: float32 outputs are off by a relative 3.7e-8 root mean square
+// against 64 bits, 2.9e-8 with sines of the unrounded angle, which would cost the
+// float64 units' latency in a call that is one chain of latencies.)
 //
 // The call only moves data: a token's rows are read and written once.  One CTA
 // per token: its rotary angles are computed once, by one thread per pair, and
@@ -224,8 +227,13 @@ void launch(const AppendArgs& a, bool inter, unsigned grid, cudaStream_t s) {
 // Tokens up to which a CTA has 256 threads and not 128: few tokens leave SMs
 // idle, and the wider CTA is done sooner (8 tokens of 16/4 heads of 128, bf16: 3.3 us
 // against 3.7); many are held up by the barrier behind the look-ups, which
-// couples fewer warps in a small CTA (1000 tokens of 32/8 heads 9.0 against 7.2 us,
-// 16384 tokens 91 against 74 us, 81 % of the measured copy bandwidth).
+// couples fewer warps in a small CTA (16384 tokens of 32/8 heads 91 against 74 us,
+// 81 % of the measured copy bandwidth).  256 against 128 threads, us, SM clock 1965 MHz:
+//     tokens           64    256    512    768   1024   2048
+//     32/8 heads      4.1    4.8    5.6    6.7    9.0   14.4
+//                     4.8    5.3    6.2    6.9    7.1   13.7
+//     8/2 heads       3.5    3.7    3.8           5.9
+//                     3.5    3.7    3.8           4.2
 constexpr int kFewTokens = 512;
 
 }  // namespace

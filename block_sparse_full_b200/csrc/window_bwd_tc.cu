@@ -44,6 +44,11 @@
 // formed as soon as the softmax has read the last, and the exponentials do not
 // wait for dP (573 us -> 436 us at the same shape).
 //
+// P and dS are rounded to bf16, each value by at most 2^-8 of itself, because they
+// are operands of products with the bf16 rows of Q, K and dO; sums, the row values and
+// dS before that rounding are float32.  Against 64 bits dq, dk and dv are off by a
+// relative 0.0024 (root mean square), where their own rounding alone is 0.0016.
+//
 // Rows and keys behind a sequence's length may be NaN: weights are selected, not
 // multiplied, to zero, and such rows of a tile are cleared in shared memory
 // before they are an operand along the summed axis.

@@ -30,6 +30,11 @@
 // polynomial on the FMA pipe for a part of them measured slower at every share
 // from an eighth to a half (the softmax is bound by latency and issue slots).
 //
+// P is rounded to bf16 because both operands of a product have one 16-bit type and V
+// is bf16; each weight is then off by at most 2^-8 of itself, independently of the
+// others.  l takes the weights before that rounding, in float32.  Against 64 bits h
+// is off by a relative 0.0024 (root mean square), where its own rounding alone is 0.0016.
+//
 // Sinks that the window has left behind are a key tile of their own, of
 // 16-row steps: loads, products and weights cover ceil(sinks / 16) steps only.
 //

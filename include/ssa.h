@@ -289,6 +289,7 @@ int ssa_attn_bwd(const ssa_params_t* params, const void* q, const void* k,
  * count elements.  data and every stride are multiples of 16 bytes, and the
  * strides of axes longer than 1 are at least D (no broadcast axes).
  * Where a call has no batch or no token axis that stride is not read.
+ * Outputs must not overlap inputs or one another, but where a call says so.
  * Lengths, tables, lse and inv_freq need the alignment of their own type only.
  */
 typedef struct {
@@ -421,8 +422,10 @@ int ssa_paged_decode(const ssa_cache_params_t* params, const ssa_view_t* q, cons
  * The same for a batch whose sequences all begin with the same prefix of
  * prefix_len tokens (>= 0), held once in pages prefix_pages (int32, device,
  * ceil(prefix_len / page) entries; NULL when prefix_len is 0): every query sees the whole prefix and the
- * lens[b] tokens of its own pages.  The prefix is read once for the batch,
- * not once per sequence.  params->window must be 0.
+ * lens[b] tokens of its own pages.  The prefix is read once for every 128 rows
+ * of a key/value head (rows: sequences times Hq / Hkv; bf16 with more than 16 rows
+ * and Hq / Hkv <= 128) or for every 16 (else), not once per sequence.
+ * params->window must be 0.
  */
 int ssa_prefix_decode(const ssa_cache_params_t* params, const ssa_view_t* q, const void* k_pages,
                       const void* v_pages, const int32_t* prefix_pages, int prefix_len,
